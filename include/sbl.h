@@ -173,6 +173,55 @@ sbl_status sbl_quant_act(const uint16_t* x_bf16, int64_t T, int64_t K,
 sbl_status sbl_rmsnorm_quant_act(const uint16_t* x_bf16, const float* g, float eps, int64_t T, int64_t K,
                                  int8_t* x_q, float* s_tok, void* stream);
 
+/* Kinds of sbl_norm. */
+enum { SBL_NORM_RMS = 0, SBL_NORM_LAYER = 1 };
+
+/*
+ * sbl_norm — RMS norm or layer norm of every row, on its own (the RMSNorm in
+ * front of the layer, Sparse-BitNet Guide, "Mathematical Formulation of
+ * Sparse-BitLinear", for callers that need the normalised activations
+ * themselves or train through them; sbl_rmsnorm_quant_act is the form fused
+ * with the quantiser).
+ *   xhat = (x - mean) * rstd, rstd = 1 / sqrt(mean_k((x - mean)^2) + eps),
+ *   y = xhat * weight + bias; mean = mean_k(x) for SBL_NORM_LAYER and 0 for
+ *   SBL_NORM_RMS.  Sums, mean, rstd and y in fp32 (two passes for the
+ *   variance), y rounded once.
+ *
+ *   x, y     [T, K], both fp32 (dtype SBL_F32) or both bf16 (SBL_BF16); y must
+ *            not overlap x.
+ *   weight   fp32 [K]; bias fp32 [K] or NULL.
+ *   eps      finite, >= 0.
+ *   mean     fp32 [T] (output) or NULL; rstd fp32 [T] (output) or NULL: the
+ *            statistics sbl_norm_backward reads (mean is not written for
+ *            SBL_NORM_RMS).
+ * NaN and Inf in a row pass to that row's outputs.  Asynchronous on `stream`;
+ * no workspace.
+ */
+sbl_status sbl_norm(const void* x, int dtype, int64_t T, int64_t K, int kind, const float* weight, const float* bias,
+                    float eps, void* y, float* mean, float* rstd, void* stream);
+
+/*
+ * sbl_norm_backward — the gradients of sbl_norm.
+ *   With q = dy * weight: dx = rstd * (q - mean_k(q) - xhat * mean_k(q * xhat))
+ *   (without mean_k(q) for SBL_NORM_RMS), dweight = sum_t dy * xhat,
+ *   dbias = sum_t dy.
+ *
+ *   dy, x, dx   [T, K] in one type (dtype); dx (output) may be NULL and must not
+ *               overlap dy or x.
+ *   mean, rstd  fp32 [T] as sbl_norm wrote them (mean is not read for SBL_NORM_RMS).
+ *   dweight, dbias  fp32 [K] (outputs), each may be NULL; overwritten, zeros for
+ *               T == 0.  The sums run in a fixed order: the same inputs give
+ *               the same bits.
+ *   workspace   sbl_norm_backward_workspace_bytes(T, K, dtype) bytes, 256-byte
+ *               aligned, when dweight or dbias is given (else SBL_ERR_WORKSPACE);
+ *               calls that share it must be ordered on one stream.
+ * At least one output.  Asynchronous on `stream`.
+ */
+size_t sbl_norm_backward_workspace_bytes(int64_t T, int64_t K, int dtype);
+sbl_status sbl_norm_backward(const void* dy, const void* x, int dtype, int64_t T, int64_t K, int kind,
+                             const float* weight, const float* mean, const float* rstd, void* dx, float* dweight,
+                             float* dbias, void* workspace, size_t workspace_bytes, void* stream);
+
 /*
  * sbl_mask_monitor — mask change rate and mask verification.
  *

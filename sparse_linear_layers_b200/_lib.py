@@ -25,6 +25,9 @@ SBL_PREP_SCALE_GLOBAL = 2
 
 SBL_BWD_DW_TERNARY = 1
 
+SBL_NORM_RMS = 0
+SBL_NORM_LAYER = 1
+
 SBL_MAX_GROUP = 8
 
 SBL_F32 = 0
@@ -59,6 +62,9 @@ SIGNATURES = {
     "sbl_copy_to_host": (_int, [_vp, _vp, _sz, _vp]),
     "sbl_linear_hostio": (_int, [_vp, _i64, _i64, _vp, _vp, _vp, _i64, _int, _int, _vp, _vp, _int, _vp, _sz, _vp]),
     "sbl_linear_plan": (_int, [_i64, _i64, _i64, _int, _int, _sz]),
+    "sbl_norm": (_int, [_vp, _int, _i64, _i64, _int, _vp, _vp, _f32, _vp, _vp, _vp, _vp]),
+    "sbl_norm_backward_workspace_bytes": (_sz, [_i64, _i64, _int]),
+    "sbl_norm_backward": (_int, [_vp, _vp, _int, _i64, _i64, _int, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "sbl_mask_monitor": (_int, [_vp, _vp, _i64, _i64, _int, _int, _vp, _vp, _vp]),
     "sbl_linear_backward": (_int, [_vp, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _int, _vp]),
     "sbl_linear_backward_workspace_bytes": (_sz, [_i64, _i64, _i64, _int, _int]),

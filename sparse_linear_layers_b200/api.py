@@ -58,6 +58,43 @@ def _need_workspace(ws: torch.Tensor, device) -> None:
     _need_cuda(ws, "workspace", torch.uint8, None, device)
 
 
+class _LaunchOn:
+    """``with _LaunchOn(device, stream) as handle``: makes ``device`` current, and
+    ``stream`` when one is given, for a call: the kernels run there, and what
+    the call allocates belongs to that stream."""
+    __slots__ = ("_held",)
+
+    def __init__(self, device, stream: Optional[torch.cuda.Stream]):
+        if stream is not None and stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the operands on {device}")
+        self._held = ()
+        if stream is not None:
+            self._held = (torch.cuda.stream(stream),)  # makes its device current as well
+        elif device.index != torch.cuda.current_device():
+            self._held = (torch.cuda.device(device),)
+
+    def __enter__(self) -> int:
+        for c in self._held:
+            c.__enter__()
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc) -> None:
+        for c in reversed(self._held):
+            c.__exit__(*exc)
+
+
+def _ptr(t: Optional[torch.Tensor]):
+    return t.data_ptr() if t is not None else None
+
+
+def _scratch(nbytes: int, workspace: Optional[torch.Tensor], device) -> torch.Tensor:
+    """``workspace``, checked, or a new one of ``nbytes``."""
+    if workspace is None:
+        return torch.empty((max(1, nbytes),), dtype=torch.uint8, device=device)
+    _need_workspace(workspace, device)
+    return workspace
+
+
 @dataclass
 class PreparedWeights:
     """2-bit packed ternary weights of one layer plus its per-row scales."""
@@ -161,6 +198,78 @@ def sbl_rmsnorm_quant_act(x: torch.Tensor, g: torch.Tensor, eps: float = RMSNORM
     check(lib.sbl_rmsnorm_quant_act(x.data_ptr(), g.data_ptr(), float(eps), T, K, xq.data_ptr(), s.data_ptr(),
                                     _stream(stream)), "sbl_rmsnorm_quant_act")
     return xq, s
+
+
+_NORM_KINDS = {"rms": _lib.SBL_NORM_RMS, "layer": _lib.SBL_NORM_LAYER}
+_DTYPES = {torch.float32: _lib.SBL_F32, torch.bfloat16: _lib.SBL_BF16}
+
+
+def _need_norm(x: torch.Tensor, weight: torch.Tensor, kind: str):
+    if kind not in _NORM_KINDS:
+        raise ValueError(f"kind must be one of {sorted(_NORM_KINDS)}, got {kind!r}")
+    T, K = _need_2d(x, "x")
+    if x.dtype not in _DTYPES:
+        raise ValueError(f"x must be float32 or bfloat16, got {x.dtype}")
+    _need_cuda(x, "x", x.dtype)
+    _need_cuda(weight, "weight", torch.float32, (K,), x.device)
+    return T, K
+
+
+def sbl_norm(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None, kind: str = "rms",
+             eps: float = RMSNORM_EPS_F32, y: Optional[torch.Tensor] = None, with_stats: bool = False,
+             stream: Optional[torch.cuda.Stream] = None):
+    """RMS norm (``kind="rms"``) or layer norm (``"layer"``) of the rows of x (fp32
+    or bf16 [T,K]) with fp32 weight and optional bias [K]: y in x's type.
+    ``with_stats`` returns (y, mean, rstd), fp32 [T], for sbl_norm_backward
+    (mean is None for the RMS form)."""
+    T, K = _need_norm(x, weight, kind)
+    if bias is not None:
+        _need_cuda(bias, "bias", torch.float32, (K,), x.device)
+    with _LaunchOn(x.device, stream) as st:
+        if y is None:
+            y = torch.empty_like(x)
+        _need_cuda(y, "y", x.dtype, (T, K), x.device)
+        stat = lambda: torch.empty((T,), dtype=torch.float32, device=x.device)
+        mean = stat() if with_stats and kind == "layer" else None
+        rstd = stat() if with_stats else None
+        check(lib.sbl_norm(x.data_ptr(), _DTYPES[x.dtype], T, K, _NORM_KINDS[kind], weight.data_ptr(), _ptr(bias),
+                           float(eps), y.data_ptr(), _ptr(mean), _ptr(rstd), st), "sbl_norm")
+    return (y, mean, rstd) if with_stats else y
+
+
+def sbl_norm_backward_workspace_bytes(T: int, K: int, dtype: torch.dtype = torch.bfloat16) -> int:
+    return int(lib.sbl_norm_backward_workspace_bytes(T, K, _DTYPES[dtype]))
+
+
+def sbl_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, mean: Optional[torch.Tensor],
+                      rstd: torch.Tensor, kind: str = "rms", need_dx: bool = True, need_dw: bool = True,
+                      need_db: bool = True, workspace: Optional[torch.Tensor] = None,
+                      stream: Optional[torch.cuda.Stream] = None):
+    """Gradients of sbl_norm: (dx in x's type, dweight fp32 [K], dbias fp32 [K]),
+    None for the ones not asked for.  ``mean`` (layer norm only) and ``rstd`` are
+    sbl_norm's statistics."""
+    T, K = _need_norm(x, weight, kind)
+    dev = x.device
+    _need_cuda(dy, "dy", x.dtype, (T, K), dev)
+    _need_cuda(rstd, "rstd", torch.float32, (T,), dev)
+    if kind == "layer":
+        if mean is None:
+            raise ValueError("layer norm's backward needs mean")
+        _need_cuda(mean, "mean", torch.float32, (T,), dev)
+    if not (need_dx or need_dw or need_db):
+        raise ValueError("ask for dx, dweight or dbias")
+    with _LaunchOn(dev, stream) as st:
+        dx = torch.empty_like(x) if need_dx else None
+        dw = torch.empty((K,), dtype=torch.float32, device=dev) if need_dw else None
+        db = torch.empty((K,), dtype=torch.float32, device=dev) if need_db else None
+        ws = None
+        if need_dw or need_db:
+            ws = _scratch(sbl_norm_backward_workspace_bytes(T, K, x.dtype), workspace, dev)
+        check(lib.sbl_norm_backward(dy.data_ptr(), x.data_ptr(), _DTYPES[x.dtype], T, K, _NORM_KINDS[kind],
+                                    weight.data_ptr(), _ptr(mean) if kind == "layer" else None, rstd.data_ptr(),
+                                    _ptr(dx), _ptr(dw), _ptr(db), _ptr(ws), ws.numel() if ws is not None else 0, st),
+              "sbl_norm_backward")
+    return dx, dw, db
 
 
 def sbl_linear_workspace_bytes(T: int, K: int, O: int, n: int, m: int) -> int:

@@ -1,7 +1,7 @@
 // C ABI of the Sparse-BitLinear library: argument validation, workspace
 // layout, path dispatch and the per-device status word.  All arithmetic runs
 // in the kernels of prep.cu, quant.cu, decode.cu, decode_mma.cu, prefill.cu, prefill_pair.cu, prefill_sp.cu,
-// mask_monitor.cu, backward.cu and backward_tc.cu.
+// mask_monitor.cu, backward.cu, backward_tc.cu and norm.cu.
 #include <cstdint>
 #include <cstdio>
 #include <cuda_runtime.h>
@@ -65,6 +65,12 @@ cudaError_t launch_xq_to_pairs(const int8_t* xq, long long T, long long K, int8_
 cudaError_t launch_prefill_sp(const int8_t* xq, const float* s_tok, long long T, long long K, const uint8_t* packed,
                               const float* row_scale, long long O, void* y, int y_bf16, int32_t* acc_out,
                               uint8_t* scratch, unsigned* status, int num_sms, cudaStream_t stream);
+size_t norm_bwd_part_bytes(long long T, long long K, int bf16, int num_sms);
+cudaError_t launch_norm_fwd(const void* x, int bf16, int layer, const float* w, const float* b, float eps, long long T,
+                            long long K, void* y, float* mean, float* rstd, int num_sms, cudaStream_t st);
+cudaError_t launch_norm_bwd(const void* dy, const void* x, int bf16, int layer, const float* w, const float* mean,
+                            const float* rstd, long long T, long long K, void* dx, float* dw, float* db, float* part,
+                            int num_sms, cudaStream_t st);
 #ifdef SBL_TRACE
 cudaError_t set_prefill_trace(void* buf);
 cudaError_t set_pair_trace(void* buf);
@@ -213,6 +219,65 @@ sbl_status sbl_rmsnorm_quant_act(const uint16_t* x_bf16, const float* g, float e
     if (sbl_status s = device_info(&d)) return s;
     return from_cuda(sbl::launch_rmsnorm_quant(x_bf16, g, eps, T, K, x_q, s_tok, sbl::kLayoutNatural, d->status,
                                                static_cast<cudaStream_t>(stream), nullptr, 0));
+}
+
+static sbl_status check_norm(int dtype, int64_t T, int64_t K, int kind) {
+    if (T < 0) return SBL_ERR_INVALID_ARG;
+    if (sbl_status s = check_k(K)) return s;
+    if (dtype != SBL_F32 && dtype != SBL_BF16) return SBL_ERR_INVALID_ARG;
+    if (kind != SBL_NORM_RMS && kind != SBL_NORM_LAYER) return SBL_ERR_INVALID_ARG;
+    if (T > (1ll << 31) - 1) return SBL_ERR_UNSUPPORTED;
+    return SBL_OK;
+}
+
+sbl_status sbl_norm(const void* x, int dtype, int64_t T, int64_t K, int kind, const float* weight, const float* bias,
+                    float eps, void* y, float* mean, float* rstd, void* stream) {
+    if (sbl_status s = check_norm(dtype, T, K, kind)) return s;
+    if (!(eps >= 0.0f) || !(eps < 3.0e38f)) return SBL_ERR_INVALID_ARG;
+    if (T == 0) return SBL_OK;
+    if (!x || !weight || !y || x == y) return SBL_ERR_INVALID_ARG;
+    for (const void* p : {x, static_cast<const void*>(weight), static_cast<const void*>(bias),
+                          static_cast<const void*>(y), static_cast<const void*>(mean), static_cast<const void*>(rstd)})
+        if (!aligned(p, 16)) return SBL_ERR_INVALID_ARG;
+    DeviceInfo* d;
+    if (sbl_status s = device_info(&d)) return s;
+    return from_cuda(sbl::launch_norm_fwd(x, dtype == SBL_BF16, kind == SBL_NORM_LAYER, weight, bias, eps, T, K, y,
+                                          kind == SBL_NORM_LAYER ? mean : nullptr, rstd, d->num_sms,
+                                          static_cast<cudaStream_t>(stream)));
+}
+
+size_t sbl_norm_backward_workspace_bytes(int64_t T, int64_t K, int dtype) {
+    DeviceInfo* d;
+    if (check_norm(dtype, T, K, SBL_NORM_RMS) || T == 0 || device_info(&d)) return 0;
+    return round256(sbl::norm_bwd_part_bytes(T, K, dtype == SBL_BF16, d->num_sms));
+}
+
+sbl_status sbl_norm_backward(const void* dy, const void* x, int dtype, int64_t T, int64_t K, int kind,
+                             const float* weight, const float* mean, const float* rstd, void* dx, float* dweight,
+                             float* dbias, void* workspace, size_t workspace_bytes, void* stream) {
+    if (sbl_status s = check_norm(dtype, T, K, kind)) return s;
+    if (!dx && !dweight && !dbias) return SBL_ERR_INVALID_ARG;
+    if (!aligned(dweight, 16) || !aligned(dbias, 16)) return SBL_ERR_INVALID_ARG;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (T == 0) {  // empty sums
+        cudaError_t e = cudaSuccess;
+        if (dweight) e = cudaMemsetAsync(dweight, 0, static_cast<size_t>(K) * sizeof(float), st);
+        if (dbias && e == cudaSuccess) e = cudaMemsetAsync(dbias, 0, static_cast<size_t>(K) * sizeof(float), st);
+        return from_cuda(e);
+    }
+    if (!dy || !x || !weight || !rstd || (kind == SBL_NORM_LAYER && !mean) || dx == x || dx == dy)
+        return SBL_ERR_INVALID_ARG;
+    for (const void* p : {dy, x, static_cast<const void*>(weight), static_cast<const void*>(mean),
+                          static_cast<const void*>(rstd), static_cast<const void*>(dx)})
+        if (!aligned(p, 16)) return SBL_ERR_INVALID_ARG;
+    const bool sums = dweight || dbias;
+    if (sums && (!workspace || !aligned(workspace, 256))) return SBL_ERR_WORKSPACE;
+    DeviceInfo* d;
+    if (sbl_status s = device_info(&d)) return s;
+    if (sums && workspace_bytes < sbl::norm_bwd_part_bytes(T, K, dtype == SBL_BF16, d->num_sms))
+        return SBL_ERR_WORKSPACE;
+    return from_cuda(sbl::launch_norm_bwd(dy, x, dtype == SBL_BF16, kind == SBL_NORM_LAYER, weight, mean, rstd, T, K, dx,
+                                          dweight, dbias, static_cast<float*>(workspace), d->num_sms, st));
 }
 
 sbl_status sbl_mask_monitor(const uint8_t* old_bits, const uint8_t* new_bits, int64_t O, int64_t K, int n, int m,

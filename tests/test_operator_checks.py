@@ -1,0 +1,86 @@
+"""Refusals of the norm, gated feed-forward and cross-entropy calls, without a GPU:
+the C entry points on fake aligned addresses (validation fails before anything
+is enqueued), and the PyTorch calls with the library replaced by a recorder."""
+import pytest
+import torch
+
+from sparse_linear_layers_b200 import api
+
+
+class _Recorder:
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls.append(name)
+            return 0
+        return call
+
+
+class _NoLaunch:
+    def __init__(self, device, stream):
+        pass
+
+    def __enter__(self):
+        return 0
+
+    def __exit__(self, *exc):
+        pass
+
+
+@pytest.fixture
+def rec(monkeypatch):
+    r = _Recorder()
+    monkeypatch.setattr(api, "lib", r)
+    monkeypatch.setattr(api, "_LaunchOn", _NoLaunch)
+    monkeypatch.setattr(torch.Tensor, "is_cuda", property(lambda self: self.device.type == "cpu"))
+    return r
+
+
+def test_norm_rejects_on_host():
+    from sparse_linear_layers_b200._lib import lib
+    p, q = 4096, 8192
+    N = lib.sbl_norm
+    assert N(None, 1, 0, 64, 0, None, None, 1e-5, None, None, None, None) == 0   # T == 0
+    assert N(p, 1, 4, 40, 0, p, None, 1e-5, q, None, None, None) == 1            # K % 16 != 0
+    assert N(p, 1, 4, 1 << 25, 0, p, None, 1e-5, q, None, None, None) == 2       # K too long
+    assert N(p, 1, -1, 64, 0, p, None, 1e-5, q, None, None, None) == 1
+    assert N(p, 2, 4, 64, 0, p, None, 1e-5, q, None, None, None) == 1            # type
+    assert N(p, 1, 4, 64, 2, p, None, 1e-5, q, None, None, None) == 1            # kind
+    assert N(p, 1, 4, 64, 0, p, None, -1.0, q, None, None, None) == 1            # eps
+    assert N(p, 1, 4, 64, 0, p, None, float("nan"), q, None, None, None) == 1
+    assert N(p, 1, 4, 64, 0, None, None, 1e-5, q, None, None, None) == 1         # no weight
+    assert N(p, 1, 4, 64, 0, p + 4, None, 1e-5, q, None, None, None) == 1        # unaligned weight
+    assert N(p, 1, 4, 64, 0, p, p + 8, 1e-5, q, None, None, None) == 1           # unaligned bias
+    assert N(p, 1, 4, 64, 0, p, None, 1e-5, p, None, None, None) == 1            # y is x
+    B = lib.sbl_norm_backward
+    assert B(p, p, 1, 4, 64, 0, p, None, p, None, None, None, q, 1 << 20, None) == 1        # no output
+    assert B(p, p, 1, 4, 64, 1, p, None, p, q, None, None, q, 1 << 20, None) == 1           # layer: no mean
+    assert B(p, p, 1, 4, 64, 0, p, None, None, q, None, None, q, 1 << 20, None) == 1        # no rstd
+    assert B(p, p, 1, 4, 64, 0, p, None, p, p, None, None, q, 1 << 20, None) == 1           # dx is dy
+    assert B(p, q, 1, 4, 64, 0, p, None, p, q, None, None, q, 1 << 20, None) == 1           # dx is x
+    assert B(p, p, 1, 4, 64, 0, p, None, p, None, q + 4, None, q, 1 << 20, None) == 1       # unaligned dweight
+    assert B(p, p, 1, 4, 64, 0, p, None, p, None, q, None, None, 1 << 20, None) == 6        # no workspace
+    assert B(p, p, 1, 4, 64, 0, p, None, p, None, q, None, q + 16, 1 << 20, None) == 6      # unaligned workspace
+
+
+def test_norm_tensor_checks(rec):
+    x, w = torch.zeros(4, 64), torch.ones(64)
+    ok = [lambda: api.sbl_norm(x, w), lambda: api.sbl_norm(x.bfloat16(), w, w, kind="layer", with_stats=True)]
+    for f in ok:
+        f()
+    assert rec.calls == ["sbl_norm", "sbl_norm"]
+    r = torch.ones(4)
+    bad = [lambda: api.sbl_norm(x, w, kind="batch"), lambda: api.sbl_norm(x.half(), w), lambda: api.sbl_norm(x[0], w),
+           lambda: api.sbl_norm(x, w[:32]), lambda: api.sbl_norm(x, w.double()), lambda: api.sbl_norm(x, w, w[:16]),
+           lambda: api.sbl_norm(x.t(), torch.ones(4)), lambda: api.sbl_norm(x, w, y=torch.zeros(4, 32)),
+           lambda: api.sbl_norm(x, w, y=torch.zeros(4, 64).bfloat16()),
+           lambda: api.sbl_norm_backward(x[:3], x, w, None, r), lambda: api.sbl_norm_backward(x.bfloat16(), x, w, None, r),
+           lambda: api.sbl_norm_backward(x, x, w, None, r[:3]), lambda: api.sbl_norm_backward(x, x, w, None, r, kind="layer"),
+           lambda: api.sbl_norm_backward(x, x, w, r.double(), r, kind="layer"),
+           lambda: api.sbl_norm_backward(x, x, w, None, r, need_dx=False, need_dw=False, need_db=False),
+           lambda: api.sbl_norm_backward(x, x, w, None, r, workspace=torch.zeros(8))]
+    for f in bad:
+        with pytest.raises(ValueError):
+            f()
