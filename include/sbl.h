@@ -312,6 +312,52 @@ sbl_status sbl_linear_backward_ws(const float* dY, int64_t T, int64_t O, const i
                                   int flags, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * sbl_linear_cross_entropy — softmax cross entropy of a vocabulary projection
+ * (the LM head's loss of a training or scoring pass), per token, without
+ * keeping the logits.
+ *   z[t, v] = sum_d x[t, d] * W[v, d] (exact bf16 products, fp32 sums),
+ *   lse[t] = log sum_v exp(z[t, v]), loss[t] = lse[t] - z[t, target[t]],
+ *   loss[t] = 0 where target[t] == ignore_index.
+ *
+ *   x_bf16    bf16 bit patterns [T, D]: the hidden states.
+ *   w_bf16    bf16 bit patterns [V, D]: one row per word; V >= 1.
+ *   target    int64 [T]: the word of each token, or ignore_index (any value).
+ *             Another target outside [0, V) sets SBL_ERR_INVALID_ARG in the
+ *             device status word; that token's loss is NaN.
+ *   loss, lse fp32 [T] (outputs); lse also for ignored tokens.
+ *   workspace sbl_linear_cross_entropy_workspace_bytes(T, V) bytes, 256-byte
+ *             aligned (8 bytes per token and 128 words).
+ * D % 16 == 0; T, D, V up to 2^24, else SBL_ERR_UNSUPPORTED.  x and W finite
+ * (also in ignored rows).  Asynchronous on `stream`.
+ */
+size_t sbl_linear_cross_entropy_workspace_bytes(int64_t T, int64_t V);
+sbl_status sbl_linear_cross_entropy(const uint16_t* x_bf16, int64_t T, int64_t D, const uint16_t* w_bf16, int64_t V,
+                                    const int64_t* target, int64_t ignore_index, float* loss, float* lse,
+                                    void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * sbl_linear_cross_entropy_backward — the gradients of sum_t dloss[t] * loss[t].
+ *   G[t, v] = (exp(z[t, v] - lse[t]) - [v == target[t]]) * dloss[t], 0 for
+ *   ignored tokens; dX = G . W, dW = G^T . x.
+ *
+ *   dloss     fp32 [T], finite; lse as sbl_linear_cross_entropy wrote it.
+ *   dx, dw    bf16 [T, D] and [V, D] (outputs), each may be NULL, not both;
+ *             overwritten (dw with zeros for T == 0).
+ *   workspace sbl_linear_cross_entropy_backward_workspace_bytes(T, D, V, dx != NULL)
+ *             bytes, 256-byte aligned.
+ * The logits are computed again, one piece of the vocabulary at a time.  G is
+ * rounded to bf16 for the tensor cores (relative to max |dloss|, so a uniform
+ * dloss is exact); sums are fp32, and dx and dw are rounded once.  The same
+ * inputs give the same bits.  Limits and errors as the forward; a target
+ * outside [0, V) that is not ignored has no gradient.
+ */
+size_t sbl_linear_cross_entropy_backward_workspace_bytes(int64_t T, int64_t D, int64_t V, int need_dx);
+sbl_status sbl_linear_cross_entropy_backward(const float* dloss, const uint16_t* x_bf16, int64_t T, int64_t D,
+                                             const uint16_t* w_bf16, int64_t V, const int64_t* target,
+                                             int64_t ignore_index, const float* lse, uint16_t* dx, uint16_t* dw,
+                                             void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * sbl_linear_workspace_bytes — bytes of device workspace sbl_linear needs for
  * these sizes: the quantised activations and their scales, in the kernels'
  * internal layout (T*K + 4*T bytes, each rounded up to 256), plus, for 2:4

@@ -65,6 +65,11 @@ SIGNATURES = {
     "sbl_norm": (_int, [_vp, _int, _i64, _i64, _int, _vp, _vp, _f32, _vp, _vp, _vp, _vp]),
     "sbl_norm_backward_workspace_bytes": (_sz, [_i64, _i64, _int]),
     "sbl_norm_backward": (_int, [_vp, _vp, _int, _i64, _i64, _int, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "sbl_linear_cross_entropy_workspace_bytes": (_sz, [_i64, _i64]),
+    "sbl_linear_cross_entropy": (_int, [_vp, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _sz, _vp]),
+    "sbl_linear_cross_entropy_backward_workspace_bytes": (_sz, [_i64, _i64, _i64, _int]),
+    "sbl_linear_cross_entropy_backward": (_int, [_vp, _vp, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _sz,
+                                                 _vp]),
     "sbl_mask_monitor": (_int, [_vp, _vp, _i64, _i64, _int, _int, _vp, _vp, _vp]),
     "sbl_linear_backward": (_int, [_vp, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _int, _vp]),
     "sbl_linear_backward_workspace_bytes": (_sz, [_i64, _i64, _i64, _int, _int]),

@@ -549,6 +549,61 @@ def sbl_linear_backward(dY: torch.Tensor, x_q: torch.Tensor, s_tok: torch.Tensor
     return (dX if need_dx else None), (dW if need_dw else None)
 
 
+def sbl_linear_cross_entropy_workspace_bytes(T: int, V: int) -> int:
+    return int(lib.sbl_linear_cross_entropy_workspace_bytes(T, V))
+
+
+def _need_xent(x: torch.Tensor, W: torch.Tensor, target: torch.Tensor):
+    T, D = _need_2d(x, "x")
+    _need_cuda(x, "x", torch.bfloat16)
+    V = _need_2d(W, "W")[0]
+    _need_cuda(W, "W", torch.bfloat16, (V, D), x.device)
+    _need_cuda(target, "target", torch.int64, (T,), x.device)
+    return T, D, V
+
+
+def sbl_linear_cross_entropy(x: torch.Tensor, W: torch.Tensor, target: torch.Tensor, ignore_index: int = -100,
+                             workspace: Optional[torch.Tensor] = None,
+                             stream: Optional[torch.cuda.Stream] = None):
+    """Per-token softmax cross entropy of the logits x . W^T, which are never
+    stored: (loss, lse), fp32 [T].  x bf16 [T,D], W bf16 [V,D], target int64
+    [T]; tokens whose target is ``ignore_index`` have loss 0."""
+    T, D, V = _need_xent(x, W, target)
+    with _LaunchOn(x.device, stream) as st:
+        loss, lse = torch.empty((2, (T + 3) // 4 * 4), dtype=torch.float32, device=x.device)[:, :T].unbind()
+        ws = _scratch(sbl_linear_cross_entropy_workspace_bytes(T, V), workspace, x.device)
+        check(lib.sbl_linear_cross_entropy(x.data_ptr(), T, D, W.data_ptr(), V, target.data_ptr(), ignore_index,
+                                           loss.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel(), st),
+              "sbl_linear_cross_entropy")
+    return loss, lse
+
+
+def sbl_linear_cross_entropy_backward_workspace_bytes(T: int, D: int, V: int, need_dx: bool = True) -> int:
+    return int(lib.sbl_linear_cross_entropy_backward_workspace_bytes(T, D, V, int(need_dx)))
+
+
+def sbl_linear_cross_entropy_backward(dloss: torch.Tensor, x: torch.Tensor, W: torch.Tensor, target: torch.Tensor,
+                                      lse: torch.Tensor, ignore_index: int = -100, need_dx: bool = True,
+                                      need_dw: bool = True, workspace: Optional[torch.Tensor] = None,
+                                      stream: Optional[torch.cuda.Stream] = None):
+    """Gradients of sum(dloss * loss): (dX bf16 [T,D] or None, dW bf16 [V,D] or
+    None); ``lse`` from sbl_linear_cross_entropy."""
+    T, D, V = _need_xent(x, W, target)
+    _need_cuda(dloss, "dloss", torch.float32, (T,), x.device)
+    _need_cuda(lse, "lse", torch.float32, (T,), x.device)
+    if not (need_dx or need_dw):
+        raise ValueError("ask for dX, dW or both")
+    with _LaunchOn(x.device, stream) as st:
+        dx = torch.empty_like(x) if need_dx else None
+        dw = torch.empty_like(W) if need_dw else None
+        ws = _scratch(sbl_linear_cross_entropy_backward_workspace_bytes(T, D, V, need_dx), workspace, x.device)
+        check(lib.sbl_linear_cross_entropy_backward(dloss.data_ptr(), x.data_ptr(), T, D, W.data_ptr(), V,
+                                                    target.data_ptr(), ignore_index, lse.data_ptr(), _ptr(dx), _ptr(dw),
+                                                    ws.data_ptr(), ws.numel(), st),
+              "sbl_linear_cross_entropy_backward")
+    return dx, dw
+
+
 _PATH_NAMES = {v: k for k, v in _PATHS.items()}
 
 

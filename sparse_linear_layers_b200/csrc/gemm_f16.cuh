@@ -1,0 +1,428 @@
+// A persistent 2-SM tcgen05 GEMM on bf16 or fp16 operands (kind::f16, fp32
+// accumulators) whose epilogue is a template parameter:
+//
+//   acc[m, n] = sum_j sum_k A_j[m, k] * B[n, k],  j < NA
+//
+// A cluster of two CTAs computes 256 x 256 tiles.  CTA rank r stages rows
+// 128 r .. + 127 of each A_j and 128 r .. + 127 of B per 64-deep k-block (TMA,
+// 128B swizzle) and holds the accumulators of its 128 rows in its own tensor
+// memory; the even CTA issues the MMAs (M = 256, N = 256, K = 16).  Either
+// operand may be stored with k along its rows (K-major: [m, k] row-major) or
+// with m or n along its rows (MN-major: [k, m] row-major, two boxes of 64
+// columns per stage), so no operand is transposed in memory.
+//
+// Two accumulator buffers (all 512 TMEM columns) let the eight epilogue warps
+// read one while the MMAs fill the other.
+//
+// SEGMENT > 0: the tensor cores round every fp32 accumulation towards zero, an
+// error that grows with the number of MMAs summed into one accumulator (a
+// relative 1.4e-5 after 1344 of them, measured).  The reduction is then cut
+// into segments of SEGMENT k-blocks; each segment starts from zero and the
+// epilogue threads add it, rounding to nearest, to sums in registers.
+// Costs one 128-column TMEM read and 128 additions per thread and segment,
+// hidden behind the next segment's MMAs.
+//
+// Warps (320 threads): 0-7 epilogue (warp w: TMEM lanes 32 (w % 4) .. + 31,
+// columns 128 (w / 4) .. + 127), 8 TMA producer, 9 TMEM allocation and, in the
+// even CTA, MMA issue.  Every wait is bounded; a CTA that gives up records a
+// timeout, lets its loads land and its MMAs finish (bounded) and exits.
+#pragma once
+
+#include <cuda.h>
+
+#include "sbl_common.cuh"
+#include "tc_util.cuh"
+
+namespace sbl {
+
+namespace gm {
+constexpr int BM = 128;             // rows per CTA (pair: 256)
+constexpr int BN = 256;             // columns per pair tile
+constexpr int BK = 64;              // reduction elements per stage (128 bytes)
+constexpr int TILE = BM * BK * 2;   // one operand tile of one CTA: 16 KB
+constexpr int EPI_WARPS = 8;
+constexpr int WARP_TMA = 8;
+constexpr int WARP_MMA = 9;
+constexpr int THREADS = 320;
+constexpr int BOX = 32 * 128;       // one warp's staging box: 32 rows x 128 bytes
+constexpr int stages(int na) { return na == 1 ? 6 : 4; }
+}  // namespace gm
+
+template <int NA>
+struct GemmSmem {
+    uint8_t a[gm::stages(NA)][NA][gm::TILE];  // 1024-byte aligned tiles
+    uint8_t b[gm::stages(NA)][gm::TILE];
+    uint8_t box[gm::EPI_WARPS][gm::BOX];
+    uint64_t full[gm::stages(NA)];            // used in the even CTA
+    uint64_t empty[gm::stages(NA)];
+    uint64_t tmem_full[2];
+    uint64_t tmem_empty[2];                   // used in the even CTA
+    uint64_t mma_done;
+    uint32_t tmem_base;
+    int abort_flag;
+};
+template <int NA>
+constexpr size_t gemm_smem_bytes() {
+    return sizeof(GemmSmem<NA>) + 1024;
+}
+static_assert(gemm_smem_bytes<1>() <= 232448 && gemm_smem_bytes<2>() <= 232448, "GEMM stages do not fit");
+
+// The sizes of one launch.  Rows of A beyond M, of B beyond N and k beyond K
+// are zero-filled by TMA.  a_part: k offset (elements) between the A_j when
+// they lie side by side in one K-major matrix, or row offset (in k) between
+// them in an MN-major one.
+struct GemmShape {
+    int M, N, K;
+    int a_part;
+    int panel;  // consecutive tiles walk across `panel` column tiles, then down M
+};
+
+struct GemmTile {
+    int m0, n0;       // first row and column of the pair's tile
+    int row;          // this thread's row
+    int warp_row;     // first row of this warp
+    int col0;         // first of this warp's 128 columns
+    int lane;
+    uint8_t* box;     // this warp's staging box
+};
+
+// MN-major, 128-byte swizzle: 64 columns x 8 k per 1024-byte atom, atoms along
+// k 1024 bytes apart, the second 64 columns a whole box (64 k x 128 bytes) on.
+__device__ __forceinline__ uint64_t sw128_mn_desc(uint32_t saddr) {
+    uint64_t d = static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+    d |= static_cast<uint64_t>(8192u >> 4) << 16;
+    d |= static_cast<uint64_t>(1024u >> 4) << 32;
+    d |= static_cast<uint64_t>(1u) << 46;
+    d |= static_cast<uint64_t>(2u) << 61;
+    return d;
+}
+
+__device__ __forceinline__ void tc_mma_pair_f16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                                uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+// Adds a staging box to fp32 memory (each element once: no order to depend on).
+__device__ __forceinline__ void tma_add_2d(const CUtensorMap* map, uint32_t src, int x, int y) {
+    asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(src)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
+__device__ __forceinline__ void box_put(uint8_t* box, int lane, int c, uint32_t w0, uint32_t w1, uint32_t w2,
+                                        uint32_t w3) {
+    const uint32_t a = smem_u32(box + lane * 128 + ((c ^ (lane & 7)) << 4));
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(w0), "r"(w1), "r"(w2), "r"(w3) : "memory");
+}
+__device__ __forceinline__ void box_wait(int lane) {  // the box's previous store has read it
+    if (lane == 0) bulk_wait_read<0>();
+    __syncwarp();
+}
+
+// Epi: a struct with
+//   struct Params (a kernel argument, may hold tensor maps), static prefetch(const Params&),
+//   Epi(const Params&), begin(const GemmTile&), slice(const GemmTile&, int k, float (&v)[32])
+//   for columns col0 + 32 k .. + 31 of the thread's row (k = 0..3 in order), end(const GemmTile&).
+template <class Epi, int NA, bool A_MN, bool B_MN, bool FP16, int SEGMENT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gm::THREADS, 1)
+    gemm_f16_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
+                    const __grid_constant__ typename Epi::Params params, const GemmShape shape, unsigned* status) {
+    constexpr int STAGES = gm::stages(NA);
+    extern __shared__ uint8_t smem_raw[];
+    auto* sm = reinterpret_cast<GemmSmem<NA>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    volatile int* abort_flag = &sm->abort_flag;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+    const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+    const int MT = (shape.M + 2 * gm::BM - 1) / (2 * gm::BM), NT = (shape.N + gm::BN - 1) / gm::BN;
+    const int tiles = MT * NT;
+    const int KB = (shape.K + gm::BK - 1) / gm::BK;
+    const int SEG = SEGMENT > 0 ? SEGMENT : KB;
+
+    asm volatile("griddepcontrol.launch_dependents;");
+    if (threadIdx.x == 32) {
+        prefetch_tmap(&tmap_a);
+        prefetch_tmap(&tmap_b);
+        Epi::prefetch(params);
+    }
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&sm->full[s], 1);
+            mbar_init(&sm->empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&sm->tmem_full[b], 1);
+            mbar_init(&sm->tmem_empty[b], 2 * gm::EPI_WARPS);
+        }
+        mbar_init(&sm->mma_done, 1);
+        sm->abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == gm::WARP_MMA) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm->tmem_base)),
+                     "r"(2 * gm::BN)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem_base = sm->tmem_base;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    auto give_up = [&]() {
+        if (!*abort_flag) {
+            *abort_flag = 1;
+            raise_status(status, kStatusTimeout);
+        }
+    };
+    // tiles go panel by panel of column tiles, row by row of a panel: the
+    // panel's B tiles stay in L2 while A streams past them once per panel
+    auto tile_at = [&](int tile, int& m0, int& n0) {
+        const int first = tile / (MT * shape.panel) * shape.panel;
+        const int rem = tile - first * MT;
+        const int width = NT - first < shape.panel ? NT - first : shape.panel;
+        m0 = rem / width * (2 * gm::BM);
+        n0 = (first + rem % width) * gm::BN;
+    };
+
+    if (warp < gm::EPI_WARPS) {
+        // ------------------------------------------------------------ epilogue
+        const int qd = warp & 3, half = warp >> 2;
+        const uint32_t lane_addr = static_cast<uint32_t>(qd * 32) << 16;
+        Epi epi(params);
+        GemmTile t;
+        t.lane = lane;
+        t.box = sm->box[warp];
+        uint32_t seg = 0;  // accumulator buffers taken so far
+        auto release = [&](int b) {  // every load of the buffer has completed
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (leader) mbar_arrive(&sm->tmem_empty[b]);
+                else mbar_arrive_cluster(map_to_cta(smem_u32(&sm->tmem_empty[b]), 0));
+            }
+        };
+        for (int tile = pair; tile < tiles; tile += npairs) {
+            tile_at(tile, t.m0, t.n0);
+            t.warp_row = t.m0 + static_cast<int>(rank) * gm::BM + qd * 32;
+            t.row = t.warp_row + lane;
+            t.col0 = t.n0 + half * (gm::BN / 2);
+            epi.begin(t);
+            if (SEGMENT > 0) {
+                float acc[4][32];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) acc[k][i] = 0.f;
+                bool ok = true;
+                for (int kb = 0; kb < KB; kb += SEG, ++seg) {
+                    const int b = seg & 1;
+                    if (!warp_wait(&sm->tmem_full[b], (seg >> 1) & 1, abort_flag)) { give_up(); ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t tbase = tmem_base + lane_addr + b * gm::BN + half * (gm::BN / 2);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t r[32];
+                        tmem_ld32(tbase + 32 * k, r);
+                        if (k == 3) release(b);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) acc[k][i] += __uint_as_float(r[i]);
+                    }
+                }
+                if (!ok) break;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) epi.slice(t, k, acc[k]);
+            } else {
+                const int b = seg & 1;
+                if (!warp_wait(&sm->tmem_full[b], (seg >> 1) & 1, abort_flag)) { give_up(); break; }
+                ++seg;
+                tc_fence_after();
+                const uint32_t tbase = tmem_base + lane_addr + b * gm::BN + half * (gm::BN / 2);
+                uint32_t ra[32], rb[32];
+                tmem_ld32_nowait(tbase, ra);
+                tmem_ld_wait();
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    uint32_t(&cur)[32] = k & 1 ? rb : ra;
+                    uint32_t(&nxt)[32] = k & 1 ? ra : rb;
+                    if (k < 3) tmem_ld32_nowait(tbase + 32 * (k + 1), nxt);
+                    else release(b);
+                    float v[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(cur[i]);
+                    epi.slice(t, k, v);
+                    if (k < 3) tmem_ld_wait();
+                }
+            }
+            epi.end(t);
+        }
+        if (lane == 0) bulk_wait_all();
+    } else if (warp == gm::WARP_TMA) {
+        // ------------------------------------------------------------ TMA producer
+        if (lane == 0) {
+            uint32_t it = 0;
+            bool ok = true;
+            for (int tile = pair; tile < tiles && ok; tile += npairs) {
+                int m0, n0;
+                tile_at(tile, m0, n0);
+                const int arow = m0 + static_cast<int>(rank) * gm::BM, brow = n0 + static_cast<int>(rank) * gm::BM;
+                for (int kb = 0; kb < KB; ++kb, ++it) {
+                    const int s = it % STAGES;
+                    if (!mbar_wait(&sm->empty[s], ((it / STAGES) & 1) ^ 1, abort_flag)) { give_up(); ok = false; break; }
+                    // the even CTA expects the bytes of both CTAs
+                    if (leader) mbar_arrive_expect_tx(&sm->full[s], 2 * (NA + 1) * gm::TILE);
+                    const uint32_t full = map_to_cta(smem_u32(&sm->full[s]), 0);
+                    const int k0 = kb * gm::BK;
+#pragma unroll
+                    for (int j = 0; j < NA; ++j) {
+                        const uint32_t dst = smem_u32(sm->a[s][j]);
+                        if (A_MN) {
+                            tma_load_2d_pair(dst, &tmap_a, arow, j * shape.a_part + k0, full);
+                            tma_load_2d_pair(dst + gm::TILE / 2, &tmap_a, arow + 64, j * shape.a_part + k0, full);
+                        } else {
+                            tma_load_2d_pair(dst, &tmap_a, j * shape.a_part + k0, arow, full);
+                        }
+                    }
+                    const uint32_t dst = smem_u32(sm->b[s]);
+                    if (B_MN) {
+                        tma_load_2d_pair(dst, &tmap_b, brow, k0, full);
+                        tma_load_2d_pair(dst + gm::TILE / 2, &tmap_b, brow + 64, k0, full);
+                    } else {
+                        tma_load_2d_pair(dst, &tmap_b, k0, brow, full);
+                    }
+                }
+            }
+            // let the issued loads land before either CTA can exit (the even
+            // CTA's barriers count both CTAs' loads)
+            if (leader) {
+                const uint32_t first = it > STAGES ? it - STAGES : 0;
+                volatile int never = 0;
+                for (uint32_t j = first; j < it; ++j)
+                    if (!mbar_wait(&sm->full[j % STAGES], (j / STAGES) & 1, &never)) give_up();
+            }
+        }
+    } else {
+        // ------------------------------------------------------------ MMA issuer (even CTA)
+        if (lane == 0) {
+            if (leader) {
+                const uint32_t idesc = (1u << 4) | (FP16 ? 0u : (1u << 7) | (1u << 10)) | (A_MN ? 1u << 15 : 0u) |
+                                       (B_MN ? 1u << 16 : 0u) | (static_cast<uint32_t>(gm::BN >> 3) << 17) |
+                                       (static_cast<uint32_t>((2 * gm::BM) >> 4) << 24);
+                uint32_t it = 0, seg = 0;
+                bool ok = true;
+                for (int tile = pair; tile < tiles && ok; tile += npairs) {
+                    uint32_t d = 0;
+                    for (int kb = 0; kb < KB; ++kb, ++it) {
+                        const bool first = SEGMENT > 0 ? kb % (SEGMENT > 0 ? SEGMENT : 1) == 0 : kb == 0;
+                        if (first) {
+                            const int b = seg & 1;
+                            if (!mbar_wait(&sm->tmem_empty[b], ((seg >> 1) & 1) ^ 1, abort_flag)) { give_up(); ok = false; break; }
+                            tc_fence_after();
+                            d = tmem_base + b * gm::BN;
+                        }
+                        const int s = it % STAGES;
+                        if (!mbar_wait(&sm->full[s], (it / STAGES) & 1, abort_flag)) { give_up(); ok = false; break; }
+                        tc_fence_after();
+                        const uint32_t b0 = smem_u32(sm->b[s]);
+#pragma unroll
+                        for (int j = 0; j < NA; ++j) {
+                            const uint32_t a0 = smem_u32(sm->a[s][j]);
+#pragma unroll
+                            for (int kk = 0; kk < gm::BK / 16; ++kk)
+                                tc_mma_pair_f16(d, A_MN ? sw128_mn_desc(a0 + kk * 2048) : sw128_desc(a0 + kk * 32),
+                                                B_MN ? sw128_mn_desc(b0 + kk * 2048) : sw128_desc(b0 + kk * 32), idesc,
+                                                !(first && j == 0 && kk == 0));
+                        }
+                        tc_commit_pair_both(&sm->empty[s]);
+                        if (kb == KB - 1 || (SEGMENT > 0 && kb % (SEGMENT > 0 ? SEGMENT : 1) == SEGMENT - 1)) {
+                            tc_commit_pair_both(&sm->tmem_full[seg & 1]);
+                            ++seg;
+                        }
+                    }
+                }
+                // every MMA must be complete before either CTA frees tensor memory
+                tc_commit_pair_both(&sm->mma_done);
+            }
+            volatile int never = 0;
+            if (!mbar_wait(&sm->mma_done, 0, &never)) give_up();
+        }
+        __syncwarp();
+    }
+
+    tc_fence_before();
+    cluster_sync();  // neither CTA leaves while the other may still touch its shared memory
+    if (warp == gm::WARP_MMA) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(2 * gm::BN)
+                     : "memory");
+    }
+}
+
+// ---------------------------------------------------------------- host side
+// Tensor map of a row-major [rows, cols] matrix of 2- or 4-byte elements with
+// a box of box_cols x box_rows (128-byte rows, 128B swizzle).
+inline bool gemm_map(CUtensorMap* map, CUtensorMapDataType type, const void* base, long long rows, long long cols,
+                     long long pitch_bytes, int box_cols, int box_rows) {
+    EncodeTiledFn enc = get_encode_fn();
+    if (!enc) return false;
+    const cuuint32_t estr[2] = {1, 1};
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch_bytes)};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)};
+    return enc(map, type, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+           CUDA_SUCCESS;
+}
+
+// An operand of the GEMM: a 2-byte row-major matrix [rows, cols].  K-major
+// operands are read in boxes of 64 k x 128 rows, MN-major ones in boxes of
+// 64 columns x 64 k.
+inline bool gemm_operand(CUtensorMap* map, bool fp16, bool mn_major, const void* base, long long rows, long long cols,
+                         long long pitch_elems) {
+    return gemm_map(map, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, rows, cols,
+                    pitch_elems * 2, 64, mn_major ? 64 : gm::BM);
+}
+
+template <class Epi, int NA, bool A_MN, bool B_MN, bool FP16, int SEGMENT>
+cudaError_t launch_gemm_f16(const CUtensorMap& a, const CUtensorMap& b, const typename Epi::Params& p,
+                            const GemmShape& shape, unsigned* status, cudaStream_t stream) {
+    auto kern = gemm_f16_kernel<Epi, NA, A_MN, B_MN, FP16, SEGMENT>;
+    constexpr size_t smem = gemm_smem_bytes<NA>();
+    static int clusters[64] = {};  // pairs of this kernel that fit on each device at once
+    int dev = 0;
+    if (cudaError_t e = cudaGetDevice(&dev)) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(gm::THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    if (clusters[dev] == 0) {
+        if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)))
+            return e;
+        int n = 0;
+        if (cudaError_t e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg)) return e;
+        if (n <= 0) return cudaErrorNotSupported;
+        clusters[dev] = n;
+    }
+    const long long tiles = static_cast<long long>((shape.M + 2 * gm::BM - 1) / (2 * gm::BM)) *
+                            ((shape.N + gm::BN - 1) / gm::BN);
+    if (tiles <= 0 || tiles > (1ll << 30)) return cudaErrorInvalidValue;
+    cfg.gridDim = dim3(2 * static_cast<unsigned>(tiles < clusters[dev] ? tiles : clusters[dev]));
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, a, b, p, shape, status);
+}
+
+}  // namespace sbl

@@ -1,7 +1,7 @@
 // C ABI of the Sparse-BitLinear library: argument validation, workspace
 // layout, path dispatch and the per-device status word.  All arithmetic runs
 // in the kernels of prep.cu, quant.cu, decode.cu, decode_mma.cu, prefill.cu, prefill_pair.cu, prefill_sp.cu,
-// mask_monitor.cu, backward.cu, backward_tc.cu and norm.cu.
+// mask_monitor.cu, backward.cu, backward_tc.cu, norm.cu and xent.cu.
 #include <cstdint>
 #include <cstdio>
 #include <cuda_runtime.h>
@@ -71,6 +71,14 @@ cudaError_t launch_norm_fwd(const void* x, int bf16, int layer, const float* w, 
 cudaError_t launch_norm_bwd(const void* dy, const void* x, int bf16, int layer, const float* w, const float* mean,
                             const float* rstd, long long T, long long K, void* dx, float* dw, float* db, float* part,
                             int num_sms, cudaStream_t st);
+size_t xent_workspace_bytes(long long T, long long V);
+size_t xent_backward_workspace_bytes(long long T, long long D, long long V, int need_dx);
+cudaError_t launch_xent(const uint16_t* x, long long T, long long D, const uint16_t* w, long long V,
+                        const long long* target, long long ignore, float* loss, float* lse, void* ws, unsigned* status,
+                        cudaStream_t st);
+cudaError_t launch_xent_backward(const float* dloss, const uint16_t* x, long long T, long long D, const uint16_t* w,
+                                 long long V, const long long* target, long long ignore, const float* lse, uint16_t* dx,
+                                 uint16_t* dw, void* ws, unsigned* status, int num_sms, cudaStream_t st);
 #ifdef SBL_TRACE
 cudaError_t set_prefill_trace(void* buf);
 cudaError_t set_pair_trace(void* buf);
@@ -350,6 +358,62 @@ sbl_status sbl_linear_backward_ws(const float* dY, int64_t T, int64_t O, const i
     if (sbl_status s = device_info(&d)) return s;
     return from_cuda(sbl::launch_backward_tc(dY, T, O, x_q, s_tok, K, packed, row_scale, dX, dW, ternary ? 1 : 0,
                                              workspace, d->status, d->num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+// Sizes of the cross entropy: extents that the kernels hold in int32.
+static sbl_status check_xent(int64_t T, int64_t D, int64_t V) {
+    constexpr long long most = 1ll << 24;
+    if (T < 0 || V < 1 || D <= 0 || D % 16 != 0) return SBL_ERR_INVALID_ARG;
+    if (T > most || V > most || D > most) return SBL_ERR_UNSUPPORTED;
+    return SBL_OK;
+}
+
+size_t sbl_linear_cross_entropy_workspace_bytes(int64_t T, int64_t V) {
+    return check_xent(T, 16, V) || T == 0 ? 0 : sbl::xent_workspace_bytes(T, V);
+}
+
+sbl_status sbl_linear_cross_entropy(const uint16_t* x_bf16, int64_t T, int64_t D, const uint16_t* w_bf16, int64_t V,
+                                    const int64_t* target, int64_t ignore_index, float* loss, float* lse,
+                                    void* workspace, size_t workspace_bytes, void* stream) {
+    if (sbl_status s = check_xent(T, D, V)) return s;
+    if (T == 0) return SBL_OK;
+    for (const void* p : {static_cast<const void*>(x_bf16), static_cast<const void*>(w_bf16),
+                          static_cast<const void*>(target), static_cast<const void*>(loss),
+                          static_cast<const void*>(lse)})
+        if (!p || !aligned(p, 16)) return SBL_ERR_INVALID_ARG;
+    if (!workspace || !aligned(workspace, 256) || workspace_bytes < sbl::xent_workspace_bytes(T, V))
+        return SBL_ERR_WORKSPACE;
+    DeviceInfo* d;
+    if (sbl_status s = device_info(&d)) return s;
+    return from_cuda(sbl::launch_xent(x_bf16, T, D, w_bf16, V, reinterpret_cast<const long long*>(target), ignore_index,
+                                      loss, lse, workspace, d->status, static_cast<cudaStream_t>(stream)));
+}
+
+size_t sbl_linear_cross_entropy_backward_workspace_bytes(int64_t T, int64_t D, int64_t V, int need_dx) {
+    return check_xent(T, D, V) || T == 0 ? 0 : sbl::xent_backward_workspace_bytes(T, D, V, need_dx);
+}
+
+sbl_status sbl_linear_cross_entropy_backward(const float* dloss, const uint16_t* x_bf16, int64_t T, int64_t D,
+                                             const uint16_t* w_bf16, int64_t V, const int64_t* target,
+                                             int64_t ignore_index, const float* lse, uint16_t* dx, uint16_t* dw,
+                                             void* workspace, size_t workspace_bytes, void* stream) {
+    if (sbl_status s = check_xent(T, D, V)) return s;
+    if (!dx && !dw) return SBL_ERR_INVALID_ARG;
+    if (!aligned(dx, 16) || !aligned(dw, 16)) return SBL_ERR_INVALID_ARG;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (T == 0) return dw ? from_cuda(cudaMemsetAsync(dw, 0, static_cast<size_t>(V) * D * 2, st)) : SBL_OK;
+    for (const void* p : {static_cast<const void*>(dloss), static_cast<const void*>(x_bf16),
+                          static_cast<const void*>(w_bf16), static_cast<const void*>(target),
+                          static_cast<const void*>(lse)})
+        if (!p || !aligned(p, 16)) return SBL_ERR_INVALID_ARG;
+    if (!workspace || !aligned(workspace, 256) ||
+        workspace_bytes < sbl::xent_backward_workspace_bytes(T, D, V, dx != nullptr))
+        return SBL_ERR_WORKSPACE;
+    DeviceInfo* d;
+    if (sbl_status s = device_info(&d)) return s;
+    return from_cuda(sbl::launch_xent_backward(dloss, x_bf16, T, D, w_bf16, V,
+                                               reinterpret_cast<const long long*>(target), ignore_index, lse, dx, dw,
+                                               workspace, d->status, d->num_sms, st));
 }
 
 // Quantised activations and their scales: what every path needs.

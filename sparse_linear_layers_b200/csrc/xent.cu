@@ -1,0 +1,388 @@
+// Softmax cross entropy of a vocabulary projection (the LM head's loss), with
+// its gradients, without keeping the logits.
+//
+//   z[t, v] = x[t] . W[v],  lse[t] = log sum_v exp z[t, v],  loss[t] = lse[t] - z[t, target[t]]
+//   G[t, v] = (exp(z[t, v] - lse[t]) - [v == target[t]]) * dloss[t]
+//   dX = G . W,  dW = G^T . x
+//
+// (0 for a token whose target is the ignored index.)  The pages' repository
+// layout names such a step for training (a fused LM-head matmul with a chunked
+// cross entropy); here it is three uses of one tcgen05 GEMM (gemm_f16.cuh):
+//
+//   forward   z tiles of 256 x 256 whose epilogue keeps, per row and 128
+//             columns, the maximum and the sum of exponentials below it, and
+//             the target's logit; xent_merge_kernel joins the V / 128 parts of
+//             a row.  Memory: x and W once, 8 bytes per row and 128 columns.
+//   backward  per piece of the vocabulary: the z tiles again, their epilogue
+//             writing G in bf16; dX += G . W[piece]; dW[piece] = G^T . x.  G of
+//             one piece is all that exists of the [T, V] matrix.
+//
+// What G's bf16 costs: dX and dW are bf16, rounded from fp32 sums; rounding
+// each G adds an independent error of the same relative size (2^-8 at most) to each
+// term, at most sqrt(2) times the output's own rounding in the 2-norm.  To keep
+// the largest terms out of it, c = max_t |dloss[t]| is taken out of G and
+// multiplied back into the fp32 results: under a mean or sum reduction G's
+// entry at an unlikely target is then -1 exactly.
+//
+// Bound by the tensor cores: 2 T V D operations forward, 6 T V D backward (a
+// third of them the second time z is computed, the price of not keeping it).
+// The epilogue's exponentials (one per logit: 2048 cycles of the SM's 16 per
+// clock for its 128 x 256 half tile) hide behind the next tile's MMAs (7168
+// cycles at D = 896).
+#include <cuda.h>
+
+#include "gemm_f16.cuh"
+#include "sbl_common.cuh"
+
+namespace sbl {
+
+namespace {
+
+// The forward's logits are summed in segments of 16 k-blocks (1024 terms): in
+// one piece, D = 2048 left lse 1.5e-6 off (the tensor cores' rounding towards
+// zero), three times what a sum rounded to nearest leaves.
+constexpr int kLogitSegment = 16;
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// 32 columns of a row as bf16 into half H of the warp's box; the second half
+// sends the box of 64 columns.
+__device__ __forceinline__ void put_bf16(const GemmTile& t, int k, const float (&v)[32], const CUtensorMap* map) {
+    const int h = k & 1;
+    if (h == 0) box_wait(t.lane);
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        box_put(t.box, t.lane, 4 * h + c, pack_bf16(v[8 * c], v[8 * c + 1]), pack_bf16(v[8 * c + 2], v[8 * c + 3]),
+                pack_bf16(v[8 * c + 4], v[8 * c + 5]), pack_bf16(v[8 * c + 6], v[8 * c + 7]));
+    if (h == 1) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (t.lane == 0) tma_store_2d(map, smem_u32(t.box), t.col0 + 32 * (k - 1), t.warp_row);
+    }
+}
+
+// Forward epilogue: part[p][t] = (max, sum of exp(z - max)) over columns 128 p .. + 127.
+struct LsePart {
+    struct Params {
+        float2* part;
+        float* tlogit;
+        const long long* target;
+        int T, V;
+    };
+    static __device__ __forceinline__ void prefetch(const Params&) {}
+    const Params& p;
+    float mx, sum;
+    long long tcol;  // the target's column less col0
+    __device__ __forceinline__ explicit LsePart(const Params& q) : p(q), mx(0.f), sum(0.f), tcol(-1) {}
+    __device__ __forceinline__ void begin(const GemmTile& t) {
+        mx = -INFINITY;
+        sum = 0.f;
+        tcol = t.row < p.T ? __ldg(p.target + t.row) - t.col0 : -1;
+    }
+    __device__ __forceinline__ void slice(const GemmTile& t, int k, float (&v)[32]) {
+        const int valid = p.V - (t.col0 + 32 * k);
+        if (valid <= 0) return;
+        if (valid < 32) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (i >= valid) v[i] = -INFINITY;
+        }
+        const long long tc = tcol - 32 * k;
+        if (tc >= 0 && tc < 32) {
+            // by a bit, not by index: an index would put the row into local memory
+            const uint32_t hot = 1u << tc;
+            float z = 0.f;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) z = (hot & (1u << i)) ? v[i] : z;
+            p.tlogit[t.row] = z;
+        }
+        float m4[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+        for (int i = 4; i < 32; ++i) m4[i & 3] = fmaxf(m4[i & 3], v[i]);
+        const float m = fmaxf(mx, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
+        float s4[4] = {mx == -INFINITY ? 0.f : sum * exp2_fast((mx - m) * kLog2e), 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 32; ++i) s4[i & 3] += exp2_fast((v[i] - m) * kLog2e);
+        sum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
+        mx = m;
+    }
+    __device__ __forceinline__ void end(const GemmTile& t) {
+        if (t.row < p.T && t.col0 < p.V) p.part[static_cast<size_t>(t.col0 >> 7) * p.T + t.row] = make_float2(mx, sum);
+    }
+};
+
+// Backward epilogue of the logits: G / c in bf16, columns counted from the
+// piece's first word v0.
+struct GradTile {
+    struct Params {
+        CUtensorMap g;
+        const float* lse;
+        const float* dloss;
+        const float* cmax;
+        const long long* target;
+        long long ignore, v0;
+        int T, V;
+    };
+    static __device__ __forceinline__ void prefetch(const Params& p) { prefetch_tmap(&p.g); }
+    const Params& p;
+    float lse, d;
+    long long tcol;
+    __device__ __forceinline__ explicit GradTile(const Params& q) : p(q), lse(0.f), d(0.f), tcol(-1) {}
+    __device__ __forceinline__ void begin(const GemmTile& t) {
+        d = lse = 0.f;
+        tcol = -1;
+        if (t.row < p.T) {
+            const long long y = __ldg(p.target + t.row);
+            const float c = *p.cmax;
+            lse = __ldg(p.lse + t.row);
+            if (y != p.ignore && y >= 0 && y < p.V && c != 0.f) d = __fdiv_rn(__ldg(p.dloss + t.row), c);
+            tcol = y - p.v0 - t.col0;
+        }
+    }
+    __device__ __forceinline__ void slice(const GemmTile& t, int k, float (&v)[32]) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = exp2_fast((v[i] - lse) * kLog2e);
+        const long long tc = tcol - 32 * k;
+        if (tc >= 0 && tc < 32) {
+            const uint32_t hot = 1u << tc;  // by a bit: see LsePart
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] -= (hot & (1u << i)) ? 1.0f : 0.0f;
+        }
+        // a row without a target writes zeros, whatever its logits are
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = d == 0.f ? 0.f : v[i] * d;
+        put_bf16(t, k, v, &p.g);
+    }
+    __device__ __forceinline__ void end(const GemmTile&) {}
+};
+
+// fp32 tiles stored to, or added to, a matrix (dX over the pieces).
+struct SumF32 {
+    struct Params {
+        CUtensorMap out;
+        int add;
+    };
+    static __device__ __forceinline__ void prefetch(const Params& p) { prefetch_tmap(&p.out); }
+    const Params& p;
+    __device__ __forceinline__ explicit SumF32(const Params& q) : p(q) {}
+    __device__ __forceinline__ void begin(const GemmTile&) {}
+    __device__ __forceinline__ void slice(const GemmTile& t, int k, float (&v)[32]) {
+        box_wait(t.lane);
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            box_put(t.box, t.lane, c, __float_as_uint(v[4 * c]), __float_as_uint(v[4 * c + 1]),
+                    __float_as_uint(v[4 * c + 2]), __float_as_uint(v[4 * c + 3]));
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (t.lane == 0) {
+            if (p.add) tma_add_2d(&p.out, smem_u32(t.box), t.col0 + 32 * k, t.warp_row);
+            else tma_store_2d(&p.out, smem_u32(t.box), t.col0 + 32 * k, t.warp_row);
+        }
+    }
+    __device__ __forceinline__ void end(const GemmTile&) {}
+};
+
+// c times the tile, in bf16 (dW of a piece).
+struct ScaledBf16 {
+    struct Params {
+        CUtensorMap out;
+        const float* cmax;
+    };
+    static __device__ __forceinline__ void prefetch(const Params& p) { prefetch_tmap(&p.out); }
+    const Params& p;
+    float c;
+    __device__ __forceinline__ explicit ScaledBf16(const Params& q) : p(q), c(*q.cmax) {}
+    __device__ __forceinline__ void begin(const GemmTile&) {}
+    __device__ __forceinline__ void slice(const GemmTile& t, int k, float (&v)[32]) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] *= c;
+        put_bf16(t, k, v, &p.out);
+    }
+    __device__ __forceinline__ void end(const GemmTile&) {}
+};
+
+// Joins the P parts of 32 rows per block (lane = row, warp = every 32nd part),
+// in a fixed order.
+__global__ void __launch_bounds__(1024)
+    xent_merge_kernel(const float2* __restrict__ part, const float* __restrict__ tlogit,
+                      const long long* __restrict__ target, long long ignore, int T, int V, int P,
+                      float* __restrict__ loss, float* __restrict__ lse_out, unsigned* status) {
+    __shared__ float2 s[32][33];
+    asm volatile("griddepcontrol.launch_dependents;");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
+    const int t = blockIdx.x * 32 + lane;
+    float m = -INFINITY, sum = 0.f;
+    auto join = [&](float2 q) {
+        if (q.y == 0.f) return;  // no columns (a sum of exponentials has a term 1; NaN passes)
+        const float n = fmaxf(m, q.x);
+        sum = (sum == 0.f ? 0.f : sum * exp2_fast((m - n) * kLog2e)) + q.y * exp2_fast((q.x - n) * kLog2e);
+        m = n;
+    };
+    if (t < T)
+        for (int p = slice; p < P; p += 32) join(__ldg(part + static_cast<size_t>(p) * T + t));
+    s[slice][lane] = make_float2(m, sum);
+    __syncthreads();
+    if (slice != 0 || t >= T) return;
+    for (int i = 1; i < 32; ++i) join(s[i][lane]);
+    const float lse = m + logf(sum);
+    const long long y = target[t];
+    float l = 0.f;
+    if (y != ignore) {
+        if (y >= 0 && y < V) {
+            l = lse - tlogit[t];
+        } else {
+            raise_status(status, kStatusInvalid);
+            l = NAN;
+        }
+    }
+    loss[t] = l;
+    lse_out[t] = lse;
+}
+
+// c = max |dloss[t]| over the tokens that count (NaN if one is NaN).
+__global__ void __launch_bounds__(1024) xent_cmax_kernel(const float* __restrict__ dloss,
+                                                         const long long* __restrict__ target, long long ignore,
+                                                         int T, float* __restrict__ cmax) {
+    __shared__ unsigned s[32];
+    asm volatile("griddepcontrol.launch_dependents;");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    unsigned m = 0;  // magnitudes order like their bits
+    for (int t = threadIdx.x; t < T; t += 1024)
+        if (target[t] != ignore) m = max(m, __float_as_uint(dloss[t]) & 0x7FFFFFFFu);
+    m = __reduce_max_sync(0xFFFFFFFFu, m);
+    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = m;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        m = __reduce_max_sync(0xFFFFFFFFu, s[threadIdx.x]);
+        if (threadIdx.x == 0) *cmax = __uint_as_float(m);
+    }
+}
+
+// dX = c * (the fp32 sums over the pieces), in bf16; 8 elements per thread.
+__global__ void __launch_bounds__(256) xent_dx_kernel(const float* __restrict__ sums, const float* __restrict__ cmax,
+                                                      long long n8, uint16_t* __restrict__ dx) {
+    asm volatile("griddepcontrol.launch_dependents;");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const float c = *cmax;
+    for (long long i = blockIdx.x * 256ll + threadIdx.x; i < n8; i += gridDim.x * 256ll) {
+        const float4 a = reinterpret_cast<const float4*>(sums)[2 * i], b = reinterpret_cast<const float4*>(sums)[2 * i + 1];
+        reinterpret_cast<uint4*>(dx)[i] = make_uint4(pack_bf16(a.x * c, a.y * c), pack_bf16(a.z * c, a.w * c),
+                                                     pack_bf16(b.x * c, b.y * c), pack_bf16(b.z * c, b.w * c));
+    }
+}
+
+size_t round256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
+int parts(long long V) { return static_cast<int>((V + 127) / 128); }
+
+// Words per piece of the backward.
+long long piece_words(long long T, long long V) {
+    const long long most = (64ll << 20) / (T < 256 ? 256 : T);  // entries of G
+    long long w = most / 256 * 256;
+    if (w < 2048) w = 2048;
+    const long long all = (V + 255) / 256 * 256;
+    return w < all ? w : all;
+}
+
+}  // namespace
+
+size_t xent_workspace_bytes(long long T, long long V) {
+    return round256(static_cast<size_t>(parts(V)) * T * sizeof(float2)) + round256(static_cast<size_t>(T) * sizeof(float));
+}
+
+size_t xent_backward_workspace_bytes(long long T, long long D, long long V, int need_dx) {
+    return 256 + (need_dx ? round256(static_cast<size_t>(T) * D * sizeof(float)) : 0) +
+           round256(static_cast<size_t>(T) * piece_words(T, V) * 2);
+}
+
+cudaError_t launch_xent(const uint16_t* x, long long T, long long D, const uint16_t* w, long long V,
+                        const long long* target, long long ignore, float* loss, float* lse, void* ws, unsigned* status,
+                        cudaStream_t st) {
+    float2* part = static_cast<float2*>(ws);
+    float* tlogit = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) +
+                                             round256(static_cast<size_t>(parts(V)) * T * sizeof(float2)));
+    CUtensorMap a, b;
+    if (!gemm_operand(&a, false, false, x, T, D, D) || !gemm_operand(&b, false, false, w, V, D, D))
+        return cudaErrorInvalidValue;
+    const LsePart::Params p{part, tlogit, target, static_cast<int>(T), static_cast<int>(V)};
+    const GemmShape shape{static_cast<int>(T), static_cast<int>(V), static_cast<int>(D), 0, 8};
+    if (cudaError_t e = launch_gemm_f16<LsePart, 1, false, false, false, kLogitSegment>(a, b, p, shape, status, st)) return e;
+    return pdl_launch(xent_merge_kernel, dim3(static_cast<unsigned>((T + 31) / 32)), dim3(1024), 0, st,
+                      static_cast<const float2*>(part), static_cast<const float*>(tlogit), target, ignore,
+                      static_cast<int>(T), static_cast<int>(V), parts(V), loss, lse, status);
+}
+
+cudaError_t launch_xent_backward(const float* dloss, const uint16_t* x, long long T, long long D, const uint16_t* w,
+                                 long long V, const long long* target, long long ignore, const float* lse, uint16_t* dx,
+                                 uint16_t* dw, void* ws, unsigned* status, int num_sms, cudaStream_t st) {
+    uint8_t* at = static_cast<uint8_t*>(ws);
+    float* cmax = reinterpret_cast<float*>(at);
+    at += 256;
+    float* dx32 = nullptr;
+    if (dx) {
+        dx32 = reinterpret_cast<float*>(at);
+        at += round256(static_cast<size_t>(T) * D * sizeof(float));
+    }
+    uint16_t* g = reinterpret_cast<uint16_t*>(at);
+    const long long piece = piece_words(T, V);
+    cudaError_t e = pdl_launch(xent_cmax_kernel, dim3(1), dim3(1024), 0, st, dloss, target, ignore, static_cast<int>(T), cmax);
+    const int Ti = static_cast<int>(T), Di = static_cast<int>(D);
+    const int d_tiles = (Di + gm::BN - 1) / gm::BN;
+    for (long long v0 = 0; v0 < V && e == cudaSuccess; v0 += piece) {
+        const long long n = V - v0 < piece ? V - v0 : piece;
+        const int ni = static_cast<int>(n);
+        const uint16_t* wp = w + v0 * D;
+        CUtensorMap xk, wk;
+        GradTile::Params gp;
+        if (!gemm_operand(&xk, false, false, x, T, D, D) || !gemm_operand(&wk, false, false, wp, n, D, D) ||
+            !gemm_map(&gp.g, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, g, T, n, piece * 2, 64, 32))
+            return cudaErrorInvalidValue;
+        gp.lse = lse;
+        gp.dloss = dloss;
+        gp.cmax = cmax;
+        gp.target = target;
+        gp.ignore = ignore;
+        gp.v0 = v0;
+        gp.T = Ti;
+        gp.V = static_cast<int>(V);
+        e = launch_gemm_f16<GradTile, 1, false, false, false, 0>(xk, wk, gp, GemmShape{Ti, ni, Di, 0, 8}, status, st);
+        if (e != cudaSuccess) return e;
+        if (dx) {
+            CUtensorMap gk, wn;
+            SumF32::Params sp;
+            sp.add = v0 > 0;
+            if (!gemm_operand(&gk, false, false, g, T, n, piece) || !gemm_operand(&wn, false, true, wp, n, D, D) ||
+                !gemm_map(&sp.out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, dx32, T, D, D * 4, 32, 32))
+                return cudaErrorInvalidValue;
+            e = launch_gemm_f16<SumF32, 1, false, true, false, 0>(gk, wn, sp, GemmShape{Ti, Di, ni, 0, d_tiles}, status, st);
+            if (e != cudaSuccess) return e;
+        }
+        if (dw) {
+            CUtensorMap gm_, xn;
+            ScaledBf16::Params bp;
+            bp.cmax = cmax;
+            if (!gemm_operand(&gm_, false, true, g, T, n, piece) || !gemm_operand(&xn, false, true, x, T, D, D) ||
+                !gemm_map(&bp.out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dw + v0 * D, n, D, D * 2, 64, 32))
+                return cudaErrorInvalidValue;
+            e = launch_gemm_f16<ScaledBf16, 1, true, true, false, 0>(gm_, xn, bp, GemmShape{ni, Di, Ti, 0, d_tiles}, status, st);
+        }
+    }
+    if (e == cudaSuccess && dx) {
+        const long long n8 = T * D / 8, blocks = (n8 + 255) / 256, most = 8ll * num_sms;
+        e = pdl_launch(xent_dx_kernel, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), dim3(256), 0, st,
+                       static_cast<const float*>(dx32), static_cast<const float*>(cmax), n8, dx);
+    }
+    return e;
+}
+
+}  // namespace sbl

@@ -84,3 +84,52 @@ def test_norm_tensor_checks(rec):
     for f in bad:
         with pytest.raises(ValueError):
             f()
+
+
+def test_cross_entropy_rejects_on_host():
+    from sparse_linear_layers_b200._lib import lib
+    p, big = 4096, 1 << 40
+    F = lib.sbl_linear_cross_entropy
+    assert F(None, 0, 64, None, 100, None, -100, None, None, None, 0, None) == 0      # T == 0
+    assert F(p, 4, 40, p, 100, p, -100, p, p, p, big, None) == 1                      # D % 16 != 0
+    assert F(p, -1, 64, p, 100, p, -100, p, p, p, big, None) == 1
+    assert F(p, 4, 64, p, 0, p, -100, p, p, p, big, None) == 1                        # no words
+    assert F(p, 4, 64, p, 1 << 25, p, -100, p, p, p, big, None) == 2
+    assert F(p, 1 << 25, 64, p, 100, p, -100, p, p, p, big, None) == 2
+    assert F(p, 4, 64, None, 100, p, -100, p, p, p, big, None) == 1                   # missing W
+    assert F(p + 8, 4, 64, p, 100, p, -100, p, p, p, big, None) == 1                  # unaligned x
+    assert F(p, 4, 64, p, 100, p, -100, p, p, None, big, None) == 6
+    assert F(p, 4, 64, p, 100, p, -100, p, p, p + 16, big, None) == 6
+    need = lib.sbl_linear_cross_entropy_workspace_bytes(4, 100)
+    assert need == 256 + 256 and F(p, 4, 64, p, 100, p, -100, p, p, p, need - 1, None) == 6
+    B = lib.sbl_linear_cross_entropy_backward
+    assert B(p, p, 4, 64, p, 100, p, -100, p, None, None, p, big, None) == 1          # no output
+    assert B(p, p, 4, 64, p, 100, p, -100, p, p + 4, None, p, big, None) == 1         # unaligned dx
+    assert B(p, p, 4, 64, p, 100, p, -100, None, p, None, p, big, None) == 1          # no lse
+    assert B(None, p, 4, 64, p, 100, p, -100, p, p, None, p, big, None) == 1          # no dloss
+    need = lib.sbl_linear_cross_entropy_backward_workspace_bytes(4, 64, 100, 1)
+    assert B(p, p, 4, 64, p, 100, p, -100, p, p, None, p, need - 1, None) == 6
+    assert lib.sbl_linear_cross_entropy_backward_workspace_bytes(4, 64, 100, 0) == need - 4 * 64 * 4
+    # the piece of the vocabulary is bounded: G never approaches [T, V]
+    assert lib.sbl_linear_cross_entropy_backward_workspace_bytes(8192, 896, 128000, 0) <= (128 << 20) + 256
+
+
+def test_cross_entropy_tensor_checks(rec):
+    x, w, t = torch.zeros(4, 64).bfloat16(), torch.zeros(100, 64).bfloat16(), torch.zeros(4, dtype=torch.int64)
+    f = torch.zeros(4)
+    rec.sbl_linear_cross_entropy_workspace_bytes = lambda *a: 16
+    rec.sbl_linear_cross_entropy_backward_workspace_bytes = lambda *a: 16
+    api.sbl_linear_cross_entropy(x, w, t)
+    api.sbl_linear_cross_entropy_backward(f, x, w, t, f)
+    assert rec.calls == ["sbl_linear_cross_entropy", "sbl_linear_cross_entropy_backward"]
+    bad = [lambda: api.sbl_linear_cross_entropy(x.float(), w, t), lambda: api.sbl_linear_cross_entropy(x, w.float(), t),
+           lambda: api.sbl_linear_cross_entropy(x, w[:, :32], t), lambda: api.sbl_linear_cross_entropy(x, w, t.int()),
+           lambda: api.sbl_linear_cross_entropy(x, w, t[:3]), lambda: api.sbl_linear_cross_entropy(x[0], w, t),
+           lambda: api.sbl_linear_cross_entropy(x, w.t().contiguous().t(), t),
+           lambda: api.sbl_linear_cross_entropy_backward(f[:3], x, w, t, f),
+           lambda: api.sbl_linear_cross_entropy_backward(f.double(), x, w, t, f),
+           lambda: api.sbl_linear_cross_entropy_backward(f, x, w, t, f[:2]),
+           lambda: api.sbl_linear_cross_entropy_backward(f, x, w, t, f, need_dx=False, need_dw=False)]
+    for g in bad:
+        with pytest.raises(ValueError):
+            g()
