@@ -311,6 +311,61 @@ sbl_status sbl_linear_backward_ws(const float* dY, int64_t T, int64_t O, const i
                                   int64_t K, const uint8_t* packed, const float* row_scale, float* dX, float* dW,
                                   int flags, void* workspace, size_t workspace_bytes, void* stream);
 
+/* Activations of the gated feed-forward block. */
+enum { SBL_ACT_SILU = 0, SBL_ACT_RELU2 = 1 };
+
+/*
+ * sbl_ffn_gated — the gated feed-forward block on prepared weights:
+ *   h[t, f] = act(g[t, f]) * u[t, f], g and u what sbl_linear gives in fp32 on
+ *   the gate and the up matrix (Sparse-BitNet Guide, "Mathematical Formulation
+ *   of Sparse-BitLinear"), act SiLU (g * sigmoid(g)) or max(g, 0)^2.  Both
+ *   products, the activation and the product of the two in one kernel: neither
+ *   g nor u is written.  sbl_linear on h with the down matrix completes the block.
+ *
+ *   x_bf16    bf16 bit patterns [T, K].
+ *   packed_gate, scale_gate, packed_up, scale_up
+ *             the two prepared matrices, uint8 [F, K/4] and fp32 [F] each, one
+ *             N:M pattern (n, m).
+ *   h         [T, F] (output), fp32 (SBL_F32) or bf16 (SBL_BF16, rounded once).
+ *   workspace sbl_ffn_gated_workspace_bytes(T, K, F) bytes, 256-byte aligned;
+ *             0 bytes (NULL allowed) for up to 16 tokens.  Calls that share it
+ *             must be ordered on one stream.
+ * Any T, F >= 0 and K % 16 == 0 (F, T up to 2^24, K up to 2^17, else
+ * SBL_ERR_UNSUPPORTED).  Non-finite x sets SBL_ERR_NONFINITE in the device
+ * status word.  Asynchronous on `stream`.
+ */
+size_t sbl_ffn_gated_workspace_bytes(int64_t T, int64_t K, int64_t F);
+sbl_status sbl_ffn_gated(const uint16_t* x_bf16, int64_t T, int64_t K, const uint8_t* packed_gate,
+                         const float* scale_gate, const uint8_t* packed_up, const float* scale_up, int64_t F, int n,
+                         int m, int act, void* h, int h_dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * sbl_ffn_gated_backward — the straight-through gradients of sbl_ffn_gated
+ * (every quantiser the identity, as sbl_linear_backward):
+ *   dg = dh * u * act'(g), du = dh * act(g),
+ *   dX = (dg * scale_gate) . W_gate + (du * scale_up) . W_up,
+ *   dW_gate = dg^T . (x_q / s_tok), dW_up = du^T . (x_q / s_tok);
+ *   with SBL_BWD_DW_TERNARY the rows of both times their row scale once more.
+ * Nothing of the forward is kept but x: g and u are computed again.
+ *
+ *   dh        fp32 [T, F], finite: gradient with respect to h.
+ *   dX        fp32 [T, K]; dW_gate, dW_up fp32 [F, K] (outputs), each may be
+ *             NULL, not all; overwritten (zeros for empty sums).
+ *   workspace sbl_ffn_gated_backward_workspace_bytes(T, K, F, dX != NULL,
+ *             dW_gate != NULL || dW_up != NULL) bytes, 256-byte aligned
+ *             (about 16 bytes per token and hidden unit).
+ * Tensor-core sums of fp16 parts, fp32 accumulation: with v = (dg | du) * scale /
+ * s_tok, each output is within (n / 128 + 80) * 2^-24 * sum |terms| of the sum
+ * over these fp32 v (n the reduction length, 2 F or T), plus 2^-38 of the
+ * largest |v| of each token times what it multiplies.  The same inputs give the same bits.  Other arguments, limits
+ * and errors as the forward.
+ */
+size_t sbl_ffn_gated_backward_workspace_bytes(int64_t T, int64_t K, int64_t F, int need_dx, int need_dw);
+sbl_status sbl_ffn_gated_backward(const float* dh, const uint16_t* x_bf16, int64_t T, int64_t K,
+                                  const uint8_t* packed_gate, const float* scale_gate, const uint8_t* packed_up,
+                                  const float* scale_up, int64_t F, int n, int m, int act, float* dX, float* dW_gate,
+                                  float* dW_up, int flags, void* workspace, size_t workspace_bytes, void* stream);
+
 /*
  * sbl_linear_cross_entropy — softmax cross entropy of a vocabulary projection
  * (the LM head's loss of a training or scoring pass), per token, without

@@ -25,6 +25,9 @@ SBL_PREP_SCALE_GLOBAL = 2
 
 SBL_BWD_DW_TERNARY = 1
 
+SBL_ACT_SILU = 0
+SBL_ACT_RELU2 = 1
+
 SBL_NORM_RMS = 0
 SBL_NORM_LAYER = 1
 
@@ -65,6 +68,11 @@ SIGNATURES = {
     "sbl_norm": (_int, [_vp, _int, _i64, _i64, _int, _vp, _vp, _f32, _vp, _vp, _vp, _vp]),
     "sbl_norm_backward_workspace_bytes": (_sz, [_i64, _i64, _int]),
     "sbl_norm_backward": (_int, [_vp, _vp, _int, _i64, _i64, _int, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "sbl_ffn_gated_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "sbl_ffn_gated": (_int, [_vp, _i64, _i64, _vp, _vp, _vp, _vp, _i64, _int, _int, _int, _vp, _int, _vp, _sz, _vp]),
+    "sbl_ffn_gated_backward_workspace_bytes": (_sz, [_i64, _i64, _i64, _int, _int]),
+    "sbl_ffn_gated_backward": (_int, [_vp, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _i64, _int, _int, _int, _vp, _vp, _vp,
+                                      _int, _vp, _sz, _vp]),
     "sbl_linear_cross_entropy_workspace_bytes": (_sz, [_i64, _i64]),
     "sbl_linear_cross_entropy": (_int, [_vp, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _sz, _vp]),
     "sbl_linear_cross_entropy_backward_workspace_bytes": (_sz, [_i64, _i64, _i64, _int]),

@@ -549,6 +549,76 @@ def sbl_linear_backward(dY: torch.Tensor, x_q: torch.Tensor, s_tok: torch.Tensor
     return (dX if need_dx else None), (dW if need_dw else None)
 
 
+_ACTS = {"silu": _lib.SBL_ACT_SILU, "relu2": _lib.SBL_ACT_RELU2}
+
+
+def _need_ffn(x: torch.Tensor, gate: PreparedWeights, up: PreparedWeights, act: str):
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {sorted(_ACTS)}, got {act!r}")
+    T, K = _need_2d(x, "x")
+    _need_cuda(x, "x", torch.bfloat16)
+    for w in (gate, up):
+        if w.K != K or w.O != gate.O or (w.n, w.m) != (gate.n, gate.m):
+            raise ValueError("gate and up must have the activations' K, one number of rows and one N:M pattern")
+        _need_weights(w, x.device)
+    return T, K, gate.O
+
+
+def sbl_ffn_gated_workspace_bytes(T: int, K: int, F: int) -> int:
+    return int(lib.sbl_ffn_gated_workspace_bytes(T, K, F))
+
+
+def sbl_ffn_gated(x: torch.Tensor, gate: PreparedWeights, up: PreparedWeights, act: str = "silu",
+                  out_dtype: torch.dtype = torch.float32, h: Optional[torch.Tensor] = None,
+                  workspace: Optional[torch.Tensor] = None,
+                  stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """The gated feed-forward block h = act(gate(x)) * up(x), [T,F] fp32 or bf16, on
+    two prepared matrices of one shape; ``act`` is "silu" or "relu2" (max(g, 0)^2)."""
+    T, K, F = _need_ffn(x, gate, up, act)
+    with _LaunchOn(x.device, stream) as st:
+        if h is None:
+            h = torch.empty((T, F), dtype=out_dtype, device=x.device)
+        if h.dtype not in _DTYPES:
+            raise ValueError("h must be float32 or bfloat16")
+        _need_cuda(h, "h", h.dtype, (T, F), x.device)
+        need = sbl_ffn_gated_workspace_bytes(T, K, F)
+        ws = _scratch(need, workspace, x.device) if need or workspace is not None else None
+        check(lib.sbl_ffn_gated(x.data_ptr(), T, K, gate.packed.data_ptr(), gate.row_scale.data_ptr(),
+                                up.packed.data_ptr(), up.row_scale.data_ptr(), F, gate.n, gate.m, _ACTS[act],
+                                h.data_ptr(), _DTYPES[h.dtype], _ptr(ws), ws.numel() if ws is not None else 0, st),
+              "sbl_ffn_gated")
+    return h
+
+
+def sbl_ffn_gated_backward_workspace_bytes(T: int, K: int, F: int, need_dx: bool = True, need_dw: bool = True) -> int:
+    return int(lib.sbl_ffn_gated_backward_workspace_bytes(T, K, F, int(need_dx), int(need_dw)))
+
+
+def sbl_ffn_gated_backward(dh: torch.Tensor, x: torch.Tensor, gate: PreparedWeights, up: PreparedWeights,
+                           act: str = "silu", need_dx: bool = True, need_dgate: bool = True, need_dup: bool = True,
+                           dw_ternary: bool = False, workspace: Optional[torch.Tensor] = None,
+                           stream: Optional[torch.cuda.Stream] = None):
+    """Straight-through gradients of sbl_ffn_gated from dh (fp32 [T,F]) and the
+    forward's x: (dX fp32 [T,K], dW_gate, dW_up fp32 [F,K]), None for the ones not
+    asked for.  ``dw_ternary`` as for sbl_linear_backward."""
+    T, K, F = _need_ffn(x, gate, up, act)
+    dev = x.device
+    _need_cuda(dh, "dh", torch.float32, (T, F), dev)
+    if not (need_dx or need_dgate or need_dup):
+        raise ValueError("ask for dX, dW_gate or dW_up")
+    with _LaunchOn(dev, stream) as st:
+        dx = torch.empty((T, K), dtype=torch.float32, device=dev) if need_dx else None
+        dg = torch.empty((F, K), dtype=torch.float32, device=dev) if need_dgate else None
+        du = torch.empty((F, K), dtype=torch.float32, device=dev) if need_dup else None
+        ws = _scratch(sbl_ffn_gated_backward_workspace_bytes(T, K, F, need_dx, need_dgate or need_dup), workspace, dev)
+        check(lib.sbl_ffn_gated_backward(dh.data_ptr(), x.data_ptr(), T, K, gate.packed.data_ptr(),
+                                         gate.row_scale.data_ptr(), up.packed.data_ptr(), up.row_scale.data_ptr(), F,
+                                         gate.n, gate.m, _ACTS[act], _ptr(dx), _ptr(dg), _ptr(du),
+                                         _lib.SBL_BWD_DW_TERNARY if dw_ternary else 0, ws.data_ptr(), ws.numel(), st),
+              "sbl_ffn_gated_backward")
+    return dx, dg, du
+
+
 def sbl_linear_cross_entropy_workspace_bytes(T: int, V: int) -> int:
     return int(lib.sbl_linear_cross_entropy_workspace_bytes(T, V))
 

@@ -1,0 +1,1125 @@
+// The gated feed-forward block on prepared ternary weights:
+//
+//   g[t, f] = acc_g * scale_g[f] / s_t,  u[t, f] = acc_u * scale_u[f] / s_t,  h = act(g) * u
+//
+// with acc = x_q . W_t^T the integer products of the Sparse-BitNet Guide's
+// linear-evaluation equation ("Mathematical Formulation of Sparse-BitLinear")
+// for the gate and the up matrix, act SiLU (g * sigmoid(g)) or the squared
+// ReLU, and its straight-through backward (the Guide's "Training Stability &
+// The Straight-Through Estimator"):
+//
+//   dg = dh * u * act'(g),  du = dh * act(g)
+//   dX = (dg * scale_g) . W_g + (du * scale_u) . W_u
+//   dW_g = dg^T . (x_q / s),  dW_u = du^T . (x_q / s)
+//
+// Forward, up to 16 tokens: ffn_decode_kernel streams the 2-bit codes of both
+// matrices once (bound by launch latency, then HBM).  A 16-row MMA tile holds
+// 8 rows of each matrix, so one thread ends with g and u of the same element.
+//
+// Forward, more tokens: ffn_pair_kernel, the 2-SM int8 tensor-core GEMM with
+// a 256-token x (128 gate + 128 up)-row tile.  CTA rank 0 expands the gate
+// rows, rank 1 the up rows; both hold, for their 128 tokens, g in TMEM columns
+// 0-127 and u in columns 128-255, and the epilogue multiplies them.  Neither g
+// nor u is written.  Bound by the tensor cores at large K; at K = 896 by the
+// epilogue's instructions.
+//
+// Backward: nothing is kept from the forward but x; the same kernel computes
+// g and u again and its epilogue writes v = (dg | du) * scale / s_t in fp32 and
+// each token's largest |v| (atomic maximum: no order to depend on).  Both
+// gradients are then products of v with exact factors:
+//   dX[t] = s_t * sum_f v[t, f] * W_t[f],  dW[f] = (1 / scale[f]) * sum_t v[t, f] * x_q[t].
+// ffn_operands_kernel splits v, scaled by a power of two 2^-er[t] that brings
+// the token's largest value to [2^14, 2^15), into two fp16 parts (11 + 11
+// significant bits; what they drop is at most 2^-22 of v plus 2^-39 of the
+// token's largest |v|), writes the codes as fp16, and x_q * 2^(er[t] - max er + 8) as fp16
+// (exact down to 2^-32 of the largest token).  Two GEMMs on those (gemm_f16.cuh, fp16
+// operands, both parts summed, segments of 4 k-blocks promoted to
+// round-to-nearest sums) give dX and dW.  Two parts instead of three bf16 ones
+// save a third of the tensor work that bounds this.
+#include <cuda.h>
+#include <cuda_fp16.h>
+
+#include <cstring>
+#include <type_traits>
+
+#include "gemm_f16.cuh"
+#include "sbl_common.cuh"
+#include "tc_util.cuh"
+
+namespace sbl {
+
+constexpr int kLayoutPairsFfn = 1;  // launch_quant's pairing order
+cudaError_t launch_quant(const uint16_t* x, long long T, long long K, int8_t* xq, float* s_tok, int layout,
+                         unsigned* status, cudaStream_t stream, void* zero16, long long nzero16);
+
+namespace {
+
+constexpr int kActSilu = 0;
+
+template <int ACT>
+__device__ __forceinline__ float act_value(float g) {
+    if (ACT == kActSilu) return __fdividef(g, 1.0f + __expf(-g));
+    const float r = fmaxf(g, 0.0f);
+    return r * r;
+}
+
+// act(g) and act'(g)
+template <int ACT>
+__device__ __forceinline__ void act_both(float g, float& a, float& da) {
+    if (ACT == kActSilu) {
+        const float s = __fdividef(1.0f, 1.0f + __expf(-g));
+        a = g * s;
+        da = s * fmaf(g, 1.0f - s, 1.0f);
+    } else {
+        const float r = fmaxf(g, 0.0f);
+        a = r * r;
+        da = 2.0f * r;
+    }
+}
+
+// ---------------------------------------------------------------- a few tokens
+namespace fd {
+constexpr int THREADS = 512;
+constexpr int WARPS = THREADS / 32;
+constexpr int MAX_TOKENS = 16;
+__host__ __device__ inline int pad64(int K) { return (K + 63) / 64 * 64; }
+// one token's activations: 64 mod 128 bytes apart, so two tokens of a
+// quarter-warp read disjoint banks
+__host__ __device__ inline int stride(int K) { return pad64(K) % 128 == 64 ? pad64(K) : pad64(K) + 64; }
+inline size_t smem_bytes(int K, int tokens) {
+    return static_cast<size_t>(tokens) * stride(K) + static_cast<size_t>(WARPS) * 32 * 4 * (tokens > 8 ? 2 : 1) * 4;
+}
+}  // namespace fd
+
+__device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                       uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// CW code words of a row from word w0 on, zeros past the row's end.
+template <int CW>
+__device__ __forceinline__ void load_codes(const uint8_t* row, int w0, int words, bool ok, uint32_t (&w)[CW]) {
+    if (!ok || w0 >= words) {  // CW > 1 only where CW divides the row's words
+#pragma unroll
+        for (int i = 0; i < CW; ++i) w[i] = 0u;
+        return;
+    }
+    const uint8_t* p = row + 4 * static_cast<size_t>(w0);
+    if constexpr (CW == 4) {
+        const uint4 v = ldg_stream(p);
+        w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+    } else if constexpr (CW == 2) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+        w[0] = v.x; w[1] = v.y;
+    } else {
+        w[0] = __ldg(reinterpret_cast<const unsigned int*>(p));
+    }
+}
+
+// A warp owns 8 rows f of both matrices and a slice of their chunks (64 * CW
+// weights); KS warps of a block share a tile and add their int32 partials in
+// shared memory.  NT: tiles of 8 tokens.
+template <int NT, int CW, int ACT>
+__global__ void __launch_bounds__(fd::THREADS, 1)
+    ffn_decode_kernel(const uint8_t* __restrict__ pg, const float* __restrict__ scale_g, const uint8_t* __restrict__ pu,
+                      const float* __restrict__ scale_u, int F, int K, const uint16_t* __restrict__ x, int t0, int TP,
+                      int KS, void* __restrict__ h, int h_bf16, unsigned* status) {
+    extern __shared__ __align__(16) uint8_t fd_smem[];
+    __shared__ uint32_t red_max[fd::WARPS];
+    __shared__ float s_sh[fd::MAX_TOKENS];
+    asm volatile("griddepcontrol.launch_dependents;");
+    const int S = fd::stride(K);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int gq = lane >> 2, tg = lane & 3;
+    const int words = K >> 4;
+    const int C = fd::pad64(K) / (64 * CW);
+    const int ks = warp % KS;
+    const int f = (blockIdx.x * (fd::WARPS / KS) + warp / KS) * 8 + gq;
+    const bool ok = f < F;
+    const size_t rowb = static_cast<size_t>(K) >> 2;
+    const uint8_t* const rg = pg + static_cast<size_t>(ok ? f : 0) * rowb;
+    const uint8_t* const ru = pu + static_cast<size_t>(ok ? f : 0) * rowb;
+    const int nck = ks < C ? (C - ks + KS - 1) / KS : 0;
+    auto word0 = [&](int j) { return ((ks + j * KS) * 4 + tg) * CW; };  // first code word of this thread's chunk j
+
+    // before the dependency wait: pull this warp's weights into L2
+    for (int j = 0; j < nck; ++j)
+        if (ok && word0(j) < words) {
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(rg + 4 * static_cast<size_t>(word0(j))));
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(ru + 4 * static_cast<size_t>(word0(j))));
+        }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    constexpr int NB = CW == 4 ? 2 : 4;  // chunks loaded together
+    uint32_t wg[NB][CW], wu[NB][CW];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        load_codes<CW>(rg, word0(b), words, ok && b < nck, wg[b]);
+        load_codes<CW>(ru, word0(b), words, ok && b < nck, wu[b]);
+    }
+    const float sg = ok ? __ldg(scale_g + f) : 0.f, su = ok ? __ldg(scale_u + f) : 0.f;
+
+    // quantise the pass's TP tokens, 16 / TP warps each, into the slots that
+    // the B fragments are read from
+    auto pos = [](int blk) {
+        const int c = blk / (4 * CW), l = blk % (4 * CW);
+        return c * 4 * CW + (l % CW) * 4 + l / CW;
+    };
+    {
+        const int wpt = fd::WARPS / TP;
+        const int qt = warp / wpt;
+        const bool qw = qt < TP;
+        const int qj = (warp - qt * wpt) * 32 + lane, nthr = wpt * 32;
+        const uint4* const xr = reinterpret_cast<const uint4*>(x + static_cast<size_t>(t0 + (qw ? qt : 0)) * K);
+        constexpr int XB = 4;  // 16-element blocks kept in registers
+        uint4 xa[XB][2];
+        uint32_t mx = 0;
+        if (qw) {
+#pragma unroll
+            for (int i = 0; i < XB; ++i) {
+                const int b = qj + i * nthr;
+                if (b < words) {
+                    xa[i][0] = ldg_nc(xr + 2 * b);
+                    xa[i][1] = ldg_nc(xr + 2 * b + 1);
+                    mx = absmax8(xa[i][1], absmax8(xa[i][0], mx));
+                }
+            }
+            for (int b = qj + XB * nthr; b < words; b += nthr)
+                mx = absmax8(ldg_nc(xr + 2 * b + 1), absmax8(ldg_nc(xr + 2 * b), mx));
+        }
+        mx = __reduce_max_sync(0xFFFFFFFFu, mx);
+        if (lane == 0) red_max[warp] = mx;
+        __syncthreads();
+        if (threadIdx.x < TP) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int w = 0; w < fd::WARPS; ++w)
+                if (w / wpt == static_cast<int>(threadIdx.x)) m = max(m, red_max[w]);
+            if (m >= 0x7F80u && blockIdx.x == 0) raise_status(status, kStatusNonfinite);
+            s_sh[threadIdx.x] = __fdiv_rn(127.0f, fmaxf(__uint_as_float(m << 16), 1e-5f));
+        }
+        __syncthreads();
+        if (qw) {
+            const float st = s_sh[qt];
+            uint4* const xt = reinterpret_cast<uint4*>(fd_smem + static_cast<size_t>(qt) * S);
+#pragma unroll
+            for (int i = 0; i < XB; ++i) {
+                const int b = qj + i * nthr;
+                if (b < words) xt[pos(b)] = quant_block16_pairs(xa[i][0], xa[i][1], st);
+            }
+            for (int b = qj + XB * nthr; b < words; b += nthr)
+                xt[pos(b)] = quant_block16_pairs(ldg_nc(xr + 2 * b), ldg_nc(xr + 2 * b + 1), st);
+        }
+        __syncthreads();
+    }
+
+    int acc[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[nt][r] = 0;
+    for (int j0 = 0; j0 < nck; j0 += NB) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            if (j0 + b >= nck) break;
+            const int c = ks + (j0 + b) * KS;
+#pragma unroll
+            for (int i = 0; i < CW; ++i) {
+                uint32_t eg[4], eu[4];
+                expand_pairs(wg[b][i], eg);
+                expand_pairs(wu[b][i], eu);
+                // slots past the row's end hold anything: their codes are zero
+                const int unit = c * 4 * CW + i * 4 + tg;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const int tok = nt * 8 + gq;
+                    uint4 xv = make_uint4(0u, 0u, 0u, 0u);
+                    if (tok < TP) xv = reinterpret_cast<const uint4*>(fd_smem + static_cast<size_t>(tok) * S)[unit];
+                    mma_s8(acc[nt], eg[0], eu[0], eg[1], eu[1], xv.x, xv.y);
+                    mma_s8(acc[nt], eg[2], eu[2], eg[3], eu[3], xv.z, xv.w);
+                }
+            }
+        }
+        if (j0 + NB < nck) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const int j = j0 + NB + b;
+                load_codes<CW>(rg, word0(j), words, ok && j < nck, wg[b]);
+                load_codes<CW>(ru, word0(j), words, ok && j < nck, wu[b]);
+            }
+        }
+    }
+    if (KS > 1) {
+        int* const red = reinterpret_cast<int*>(fd_smem + static_cast<size_t>(TP) * S);
+        if (ks != 0) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) red[(warp * 4 * NT + nt * 4 + r) * 32 + lane] = acc[nt][r];
+        }
+        __syncthreads();
+        if (ks == 0) {
+            for (int k2 = 1; k2 < KS; ++k2)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) acc[nt][r] += red[((warp + k2) * 4 * NT + nt * 4 + r) * 32 + lane];
+        }
+    }
+    if (ks != 0 || !ok) return;
+    // this thread: row f of both matrices, tokens 2 tg and 2 tg + 1 of each tile of 8
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int tok = nt * 8 + 2 * tg + e;
+            if (tok >= TP) continue;
+            const float st = s_sh[tok];
+            const float g = __fdiv_rn(__fmul_rn(static_cast<float>(acc[nt][e]), sg), st);
+            const float u = __fdiv_rn(__fmul_rn(static_cast<float>(acc[nt][2 + e]), su), st);
+            const float v = act_value<ACT>(g) * u;
+            const size_t at = static_cast<size_t>(t0 + tok) * F + f;
+            if (h_bf16) reinterpret_cast<__nv_bfloat16*>(h)[at] = __float2bfloat16_rn(v);
+            else reinterpret_cast<float*>(h)[at] = v;
+        }
+    }
+}
+
+// ---------------------------------------------------------------- many tokens
+namespace fp {
+constexpr int BM = 128;              // tokens per CTA (pair: 256)
+constexpr int BF = 128;              // hidden units per tile
+constexpr int BN = 2 * BF;           // accumulator columns: gate, then up
+constexpr int BK = 128;              // k per stage (bytes of int8)
+constexpr int A_BYTES = BM * BK;
+constexpr int B_BYTES = BF * BK;
+constexpr int P_BYTES = BF * BK / 4;
+constexpr int EPI_WARPS = 8;
+constexpr int DEC_WARPS = BF / 32;
+constexpr int WARP_TMA = EPI_WARPS + DEC_WARPS;
+constexpr int WARP_MMA = WARP_TMA + 1;
+constexpr int THREADS = (WARP_MMA + 1) * 32;
+constexpr int BOX = 32 * 128;
+constexpr int stages(bool bwd) { return bwd ? 4 : 5; }
+constexpr int boxes(bool bwd) { return bwd ? 2 : 1; }
+}  // namespace fp
+
+template <bool BWD>
+struct FfnSmem {
+    uint8_t a[fp::stages(BWD)][fp::A_BYTES];  // 1024-byte aligned tiles
+    uint8_t b[fp::stages(BWD)][fp::B_BYTES];
+    uint8_t box[fp::EPI_WARPS][fp::boxes(BWD)][fp::BOX];
+    uint8_t p[fp::stages(BWD)][fp::P_BYTES];
+    float scale[fp::EPI_WARPS][2][fp::BF / 2];
+    uint64_t full_a[fp::stages(BWD)];         // used in the even CTA
+    uint64_t full_c[fp::stages(BWD)];
+    uint64_t full_dec[fp::stages(BWD)];       // used in the even CTA
+    uint64_t empty[fp::stages(BWD)];
+    uint64_t tmem_full[2];
+    uint64_t tmem_empty[2];                   // used in the even CTA
+    uint64_t mma_done;
+    uint32_t tmem_base;
+    int abort_flag;
+};
+template <bool BWD>
+constexpr size_t ffn_smem_bytes() {
+    return sizeof(FfnSmem<BWD>) + 1024;
+}
+static_assert(ffn_smem_bytes<false>() <= 232448 && ffn_smem_bytes<true>() <= 232448, "feed-forward tile does not fit");
+
+struct FfnParams {
+    CUtensorMap x, wg, wu;     // int8 activations [T, K]; 2-bit codes [F, K / 4]
+    CUtensorMap out;           // h [T, F] (forward, when out_tma), v [T, 2 Fp] (backward)
+    const float* scale_g;
+    const float* scale_u;
+    const float* s_tok;
+    void* h;                   // forward
+    const float* dh;           // backward
+    unsigned* row_max;         // backward: [T] bits of the largest |v| of a token
+    unsigned* all_max;         // backward: of all tokens
+    int T, K, F, Fp;
+    int h_bf16, out_tma;
+};
+
+template <bool BWD, int ACT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp::THREADS, 1)
+    ffn_pair_kernel(const __grid_constant__ FfnParams q, unsigned* status) {
+    constexpr int STAGES = fp::stages(BWD);
+    extern __shared__ uint8_t smem_raw[];
+    auto* sm = reinterpret_cast<FfnSmem<BWD>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    volatile int* abort_flag = &sm->abort_flag;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+    const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+    const int T = q.T, F = q.F;
+    const int MT = (T + 2 * fp::BM - 1) / (2 * fp::BM), NT = (F + fp::BF - 1) / fp::BF;
+    const int tiles = MT * NT;
+    const int KB = (q.K + fp::BK - 1) / fp::BK;
+
+    asm volatile("griddepcontrol.launch_dependents;");
+    if (threadIdx.x == 32) {
+        prefetch_tmap(&q.x);
+        prefetch_tmap(rank ? &q.wu : &q.wg);
+        prefetch_tmap(&q.out);
+    }
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&sm->full_a[s], 1);
+            mbar_init(&sm->full_c[s], 1);
+            mbar_init(&sm->full_dec[s], 2 * fp::DEC_WARPS);
+            mbar_init(&sm->empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&sm->tmem_full[b], 1);
+            mbar_init(&sm->tmem_empty[b], 2 * fp::EPI_WARPS);
+        }
+        mbar_init(&sm->mma_done, 1);
+        sm->abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == fp::WARP_MMA) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm->tmem_base)),
+                     "r"(2 * fp::BN)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem_base = sm->tmem_base;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    auto give_up = [&]() {
+        if (!*abort_flag) {
+            *abort_flag = 1;
+            raise_status(status, kStatusTimeout);
+        }
+    };
+    auto arrive_leader = [&](uint64_t* bar) {
+        if (leader) mbar_arrive(bar);
+        else mbar_arrive_cluster(map_to_cta(smem_u32(bar), 0));
+    };
+
+    if (warp < fp::EPI_WARPS) {
+        // ------------------------------------------------------------ epilogue
+        // Warp w: tokens 32 (w % 4) .. + 31 of the CTA's half, hidden units
+        // 64 (w / 4) .. + 63 of the tile, in two slices of 32.
+        const int qd = warp & 3, half = warp >> 2;
+        const uint32_t lane_addr = static_cast<uint32_t>(qd * 32) << 16;
+        float* const sc_g = sm->scale[warp][0];
+        float* const sc_u = sm->scale[warp][1];
+        uint8_t* const box = sm->box[warp][0];
+        int tc = 0;
+        for (int tile = pair; tile < tiles; tile += npairs, ++tc) {
+            const int mt = tile / NT, nt = tile % NT;  // hidden tiles fastest: a token tile is read once
+            const int b = tc & 1;
+            const int f0 = nt * fp::BF + half * 64;
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int f = f0 + 32 * k + lane;
+                sc_g[32 * k + lane] = f < F ? __ldg(q.scale_g + f) : 0.f;
+                sc_u[32 * k + lane] = f < F ? __ldg(q.scale_u + f) : 0.f;
+            }
+            const int trow0 = mt * 2 * fp::BM + static_cast<int>(rank) * fp::BM + qd * 32;
+            const int t = trow0 + lane;
+            const float inv_s = t < T ? __frcp_rn(__ldg(q.s_tok + t)) : 0.f;
+            float top = 0.f;
+            __syncwarp();
+            if (!warp_wait(&sm->tmem_full[b], (tc >> 1) & 1, abort_flag)) { give_up(); break; }
+            tc_fence_after();
+            const uint32_t tbase = tmem_base + lane_addr + b * fp::BN + half * 64;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                uint32_t g[32], u[32];
+                tmem_ld32_nowait(tbase + 32 * k, g);
+                tmem_ld32_nowait(tbase + fp::BF + 32 * k, u);
+                const int fk = f0 + 32 * k;
+                if (BWD) {
+                    // dh of 32 tokens x 32 units, read along the rows and turned in
+                    // the second box (word c of row r at c ^ r: no bank conflicts)
+                    uint32_t* const tb = reinterpret_cast<uint32_t*>(sm->box[warp][1]);
+                    float d[32];
+#pragma unroll
+                    for (int r = 0; r < 32; ++r)
+                        d[r] = (trow0 + r < T && fk + lane < F)
+                                   ? __ldg(q.dh + static_cast<size_t>(trow0 + r) * F + fk + lane) : 0.f;
+                    box_wait(lane);  // both boxes' stores have been read
+#pragma unroll
+                    for (int r = 0; r < 32; ++r) tb[r * 32 + (lane ^ r)] = __float_as_uint(d[r]);
+                    __syncwarp();
+                    tmem_wait_into(g);
+                    tmem_wait_into(u);
+                    if (k == 1) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) arrive_leader(&sm->tmem_empty[b]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const float dhv = __uint_as_float(tb[lane * 32 + (i ^ lane)]);
+                        const float sgi = sc_g[32 * k + i], sui = sc_u[32 * k + i];
+                        const float gv = __fmul_rn(__fmul_rn(static_cast<float>(static_cast<int>(g[i])), sgi), inv_s);
+                        const float uv = __fmul_rn(__fmul_rn(static_cast<float>(static_cast<int>(u[i])), sui), inv_s);
+                        float a, da;
+                        act_both<ACT>(gv, a, da);
+                        const float vg = dhv * uv * da * sgi * inv_s;
+                        const float vu = dhv * a * sui * inv_s;
+                        // a token past the end has inv_s = 0, a unit past F a scale of 0
+                        g[i] = __float_as_uint(vg);
+                        u[i] = __float_as_uint(vu);
+                        top = fmaxf(top, fmaxf(fabsf(vg), fabsf(vu)));
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        box_put(box, lane, c, g[4 * c], g[4 * c + 1], g[4 * c + 2], g[4 * c + 3]);
+                        box_put(sm->box[warp][1], lane, c, u[4 * c], u[4 * c + 1], u[4 * c + 2], u[4 * c + 3]);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_2d(&q.out, smem_u32(box), fk, trow0);
+                        tma_store_2d(&q.out, smem_u32(sm->box[warp][1]), q.Fp + fk, trow0);
+                    }
+                } else {
+                    tmem_wait_into(g);
+                    tmem_wait_into(u);
+                    if (k == 1) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) arrive_leader(&sm->tmem_empty[b]);
+                    }
+                    float h[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const float gv = __fmul_rn(__fmul_rn(static_cast<float>(static_cast<int>(g[i])), sc_g[32 * k + i]), inv_s);
+                        const float uv = __fmul_rn(__fmul_rn(static_cast<float>(static_cast<int>(u[i])), sc_u[32 * k + i]), inv_s);
+                        h[i] = act_value<ACT>(gv) * uv;
+                    }
+                    if (q.out_tma) {
+                        if (q.h_bf16) {
+                            if (k == 0) box_wait(lane);
+#pragma unroll
+                            for (int c = 0; c < 4; ++c)
+                                box_put(box, lane, 4 * k + c, pack_bf16(h[8 * c], h[8 * c + 1]), pack_bf16(h[8 * c + 2], h[8 * c + 3]),
+                                        pack_bf16(h[8 * c + 4], h[8 * c + 5]), pack_bf16(h[8 * c + 6], h[8 * c + 7]));
+                        } else {
+                            box_wait(lane);
+#pragma unroll
+                            for (int c = 0; c < 8; ++c)
+                                box_put(box, lane, c, __float_as_uint(h[4 * c]), __float_as_uint(h[4 * c + 1]),
+                                        __float_as_uint(h[4 * c + 2]), __float_as_uint(h[4 * c + 3]));
+                        }
+                        if (!q.h_bf16 || k == 1) {
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (lane == 0) tma_store_2d(&q.out, smem_u32(box), q.h_bf16 ? f0 : fk, trow0);
+                        }
+                    } else {
+                        // rows that TMA cannot address (pitch not a multiple of 16
+                        // bytes): turned in the box, then written along the rows
+                        uint32_t* const tb = reinterpret_cast<uint32_t*>(box);
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) tb[lane * 32 + (i ^ lane)] = __float_as_uint(h[i]);
+                        __syncwarp();
+#pragma unroll 8
+                        for (int r = 0; r < 32; ++r) {
+                            const float v = __uint_as_float(tb[r * 32 + (lane ^ r)]);
+                            if (trow0 + r < T && fk + lane < F) {
+                                const size_t at = static_cast<size_t>(trow0 + r) * F + fk + lane;
+                                if (q.h_bf16) reinterpret_cast<__nv_bfloat16*>(q.h)[at] = __float2bfloat16_rn(v);
+                                else reinterpret_cast<float*>(q.h)[at] = v;
+                            }
+                        }
+                    }
+                }
+            }
+            if (BWD) {
+                const unsigned bits = __float_as_uint(top);
+                if (t < T && bits) atomicMax(q.row_max + t, bits);
+                const unsigned m = __reduce_max_sync(0xFFFFFFFFu, bits);
+                if (lane == 0 && m) atomicMax(q.all_max, m);
+            }
+        }
+        if (lane == 0) bulk_wait_all();
+    } else if (warp < fp::WARP_TMA) {
+        // ------------------------------------------------------------ weight expansion
+        // Thread r expands row r of this CTA's matrix (rank 0: gate, rank 1: up).
+        const int r = threadIdx.x - fp::EPI_WARPS * 32;
+        uint32_t it = 0;
+        bool ok = true;
+        for (int tile = pair; tile < tiles && ok; tile += npairs) {
+            for (int kb = 0; kb < KB; ++kb, ++it) {
+                const int s = it % STAGES;
+                // the producer loads codes only into a stage that the MMAs released
+                if (!mbar_wait(&sm->full_c[s], (it / STAGES) & 1, abort_flag)) { give_up(); ok = false; break; }
+                // 32-byte code rows, 32B-swizzled by TMA
+                const uint8_t* src = sm->p[s] + r * 32;
+                const int hs = (r >> 2) & 1;
+                const uint4 p0 = *reinterpret_cast<const uint4*>(src + (hs << 4));
+                const uint4 p1 = *reinterpret_cast<const uint4*>(src + ((hs ^ 1) << 4));
+                uint8_t* dst = sm->b[s] + r * 128;
+                const int sw = r & 7;
+                const uint32_t w[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    uint32_t e[4];
+                    expand_pairs(w[c], e);
+                    const uint32_t a = smem_u32(dst + ((c ^ sw) << 4));
+                    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(e[0]), "r"(e[1]), "r"(e[2]),
+                                 "r"(e[3])
+                                 : "memory");
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if ((r & 31) == 0) arrive_leader(&sm->full_dec[s]);
+            }
+        }
+    } else if (warp == fp::WARP_TMA) {
+        // ------------------------------------------------------------ TMA producer
+        if (lane == 0) {
+            const CUtensorMap* const wmap = rank ? &q.wu : &q.wg;
+            uint32_t it = 0;
+            bool ok = true;
+            for (int tile = pair; tile < tiles && ok; tile += npairs) {
+                const int trow = tile / NT * 2 * fp::BM + static_cast<int>(rank) * fp::BM;
+                const int frow = tile % NT * fp::BF;
+                for (int kb = 0; kb < KB; ++kb, ++it) {
+                    const int s = it % STAGES;
+                    if (!mbar_wait(&sm->empty[s], ((it / STAGES) & 1) ^ 1, abort_flag)) { give_up(); ok = false; break; }
+                    if (leader) mbar_arrive_expect_tx(&sm->full_a[s], 2 * fp::A_BYTES);
+                    mbar_arrive_expect_tx(&sm->full_c[s], fp::P_BYTES);
+                    tma_load_2d_pair(smem_u32(sm->a[s]), &q.x, kb * fp::BK, trow, map_to_cta(smem_u32(&sm->full_a[s]), 0));
+                    tma_load_2d(smem_u32(sm->p[s]), wmap, kb * (fp::BK / 4), frow, &sm->full_c[s]);
+                }
+            }
+            // let the issued loads land before the CTA can exit
+            const uint32_t first = it > STAGES ? it - STAGES : 0;
+            volatile int never = 0;
+            for (uint32_t j = first; j < it; ++j) {
+                const int s = j % STAGES;
+                const uint32_t ph = (j / STAGES) & 1;
+                if (!mbar_wait(&sm->full_c[s], ph, &never)) give_up();
+                if (leader && !mbar_wait(&sm->full_a[s], ph, &never)) give_up();
+            }
+        }
+    } else {
+        // ------------------------------------------------------------ MMA issuer (even CTA)
+        if (lane == 0) {
+            if (leader) {
+                const uint32_t idesc = i8_idesc<2 * fp::BM, fp::BN>();
+                uint32_t it = 0;
+                int tc = 0;
+                bool ok = true;
+                for (int tile = pair; tile < tiles && ok; tile += npairs, ++tc) {
+                    const int b = tc & 1;
+                    if (!mbar_wait(&sm->tmem_empty[b], ((tc >> 1) & 1) ^ 1, abort_flag)) { give_up(); break; }
+                    tc_fence_after();
+                    const uint32_t d = tmem_base + b * fp::BN;
+                    for (int kb = 0; kb < KB; ++kb, ++it) {
+                        const int s = it % STAGES;
+                        const uint32_t ph = (it / STAGES) & 1;
+                        if (!mbar_wait(&sm->full_a[s], ph, abort_flag) || !mbar_wait(&sm->full_dec[s], ph, abort_flag)) {
+                            give_up(); ok = false; break;
+                        }
+                        tc_fence_after();
+                        const uint32_t a0 = smem_u32(sm->a[s]), b0 = smem_u32(sm->b[s]);
+#pragma unroll
+                        for (int kk = 0; kk < fp::BK / 32; ++kk)
+                            tc_mma_pair(d, sw128_desc(a0 + kk * 32), sw128_desc(b0 + kk * 32), idesc, (kb | kk) != 0);
+                        tc_commit_pair_both(&sm->empty[s]);
+                    }
+                    if (ok) tc_commit_pair_both(&sm->tmem_full[b]);
+                }
+                tc_commit_pair_both(&sm->mma_done);
+            }
+            volatile int never = 0;
+            if (!mbar_wait(&sm->mma_done, 0, &never)) give_up();
+        }
+        __syncwarp();
+    }
+
+    tc_fence_before();
+    cluster_sync();
+    if (warp == fp::WARP_MMA) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(2 * fp::BN)
+                     : "memory");
+    }
+}
+
+// Codes of a matrix whose rows are not a multiple of 16 bytes (K % 64 != 0),
+// copied to rows that are, zero codes at the end: TMA's row pitch.
+__global__ void __launch_bounds__(256)
+    ffn_pad_codes_kernel(const uint32_t* __restrict__ pg, const uint32_t* __restrict__ pu, long long F, int words,
+                         int padded, uint32_t* __restrict__ og, uint32_t* __restrict__ ou) {
+    asm volatile("griddepcontrol.launch_dependents;");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const long long n = F * padded;
+    for (long long i = blockIdx.x * 256ll + threadIdx.x; i < 2 * n; i += gridDim.x * 256ll) {
+        const bool up = i >= n;
+        const long long j = up ? i - n : i, row = j / padded;
+        const int c = static_cast<int>(j - row * padded);
+        (up ? ou : og)[j] = c < words ? __ldg((up ? pu : pg) + row * words + c) : 0u;
+    }
+}
+
+// ---------------------------------------------------------------- backward operands
+// er: the power of two that a token's v is divided by.  Its largest |v|, with
+// exponent e, lands in [2^14, 2^15) (a token below 2^-112 keeps what 2^126 gives it).
+__device__ __forceinline__ int row_exponent(unsigned bits) {
+    if (bits >= 0x7F800000u) return 0;  // NaN or Inf: passed on unscaled
+    const int e = static_cast<int>(bits >> 23) - 127;
+    return max(e - 14, -126);
+}
+__device__ __forceinline__ float pow2f(int e) { return __uint_as_float(static_cast<unsigned>(e + 127) << 23); }
+
+struct FfnOperands {
+    const float* v;            // [T, 2 Fp]
+    const unsigned* row_max;
+    const unsigned* all_max;
+    const uint8_t* pg;
+    const uint8_t* pu;
+    const int8_t* xq;          // [T, K], pairing order
+    __half* parts;             // [T, 2 * 2 Fp]: high parts, low parts
+    __half* codes;             // [2 Fp, K] or NULL (no dX)
+    __half* xs;                // [T, K] or NULL (no dW)
+    int T, K, F, Fp;
+    int split_blocks, code_blocks, x_blocks;
+};
+
+// Three copies in one launch: blocks split into ranges, 256 threads, items of 8 or 16 elements.
+__global__ void __launch_bounds__(256) ffn_operands_kernel(const FfnOperands q) {
+    asm volatile("griddepcontrol.launch_dependents;");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    int block = blockIdx.x;
+    if (block < q.split_blocks) {
+        // 8 values of one token: v * 2^-er in two fp16 parts
+        const int per_row = 2 * q.Fp / 8;
+        const long long n = static_cast<long long>(q.T) * per_row;
+        for (long long i = block * 256ll + threadIdx.x; i < n; i += q.split_blocks * 256ll) {
+            const long long t = i / per_row;
+            const int c = static_cast<int>(i - t * per_row) * 8;
+            const float s = pow2f(-row_exponent(__ldg(q.row_max + t)));
+            const float4* const p = reinterpret_cast<const float4*>(q.v + t * 2 * q.Fp + c);
+            const float4 a = __ldg(p), b = __ldg(p + 1);
+            const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float v0 = f[2 * j] * s, v1 = f[2 * j + 1] * s;
+                const __half2 h = __floats2half2_rn(v0, v1);
+                const float2 hf = __half22float2(h);
+                const __half2 l = __floats2half2_rn(v0 - hf.x, v1 - hf.y);  // the difference is exact
+                hi[j] = *reinterpret_cast<const uint32_t*>(&h);
+                lo[j] = *reinterpret_cast<const uint32_t*>(&l);
+            }
+            __half* const o = q.parts + t * 4 * q.Fp + c;
+            *reinterpret_cast<uint4*>(o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(o + 2 * q.Fp) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+        return;
+    }
+    block -= q.split_blocks;
+    const int words = q.K / 16;
+    if (block < q.code_blocks) {
+        // 16 codes of one row: 0, +1, -1 in fp16; rows past F are zeros
+        const long long n = 2ll * q.Fp * words;
+        for (long long i = block * 256ll + threadIdx.x; i < n; i += q.code_blocks * 256ll) {
+            const long long r = i / words;
+            const int c = static_cast<int>(i - r * words);
+            const bool up = r >= q.Fp;
+            const long long f = up ? r - q.Fp : r;
+            const uint32_t w = f < q.F ? __ldg(reinterpret_cast<const uint32_t*>(up ? q.pu : q.pg) + f * words + c) : 0u;
+            uint32_t o[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t c0 = (w >> (4 * j)) & 3u, c1 = (w >> (4 * j + 2)) & 3u;
+                // 01 -> 0x3C00, 10 -> 0xBC00
+                o[j] = (c0 ? 0x3C00u | (c0 & 2u) << 14 : 0u) | (c1 ? 0x3C00u | (c1 & 2u) << 14 : 0u) << 16;
+            }
+            uint4* const p = reinterpret_cast<uint4*>(q.codes + r * q.K + 16 * c);
+            p[0] = make_uint4(o[0], o[1], o[2], o[3]);
+            p[1] = make_uint4(o[4], o[5], o[6], o[7]);
+        }
+        return;
+    }
+    block -= q.code_blocks;
+    // 16 activations of one token: x_q * 2^(er - max er + 8), back in column order
+    const long long n = static_cast<long long>(q.T) * words;
+    const int top = row_exponent(*q.all_max);
+    for (long long i = block * 256ll + threadIdx.x; i < n; i += q.x_blocks * 256ll) {
+        const long long t = i / words;
+        const int e = row_exponent(__ldg(q.row_max + t)) - top + 8;
+        const float s = e < -40 ? 0.f : pow2f(e);  // 127 * 2^-40 is below half of fp16's smallest step
+        const uint4 u = __ldg(reinterpret_cast<const uint4*>(q.xq) + i);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};  // even 0-6, odd 1-7, even 8-14, odd 9-15
+        uint32_t o[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {  // elements 2 j and 2 j + 1
+            const int g = (j >> 2) * 2, sh = 8 * (j & 3);
+            const float a = static_cast<float>(static_cast<int8_t>(w[g] >> sh)) * s;
+            const float b = static_cast<float>(static_cast<int8_t>(w[g + 1] >> sh)) * s;
+            const __half2 h = __floats2half2_rn(a, b);
+            o[j] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        uint4* const p = reinterpret_cast<uint4*>(q.xs) + 2 * i;
+        p[0] = make_uint4(o[0], o[1], o[2], o[3]);
+        p[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    }
+}
+
+// dX: the token's sums times 2^er * s_t.
+struct FfnDx {
+    struct Params {
+        CUtensorMap out;
+        const unsigned* row_max;
+        const float* s_tok;
+        int T;
+    };
+    static __device__ __forceinline__ void prefetch(const Params& p) { prefetch_tmap(&p.out); }
+    const Params& p;
+    float e, s;
+    __device__ __forceinline__ explicit FfnDx(const Params& r) : p(r), e(0.f), s(0.f) {}
+    __device__ __forceinline__ void begin(const GemmTile& t) {
+        if (t.row < p.T) {
+            e = pow2f(row_exponent(__ldg(p.row_max + t.row)));
+            s = __ldg(p.s_tok + t.row);
+        }
+    }
+    __device__ __forceinline__ void slice(const GemmTile& t, int k, float (&v)[32]) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = (v[i] * e) * s;
+        put_f32(t, k, v, &p.out, 0, false);
+    }
+    __device__ __forceinline__ void end(const GemmTile&) {}
+};
+
+// dW: rows 0 .. Fp - 1 to the gate's gradient, the next Fp to the up's, times
+// 2^(max er - 8) / scale (ternary: without the division).
+struct FfnDw {
+    struct Params {
+        CUtensorMap out_g, out_u;
+        const unsigned* all_max;
+        const float* scale_g;
+        const float* scale_u;
+        int F, Fp, want_g, want_u, ternary;
+    };
+    static __device__ __forceinline__ void prefetch(const Params& p) {
+        if (p.want_g) prefetch_tmap(&p.out_g);
+        if (p.want_u) prefetch_tmap(&p.out_u);
+    }
+    const Params& p;
+    float e, s;
+    bool up;
+    __device__ __forceinline__ explicit FfnDw(const Params& r) : p(r), e(pow2f(row_exponent(*r.all_max))), s(0.f), up(false) {}
+    __device__ __forceinline__ void begin(const GemmTile& t) {
+        up = t.warp_row >= p.Fp;  // Fp % 128 == 0: a warp's 32 rows are of one matrix
+        const int f = t.row - (up ? p.Fp : 0);
+        s = f < p.F ? (p.ternary ? 1.0f : __frcp_rn(__ldg((up ? p.scale_u : p.scale_g) + f))) : 0.f;
+        s *= 0.00390625f;  // x_q came times 2^8
+    }
+    __device__ __forceinline__ void slice(const GemmTile& t, int k, float (&v)[32]) {
+        if (up ? !p.want_u : !p.want_g) return;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = (v[i] * e) * s;
+        put_f32(t, k, v, up ? &p.out_u : &p.out_g, up ? p.Fp : 0, false);
+    }
+    __device__ __forceinline__ void end(const GemmTile&) {}
+};
+
+// ---------------------------------------------------------------- host side
+size_t round256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
+
+bool takes_decode(long long T, long long K) {
+    return T <= fd::MAX_TOKENS && K <= (1 << 20) && fd::smem_bytes(static_cast<int>(K), 1) <= 200 * 1024;
+}
+
+// Quantised activations, their scales, and the padded codes of both matrices.
+struct FfnSpace {
+    size_t xq, s_tok, codes, end;
+};
+FfnSpace ffn_space(long long T, long long K, long long F) {
+    FfnSpace s;
+    s.xq = 0;
+    s.s_tok = round256(static_cast<size_t>(T) * K);
+    s.codes = s.s_tok + round256(static_cast<size_t>(T) * 4);
+    s.end = s.codes + (K % 64 ? 2 * round256(static_cast<size_t>(F) * ((K + 63) / 64 * 16)) : 0);
+    return s;
+}
+
+struct FfnBwdSpace {
+    FfnSpace fwd;
+    size_t maxima, v, parts, codes, xs, end;
+    long long Fp, nmax16;
+};
+FfnBwdSpace ffn_bwd_space(long long T, long long K, long long F, int need_dx, int need_dw) {
+    FfnBwdSpace s;
+    s.fwd = ffn_space(T, K, F);
+    s.Fp = (F + 127) / 128 * 128;
+    s.nmax16 = (T + 1 + 3) / 4;  // row maxima and the maximum of all, in 16-byte units
+    s.maxima = s.fwd.end;
+    s.v = s.maxima + round256(static_cast<size_t>(s.nmax16) * 16);
+    s.parts = s.v + round256(static_cast<size_t>(T) * 2 * s.Fp * 4);
+    s.codes = s.parts + round256(static_cast<size_t>(T) * 4 * s.Fp * 2);
+    s.xs = s.codes + (need_dx ? round256(static_cast<size_t>(2) * s.Fp * K * 2) : 0);
+    s.end = s.xs + (need_dw ? round256(static_cast<size_t>(T) * K * 2) : 0);
+    return s;
+}
+
+bool byte_map(CUtensorMap* map, const void* base, long long rows, long long row_bytes, int box_bytes, int box_rows,
+              CUtensorMapSwizzle swizzle) {
+    EncodeTiledFn enc = get_encode_fn();
+    if (!enc) return false;
+    const cuuint32_t estr[2] = {1, 1};
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_bytes)};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_bytes), static_cast<cuuint32_t>(box_rows)};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool BWD, int ACT>
+cudaError_t launch_pair(const FfnParams& q, unsigned* status, cudaStream_t st) {
+    auto kern = ffn_pair_kernel<BWD, ACT>;
+    static int clusters[64] = {};
+    int dev = 0;
+    if (cudaError_t e = cudaGetDevice(&dev)) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(fp::THREADS);
+    cfg.dynamicSmemBytes = ffn_smem_bytes<BWD>();
+    cfg.stream = st;
+    if (clusters[dev] == 0) {
+        if (cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 static_cast<int>(ffn_smem_bytes<BWD>())))
+            return e;
+        int n = 0;
+        if (cudaError_t e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg)) return e;
+        if (n <= 0) return cudaErrorNotSupported;
+        clusters[dev] = n;
+    }
+    const long long tiles = ((q.T + 2ll * fp::BM - 1) / (2 * fp::BM)) * ((q.F + fp::BF - 1) / fp::BF);
+    if (tiles > (1ll << 30)) return cudaErrorInvalidValue;
+    cfg.gridDim = dim3(2 * static_cast<unsigned>(tiles < clusters[dev] ? tiles : clusters[dev]));
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, q, status);
+}
+
+// Activations quantised (and `nzero16` 16-byte units at zero16 cleared), codes
+// padded where TMA needs it, and the tensor maps and scales that both
+// directions share.
+cudaError_t pair_inputs(FfnParams& q, const uint16_t* x, long long T, long long K, const uint8_t* pg,
+                        const float* scale_g, const uint8_t* pu, const float* scale_u, long long F, uint8_t* ws,
+                        void* zero16, long long nzero16, unsigned* status, int num_sms, cudaStream_t st) {
+    const FfnSpace sp = ffn_space(T, K, F);
+    int8_t* const xq = reinterpret_cast<int8_t*>(ws + sp.xq);
+    float* const s_tok = reinterpret_cast<float*>(ws + sp.s_tok);
+    if (cudaError_t e = launch_quant(x, T, K, xq, s_tok, kLayoutPairsFfn, status, st, zero16, nzero16)) return e;
+    long long row_bytes = K / 4;
+    if (K % 64) {
+        const int words = static_cast<int>(K / 16), padded = (words + 3) / 4 * 4;
+        uint8_t* const og = ws + sp.codes;
+        uint8_t* const ou = og + round256(static_cast<size_t>(F) * padded * 4);
+        const long long blocks = (2 * F * padded + 255) / 256, most = 8ll * num_sms;
+        if (cudaError_t e = pdl_launch(ffn_pad_codes_kernel, dim3(static_cast<unsigned>(blocks < most ? blocks : most)),
+                                       dim3(256), 0, st, reinterpret_cast<const uint32_t*>(pg),
+                                       reinterpret_cast<const uint32_t*>(pu), F, words, padded,
+                                       reinterpret_cast<uint32_t*>(og), reinterpret_cast<uint32_t*>(ou)))
+            return e;
+        pg = og;
+        pu = ou;
+        row_bytes = padded * 4ll;
+    }
+    if (!byte_map(&q.x, xq, T, K, fp::BK, fp::BM, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !byte_map(&q.wg, pg, F, row_bytes, fp::BK / 4, fp::BF, CU_TENSOR_MAP_SWIZZLE_32B) ||
+        !byte_map(&q.wu, pu, F, row_bytes, fp::BK / 4, fp::BF, CU_TENSOR_MAP_SWIZZLE_32B))
+        return cudaErrorInvalidValue;
+    q.scale_g = scale_g;
+    q.scale_u = scale_u;
+    q.s_tok = s_tok;
+    q.T = static_cast<int>(T);
+    q.K = static_cast<int>(K);
+    q.F = static_cast<int>(F);
+    return cudaSuccess;
+}
+
+template <int NT, int CW, int ACT>
+cudaError_t launch_decode_as(const uint8_t* pg, const float* sg, const uint8_t* pu, const float* su, int F, int K,
+                             const uint16_t* x, int t0, int TP, int KS, void* h, int h_bf16, unsigned* status,
+                             cudaStream_t st) {
+    const size_t smem = fd::smem_bytes(K, TP);
+    if (smem > 48 * 1024)
+        if (cudaError_t e = cudaFuncSetAttribute(ffn_decode_kernel<NT, CW, ACT>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)))
+            return e;
+    const int tiles = (F + 7) / 8, per_block = fd::WARPS / KS;
+    return pdl_launch(ffn_decode_kernel<NT, CW, ACT>, dim3((tiles + per_block - 1) / per_block), dim3(fd::THREADS), smem,
+                      st, pg, sg, pu, su, F, K, x, t0, TP, KS, h, h_bf16, status);
+}
+
+template <int NT, int ACT>
+cudaError_t launch_decode_cw(int CW, const uint8_t* pg, const float* sg, const uint8_t* pu, const float* su, int F, int K,
+                             const uint16_t* x, int t0, int TP, int KS, void* h, int h_bf16, unsigned* status,
+                             cudaStream_t st) {
+    if (CW == 4) return launch_decode_as<NT, 4, ACT>(pg, sg, pu, su, F, K, x, t0, TP, KS, h, h_bf16, status, st);
+    if (CW == 2) return launch_decode_as<NT, 2, ACT>(pg, sg, pu, su, F, K, x, t0, TP, KS, h, h_bf16, status, st);
+    return launch_decode_as<NT, 1, ACT>(pg, sg, pu, su, F, K, x, t0, TP, KS, h, h_bf16, status, st);
+}
+
+template <int ACT>
+cudaError_t run_decode(const uint16_t* x, long long T, int K, const uint8_t* pg, const float* sg, const uint8_t* pu,
+                       const float* su, int F, void* h, int h_bf16, unsigned* status, int num_sms, cudaStream_t st) {
+    const int CW = K % 256 == 0 ? 4 : K % 128 == 0 ? 2 : 1;
+    const int C = fd::pad64(K) / (64 * CW), nb = CW == 4 ? 2 : 4, tiles = (F + 7) / 8;
+    // warps per tile: the fewest whose slices fit one batch of loads, then more
+    // while the grid has fewer blocks than SMs, never more warps than chunks
+    int KS = 1;
+    while (KS < fd::WARPS && KS < C && (C + KS - 1) / KS > nb) KS *= 2;
+    while (KS < fd::WARPS && 2 * KS <= C && static_cast<long long>(tiles) * 2 * KS <= static_cast<long long>(num_sms) * fd::WARPS)
+        KS *= 2;
+    int cap = fd::MAX_TOKENS;  // tokens of one pass
+    while (cap > 1 && fd::smem_bytes(K, cap) > 200 * 1024) --cap;
+    for (int t0 = 0; t0 < T; t0 += cap) {
+        const int TP = static_cast<int>(T) - t0 < cap ? static_cast<int>(T) - t0 : cap;
+        const cudaError_t e = TP > 8 ? launch_decode_cw<2, ACT>(CW, pg, sg, pu, su, F, K, x, t0, TP, KS, h, h_bf16, status, st)
+                                     : launch_decode_cw<1, ACT>(CW, pg, sg, pu, su, F, K, x, t0, TP, KS, h, h_bf16, status, st);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace
+
+size_t ffn_workspace_bytes(long long T, long long K, long long F) { return takes_decode(T, K) ? 0 : ffn_space(T, K, F).end; }
+
+size_t ffn_backward_workspace_bytes(long long T, long long K, long long F, int need_dx, int need_dw) {
+    return ffn_bwd_space(T, K, F, need_dx, need_dw).end;
+}
+
+cudaError_t launch_ffn(const uint16_t* x, long long T, long long K, const uint8_t* pg, const float* scale_g,
+                       const uint8_t* pu, const float* scale_u, long long F, int act, void* h, int h_bf16, void* ws,
+                       unsigned* status, int num_sms, cudaStream_t st) {
+    if (takes_decode(T, K))
+        return act == kActSilu ? run_decode<0>(x, T, static_cast<int>(K), pg, scale_g, pu, scale_u, static_cast<int>(F), h,
+                                               h_bf16, status, num_sms, st)
+                               : run_decode<1>(x, T, static_cast<int>(K), pg, scale_g, pu, scale_u, static_cast<int>(F), h,
+                                               h_bf16, status, num_sms, st);
+    FfnParams q;
+    memset(&q, 0, sizeof(q));
+    if (cudaError_t e = pair_inputs(q, x, T, K, pg, scale_g, pu, scale_u, F, static_cast<uint8_t*>(ws), nullptr, 0, status,
+                                    num_sms, st))
+        return e;
+    const int es = h_bf16 ? 2 : 4;
+    q.h = h;
+    q.h_bf16 = h_bf16;
+    q.out_tma = F * es % 16 == 0;
+    q.out = q.x;
+    if (q.out_tma && !gemm_map(&q.out, h_bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, h, T, F,
+                               F * es, 128 / es, 32))
+        return cudaErrorInvalidValue;
+    return act == kActSilu ? launch_pair<false, 0>(q, status, st) : launch_pair<false, 1>(q, status, st);
+}
+
+cudaError_t launch_ffn_backward(const float* dh, const uint16_t* x, long long T, long long K, const uint8_t* pg,
+                                const float* scale_g, const uint8_t* pu, const float* scale_u, long long F, int act,
+                                float* dx, float* dwg, float* dwu, int ternary, void* ws, unsigned* status, int num_sms,
+                                cudaStream_t st) {
+    uint8_t* const base = static_cast<uint8_t*>(ws);
+    const int need_dw = dwg || dwu;
+    const FfnBwdSpace sp = ffn_bwd_space(T, K, F, dx != nullptr, need_dw);
+    const int Ti = static_cast<int>(T), Ki = static_cast<int>(K), Fi = static_cast<int>(F), Fp = static_cast<int>(sp.Fp);
+    FfnParams q;
+    memset(&q, 0, sizeof(q));
+    if (cudaError_t e = pair_inputs(q, x, T, K, pg, scale_g, pu, scale_u, F, base, base + sp.maxima, sp.nmax16, status,
+                                    num_sms, st))
+        return e;
+    float* const v = reinterpret_cast<float*>(base + sp.v);
+    unsigned* const row_max = reinterpret_cast<unsigned*>(base + sp.maxima);
+    unsigned* const all_max = row_max + T;
+    q.dh = dh;
+    q.row_max = row_max;
+    q.all_max = all_max;
+    q.Fp = Fp;
+    if (!gemm_map(&q.out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, v, T, 2 * sp.Fp, 2 * sp.Fp * 4, 32, 32)) return cudaErrorInvalidValue;
+    if (cudaError_t e = act == kActSilu ? launch_pair<true, 0>(q, status, st) : launch_pair<true, 1>(q, status, st)) return e;
+
+    __half* const parts = reinterpret_cast<__half*>(base + sp.parts);
+    __half* const codes = reinterpret_cast<__half*>(base + sp.codes);
+    __half* const xs = reinterpret_cast<__half*>(base + sp.xs);
+    auto blocks_for = [&](long long items, int per_sm) {
+        const long long want = (items + 255) / 256, most = static_cast<long long>(per_sm) * num_sms;
+        return static_cast<int>(want < most ? want : most);
+    };
+    FfnOperands o;
+    o.v = v;
+    o.row_max = row_max;
+    o.all_max = all_max;
+    o.pg = pg;
+    o.pu = pu;
+    o.xq = reinterpret_cast<const int8_t*>(base + sp.fwd.xq);
+    o.parts = parts;
+    o.codes = codes;
+    o.xs = xs;
+    o.T = Ti;
+    o.K = Ki;
+    o.F = Fi;
+    o.Fp = Fp;
+    o.split_blocks = blocks_for(T * (2 * sp.Fp / 8), 8);
+    o.code_blocks = dx ? blocks_for(2 * sp.Fp * (K / 16), 4) : 0;
+    o.x_blocks = need_dw ? blocks_for(T * (K / 16), 4) : 0;
+    if (cudaError_t e = pdl_launch(ffn_operands_kernel, dim3(o.split_blocks + o.code_blocks + o.x_blocks), dim3(256), 0, st, o))
+        return e;
+
+    const int k_tiles = (Ki + gm::BN - 1) / gm::BN;
+    if (dx) {
+        CUtensorMap a, b;
+        FfnDx::Params p;
+        if (!gemm_operand(&a, true, false, parts, T, 4 * sp.Fp, 4 * sp.Fp) ||
+            !gemm_operand(&b, true, true, codes, 2 * sp.Fp, K, K) ||
+            !gemm_map(&p.out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, dx, T, K, K * 4, 32, 32))
+            return cudaErrorInvalidValue;
+        p.row_max = row_max;
+        p.s_tok = q.s_tok;
+        p.T = Ti;
+        if (cudaError_t e = launch_gemm_f16<FfnDx, 2, false, true, true, 4>(a, b, p, GemmShape{Ti, Ki, 2 * Fp, 2 * Fp, k_tiles},
+                                                                            status, st))
+            return e;
+    }
+    if (need_dw) {
+        CUtensorMap a, b;
+        FfnDw::Params p;
+        memset(&p, 0, sizeof(p));
+        if (!gemm_operand(&a, true, true, parts, T, 4 * sp.Fp, 4 * sp.Fp) || !gemm_operand(&b, true, true, xs, T, K, K) ||
+            (dwg && !gemm_map(&p.out_g, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, dwg, F, K, K * 4, 32, 32)) ||
+            (dwu && !gemm_map(&p.out_u, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, dwu, F, K, K * 4, 32, 32)))
+            return cudaErrorInvalidValue;
+        p.all_max = all_max;
+        p.scale_g = scale_g;
+        p.scale_u = scale_u;
+        p.F = Fi;
+        p.Fp = Fp;
+        p.want_g = dwg != nullptr;
+        p.want_u = dwu != nullptr;
+        p.ternary = ternary;
+        if (cudaError_t e = launch_gemm_f16<FfnDw, 2, true, true, true, 4>(a, b, p, GemmShape{2 * Fp, Ki, Ti, 2 * Fp, k_tiles},
+                                                                           status, st))
+            return e;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace sbl

@@ -68,9 +68,8 @@ constexpr size_t gemm_smem_bytes() {
 static_assert(gemm_smem_bytes<1>() <= 232448 && gemm_smem_bytes<2>() <= 232448, "GEMM stages do not fit");
 
 // The sizes of one launch.  Rows of A beyond M, of B beyond N and k beyond K
-// are zero-filled by TMA.  a_part: k offset (elements) between the A_j when
-// they lie side by side in one K-major matrix, or row offset (in k) between
-// them in an MN-major one.
+// are zero-filled by TMA.  a_part: columns between the A_j, which lie side by
+// side in one matrix (columns of k when K-major, of m when MN-major).
 struct GemmShape {
     int M, N, K;
     int a_part;
@@ -95,6 +94,16 @@ __device__ __forceinline__ uint64_t sw128_mn_desc(uint32_t saddr) {
     d |= static_cast<uint64_t>(1u) << 46;
     d |= static_cast<uint64_t>(2u) << 61;
     return d;
+}
+
+// Wait for this thread's TMEM loads; the registers pass through, so that no
+// use of them can be moved before the wait.
+__device__ __forceinline__ void tmem_wait_into(uint32_t (&r)[32]) {
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 32; i += 8)
+        asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
+                          "+r"(r[i + 6]), "+r"(r[i + 7]));
 }
 
 __device__ __forceinline__ void tc_mma_pair_f16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
@@ -123,6 +132,44 @@ __device__ __forceinline__ void box_put(uint8_t* box, int lane, int c, uint32_t 
 __device__ __forceinline__ void box_wait(int lane) {  // the box's previous store has read it
     if (lane == 0) bulk_wait_read<0>();
     __syncwarp();
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// 32 columns of a row as bf16 into one half of the warp's box; the second
+// half sends the box of 64 columns.
+__device__ __forceinline__ void put_bf16(const GemmTile& t, int k, const float (&v)[32], const CUtensorMap* map) {
+    const int h = k & 1;
+    if (h == 0) box_wait(t.lane);
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        box_put(t.box, t.lane, 4 * h + c, pack_bf16(v[8 * c], v[8 * c + 1]), pack_bf16(v[8 * c + 2], v[8 * c + 3]),
+                pack_bf16(v[8 * c + 4], v[8 * c + 5]), pack_bf16(v[8 * c + 6], v[8 * c + 7]));
+    if (h == 1) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (t.lane == 0) tma_store_2d(map, smem_u32(t.box), t.col0 + 32 * (k - 1), t.warp_row);
+    }
+}
+
+// 32 fp32 columns of a row through the warp's box to rows warp_row - row0 of
+// a matrix; added to what is there when `add`.
+__device__ __forceinline__ void put_f32(const GemmTile& t, int k, const float (&v)[32], const CUtensorMap* map, int row0,
+                                        bool add) {
+    box_wait(t.lane);
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+        box_put(t.box, t.lane, c, __float_as_uint(v[4 * c]), __float_as_uint(v[4 * c + 1]),
+                __float_as_uint(v[4 * c + 2]), __float_as_uint(v[4 * c + 3]));
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (t.lane == 0) {
+        if (add) tma_add_2d(map, smem_u32(t.box), t.col0 + 32 * k, t.warp_row - row0);
+        else tma_store_2d(map, smem_u32(t.box), t.col0 + 32 * k, t.warp_row - row0);
+    }
 }
 
 // Epi: a struct with
@@ -231,7 +278,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gm::THREADS, 1)
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         uint32_t r[32];
-                        tmem_ld32(tbase + 32 * k, r);
+                        tmem_ld32_nowait(tbase + 32 * k, r);
+                        tmem_wait_into(r);
                         if (k == 3) release(b);
 #pragma unroll
                         for (int i = 0; i < 32; ++i) acc[k][i] += __uint_as_float(r[i]);
@@ -248,7 +296,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gm::THREADS, 1)
                 const uint32_t tbase = tmem_base + lane_addr + b * gm::BN + half * (gm::BN / 2);
                 uint32_t ra[32], rb[32];
                 tmem_ld32_nowait(tbase, ra);
-                tmem_ld_wait();
+                tmem_wait_into(ra);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     uint32_t(&cur)[32] = k & 1 ? rb : ra;
@@ -259,7 +307,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gm::THREADS, 1)
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(cur[i]);
                     epi.slice(t, k, v);
-                    if (k < 3) tmem_ld_wait();
+                    if (k < 3) tmem_wait_into(nxt);
                 }
             }
             epi.end(t);
@@ -285,8 +333,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gm::THREADS, 1)
                     for (int j = 0; j < NA; ++j) {
                         const uint32_t dst = smem_u32(sm->a[s][j]);
                         if (A_MN) {
-                            tma_load_2d_pair(dst, &tmap_a, arow, j * shape.a_part + k0, full);
-                            tma_load_2d_pair(dst + gm::TILE / 2, &tmap_a, arow + 64, j * shape.a_part + k0, full);
+                            tma_load_2d_pair(dst, &tmap_a, j * shape.a_part + arow, k0, full);
+                            tma_load_2d_pair(dst + gm::TILE / 2, &tmap_a, j * shape.a_part + arow + 64, k0, full);
                         } else {
                             tma_load_2d_pair(dst, &tmap_a, j * shape.a_part + k0, arow, full);
                         }

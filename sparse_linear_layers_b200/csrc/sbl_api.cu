@@ -1,7 +1,7 @@
 // C ABI of the Sparse-BitLinear library: argument validation, workspace
 // layout, path dispatch and the per-device status word.  All arithmetic runs
 // in the kernels of prep.cu, quant.cu, decode.cu, decode_mma.cu, prefill.cu, prefill_pair.cu, prefill_sp.cu,
-// mask_monitor.cu, backward.cu, backward_tc.cu, norm.cu and xent.cu.
+// mask_monitor.cu, backward.cu, backward_tc.cu, norm.cu, xent.cu and ffn.cu.
 #include <cstdint>
 #include <cstdio>
 #include <cuda_runtime.h>
@@ -71,6 +71,15 @@ cudaError_t launch_norm_fwd(const void* x, int bf16, int layer, const float* w, 
 cudaError_t launch_norm_bwd(const void* dy, const void* x, int bf16, int layer, const float* w, const float* mean,
                             const float* rstd, long long T, long long K, void* dx, float* dw, float* db, float* part,
                             int num_sms, cudaStream_t st);
+size_t ffn_workspace_bytes(long long T, long long K, long long F);
+size_t ffn_backward_workspace_bytes(long long T, long long K, long long F, int need_dx, int need_dw);
+cudaError_t launch_ffn(const uint16_t* x, long long T, long long K, const uint8_t* pg, const float* scale_g,
+                       const uint8_t* pu, const float* scale_u, long long F, int act, void* h, int h_bf16, void* ws,
+                       unsigned* status, int num_sms, cudaStream_t st);
+cudaError_t launch_ffn_backward(const float* dh, const uint16_t* x, long long T, long long K, const uint8_t* pg,
+                                const float* scale_g, const uint8_t* pu, const float* scale_u, long long F, int act,
+                                float* dx, float* dwg, float* dwu, int ternary, void* ws, unsigned* status, int num_sms,
+                                cudaStream_t st);
 size_t xent_workspace_bytes(long long T, long long V);
 size_t xent_backward_workspace_bytes(long long T, long long D, long long V, int need_dx);
 cudaError_t launch_xent(const uint16_t* x, long long T, long long D, const uint16_t* w, long long V,
@@ -358,6 +367,76 @@ sbl_status sbl_linear_backward_ws(const float* dY, int64_t T, int64_t O, const i
     if (sbl_status s = device_info(&d)) return s;
     return from_cuda(sbl::launch_backward_tc(dY, T, O, x_q, s_tok, K, packed, row_scale, dX, dW, ternary ? 1 : 0,
                                              workspace, d->status, d->num_sms, static_cast<cudaStream_t>(stream)));
+}
+
+// Sizes of the gated feed-forward block: extents that the kernels hold in
+// int32, and K whose |acc| <= 127 * K is exact in fp32.
+static sbl_status check_ffn(int64_t T, int64_t K, int64_t F, int n, int m, int act) {
+    if (T < 0 || F < 0) return SBL_ERR_INVALID_ARG;
+    if (sbl_status s = check_k(K)) return s;
+    if (!nm_ok(n, m)) return SBL_ERR_UNSUPPORTED;
+    if (act != SBL_ACT_SILU && act != SBL_ACT_RELU2) return SBL_ERR_INVALID_ARG;
+    if (T > (1ll << 24) || F > (1ll << 24) || K > (1ll << 17)) return SBL_ERR_UNSUPPORTED;
+    return SBL_OK;
+}
+
+size_t sbl_ffn_gated_workspace_bytes(int64_t T, int64_t K, int64_t F) {
+    return check_ffn(T, K, F, 2, 4, SBL_ACT_SILU) || T == 0 || F == 0 ? 0 : sbl::ffn_workspace_bytes(T, K, F);
+}
+
+sbl_status sbl_ffn_gated(const uint16_t* x_bf16, int64_t T, int64_t K, const uint8_t* packed_gate,
+                         const float* scale_gate, const uint8_t* packed_up, const float* scale_up, int64_t F, int n,
+                         int m, int act, void* h, int h_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+    if (sbl_status s = check_ffn(T, K, F, n, m, act)) return s;
+    if (h_dtype != SBL_F32 && h_dtype != SBL_BF16) return SBL_ERR_INVALID_ARG;
+    if (T == 0 || F == 0) return SBL_OK;
+    for (const void* p : {static_cast<const void*>(x_bf16), static_cast<const void*>(packed_gate),
+                          static_cast<const void*>(scale_gate), static_cast<const void*>(packed_up),
+                          static_cast<const void*>(scale_up), static_cast<const void*>(h)})
+        if (!p || !aligned(p, 16)) return SBL_ERR_INVALID_ARG;
+    const size_t need = sbl::ffn_workspace_bytes(T, K, F);
+    if (need && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return SBL_ERR_WORKSPACE;
+    DeviceInfo* d;
+    if (sbl_status s = device_info(&d)) return s;
+    return from_cuda(sbl::launch_ffn(x_bf16, T, K, packed_gate, scale_gate, packed_up, scale_up, F, act, h,
+                                     h_dtype == SBL_BF16, workspace, d->status, d->num_sms,
+                                     static_cast<cudaStream_t>(stream)));
+}
+
+size_t sbl_ffn_gated_backward_workspace_bytes(int64_t T, int64_t K, int64_t F, int need_dx, int need_dw) {
+    return check_ffn(T, K, F, 2, 4, SBL_ACT_SILU) || T == 0 || F == 0
+               ? 0 : sbl::ffn_backward_workspace_bytes(T, K, F, need_dx, need_dw);
+}
+
+sbl_status sbl_ffn_gated_backward(const float* dh, const uint16_t* x_bf16, int64_t T, int64_t K,
+                                  const uint8_t* packed_gate, const float* scale_gate, const uint8_t* packed_up,
+                                  const float* scale_up, int64_t F, int n, int m, int act, float* dX, float* dW_gate,
+                                  float* dW_up, int flags, void* workspace, size_t workspace_bytes, void* stream) {
+    if (sbl_status s = check_ffn(T, K, F, n, m, act)) return s;
+    if (flags & ~SBL_BWD_DW_TERNARY) return SBL_ERR_INVALID_ARG;
+    if (!dX && !dW_gate && !dW_up) return SBL_ERR_INVALID_ARG;
+    for (const void* p : {static_cast<const void*>(dX), static_cast<const void*>(dW_gate),
+                          static_cast<const void*>(dW_up)})
+        if (!aligned(p, 16)) return SBL_ERR_INVALID_ARG;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (T == 0 || F == 0) {  // empty sums
+        cudaError_t e = cudaSuccess;
+        if (dX && T > 0) e = cudaMemsetAsync(dX, 0, static_cast<size_t>(T) * K * sizeof(float), st);
+        for (float* w : {dW_gate, dW_up})
+            if (w && F > 0 && e == cudaSuccess) e = cudaMemsetAsync(w, 0, static_cast<size_t>(F) * K * sizeof(float), st);
+        return from_cuda(e);
+    }
+    for (const void* p : {static_cast<const void*>(dh), static_cast<const void*>(x_bf16),
+                          static_cast<const void*>(packed_gate), static_cast<const void*>(scale_gate),
+                          static_cast<const void*>(packed_up), static_cast<const void*>(scale_up)})
+        if (!p || !aligned(p, 16)) return SBL_ERR_INVALID_ARG;
+    const size_t need = sbl::ffn_backward_workspace_bytes(T, K, F, dX != nullptr, dW_gate || dW_up);
+    if (!workspace || !aligned(workspace, 256) || workspace_bytes < need) return SBL_ERR_WORKSPACE;
+    DeviceInfo* d;
+    if (sbl_status s = device_info(&d)) return s;
+    return from_cuda(sbl::launch_ffn_backward(dh, x_bf16, T, K, packed_gate, scale_gate, packed_up, scale_up, F, act, dX,
+                                              dW_gate, dW_up, (flags & SBL_BWD_DW_TERNARY) != 0, workspace, d->status,
+                                              d->num_sms, st));
 }
 
 // Sizes of the cross entropy: extents that the kernels hold in int32.

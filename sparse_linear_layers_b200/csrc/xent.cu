@@ -50,27 +50,6 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// 32 columns of a row as bf16 into half H of the warp's box; the second half
-// sends the box of 64 columns.
-__device__ __forceinline__ void put_bf16(const GemmTile& t, int k, const float (&v)[32], const CUtensorMap* map) {
-    const int h = k & 1;
-    if (h == 0) box_wait(t.lane);
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-        box_put(t.box, t.lane, 4 * h + c, pack_bf16(v[8 * c], v[8 * c + 1]), pack_bf16(v[8 * c + 2], v[8 * c + 3]),
-                pack_bf16(v[8 * c + 4], v[8 * c + 5]), pack_bf16(v[8 * c + 6], v[8 * c + 7]));
-    if (h == 1) {
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (t.lane == 0) tma_store_2d(map, smem_u32(t.box), t.col0 + 32 * (k - 1), t.warp_row);
-    }
-}
-
 // Forward epilogue: part[p][t] = (max, sum of exp(z - max)) over columns 128 p .. + 127.
 struct LsePart {
     struct Params {
@@ -177,17 +156,7 @@ struct SumF32 {
     __device__ __forceinline__ explicit SumF32(const Params& q) : p(q) {}
     __device__ __forceinline__ void begin(const GemmTile&) {}
     __device__ __forceinline__ void slice(const GemmTile& t, int k, float (&v)[32]) {
-        box_wait(t.lane);
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-            box_put(t.box, t.lane, c, __float_as_uint(v[4 * c]), __float_as_uint(v[4 * c + 1]),
-                    __float_as_uint(v[4 * c + 2]), __float_as_uint(v[4 * c + 3]));
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (t.lane == 0) {
-            if (p.add) tma_add_2d(&p.out, smem_u32(t.box), t.col0 + 32 * k, t.warp_row);
-            else tma_store_2d(&p.out, smem_u32(t.box), t.col0 + 32 * k, t.warp_row);
-        }
+        put_f32(t, k, v, &p.out, 0, p.add != 0);
     }
     __device__ __forceinline__ void end(const GemmTile&) {}
 };

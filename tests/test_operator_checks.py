@@ -133,3 +133,56 @@ def test_cross_entropy_tensor_checks(rec):
     for g in bad:
         with pytest.raises(ValueError):
             g()
+
+
+def test_ffn_gated_rejects_on_host():
+    from sparse_linear_layers_b200._lib import lib
+    p, big = 4096, 1 << 40
+    F = lib.sbl_ffn_gated
+    assert F(None, 0, 64, None, None, None, None, 8, 2, 4, 0, None, 1, None, 0, None) == 0     # T == 0
+    assert F(None, 4, 64, None, None, None, None, 0, 2, 4, 0, None, 1, None, 0, None) == 0     # F == 0
+    assert F(p, 4, 40, p, p, p, p, 8, 2, 4, 0, p, 1, p, big, None) == 1                        # K % 16 != 0
+    assert F(p, 4, 64, p, p, p, p, 8, 1, 4, 0, p, 1, p, big, None) == 2                        # pattern
+    assert F(p, 4, 64, p, p, p, p, 8, 2, 4, 2, p, 1, p, big, None) == 1                        # activation
+    assert F(p, 4, 64, p, p, p, p, 8, 2, 4, 0, p, 2, p, big, None) == 1                        # output type
+    assert F(p, 4, 64, p, p, None, p, 8, 2, 4, 0, p, 1, p, big, None) == 1                     # no up matrix
+    assert F(p, 4, 64, p, p, p, p + 4, 8, 2, 4, 0, p, 1, p, big, None) == 1                    # unaligned scale
+    assert F(p, 1 << 25, 64, p, p, p, p, 8, 2, 4, 0, p, 1, p, big, None) == 2
+    assert F(p, 4, 1 << 18, p, p, p, p, 8, 2, 4, 0, p, 1, p, big, None) == 2
+    assert lib.sbl_ffn_gated_workspace_bytes(16, 2048, 7168) == 0
+    need = lib.sbl_ffn_gated_workspace_bytes(17, 64, 8)
+    assert need == 17 * 64 + 192 + 256                 # x_q rounded to 256, s_tok
+    assert F(p, 17, 64, p, p, p, p, 8, 2, 4, 0, p, 1, None, big, None) == 6
+    assert F(p, 17, 64, p, p, p, p, 8, 2, 4, 0, p, 1, p + 64, big, None) == 6
+    assert F(p, 17, 64, p, p, p, p, 8, 2, 4, 0, p, 1, p, need - 1, None) == 6
+    B = lib.sbl_ffn_gated_backward
+    assert B(p, p, 4, 64, p, p, p, p, 8, 2, 4, 0, None, None, None, 0, p, big, None) == 1      # no output
+    assert B(p, p, 4, 64, p, p, p, p, 8, 2, 4, 0, p, None, None, 2, p, big, None) == 1         # flags
+    assert B(None, p, 4, 64, p, p, p, p, 8, 2, 4, 0, p, None, None, 0, p, big, None) == 1      # no dh
+    assert B(p, p, 4, 64, p, p, p, p, 8, 2, 4, 0, p, p + 4, None, 0, p, big, None) == 1        # unaligned dW
+    need = lib.sbl_ffn_gated_backward_workspace_bytes(4, 64, 8, 1, 0)
+    assert need > 0 and B(p, p, 4, 64, p, p, p, p, 8, 2, 4, 0, p, None, None, 0, p, need - 1, None) == 6
+    assert B(p, p, 4, 64, p, p, p, p, 8, 2, 4, 0, p, None, None, 0, None, big, None) == 6
+
+
+def test_ffn_gated_tensor_checks(rec):
+    def weights(F=8, K=64, n=2, m=4):
+        return api.PreparedWeights(torch.zeros((F, K // 4), dtype=torch.uint8), torch.zeros(F), n, m, K)
+
+    x, g, u, dh = torch.zeros(4, 64).bfloat16(), weights(), weights(), torch.zeros(4, 8)
+    rec.sbl_ffn_gated_workspace_bytes = lambda *a: 0
+    rec.sbl_ffn_gated_backward_workspace_bytes = lambda *a: 16
+    api.sbl_ffn_gated(x, g, u)
+    api.sbl_ffn_gated_backward(dh, x, g, u)
+    assert rec.calls == ["sbl_ffn_gated", "sbl_ffn_gated_backward"]
+    short = api.PreparedWeights(g.packed, torch.zeros(7), 2, 4, 64)
+    bad = [lambda: api.sbl_ffn_gated(x.float(), g, u), lambda: api.sbl_ffn_gated(x[0], g, u),
+           lambda: api.sbl_ffn_gated(x, g, weights(F=9)), lambda: api.sbl_ffn_gated(x, g, weights(K=128)),
+           lambda: api.sbl_ffn_gated(x, g, weights(n=3)), lambda: api.sbl_ffn_gated(x, g, short),
+           lambda: api.sbl_ffn_gated(x, g, u, act="gelu"), lambda: api.sbl_ffn_gated(x, g, u, out_dtype=torch.float16),
+           lambda: api.sbl_ffn_gated(x, g, u, h=torch.zeros(4, 7)), lambda: api.sbl_ffn_gated(x, g, u, h=torch.zeros(8, 4).t()),
+           lambda: api.sbl_ffn_gated_backward(dh[:, :4], x, g, u), lambda: api.sbl_ffn_gated_backward(dh.bfloat16(), x, g, u),
+           lambda: api.sbl_ffn_gated_backward(dh, x, g, u, need_dx=False, need_dgate=False, need_dup=False)]
+    for f in bad:
+        with pytest.raises(ValueError):
+            f()
