@@ -26,11 +26,13 @@ _TRAIN = ("SparseBitLinear", "SparseBitLinearFunction")
 def __getattr__(name):
     if name in _TRAIN:
         from . import train
-        return getattr(train, name)
+        globals()[name] = value = getattr(train, name)  # found without this function from now on
+        return value
     if name in _API:
         from . import api
         from ._lib import SblError
-        return SblError if name == "SblError" else getattr(api, name)
+        globals()[name] = value = SblError if name == "SblError" else getattr(api, name)
+        return value
     raise AttributeError(name)
 
 

@@ -29,6 +29,9 @@ def _need_cuda(t: torch.Tensor, name: str, dtype: torch.dtype, shape=None, devic
     (and, when given, exactly ``shape`` and on ``device``): the kernels write
     and read through raw pointers, so a tensor of the wrong size or on another
     GPU must never reach them."""
+    if (t.dtype is dtype and (shape is None or t.shape == shape) and (device is None or t.device == device)
+            and t.is_contiguous() and t.is_cuda):
+        return  # the usual case in one expression; what follows says what is wrong
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if shape is not None and tuple(t.shape) != tuple(shape):
@@ -58,29 +61,35 @@ def _need_workspace(ws: torch.Tensor, device) -> None:
     _need_cuda(ws, "workspace", torch.uint8, None, device)
 
 
+# The current stream's handle of a device, without building a Stream object.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 class _LaunchOn:
     """``with _LaunchOn(device, stream) as handle``: makes ``device`` current, and
     ``stream`` when one is given, for a call: the kernels run there, and what
     the call allocates belongs to that stream."""
-    __slots__ = ("_held",)
+    __slots__ = ("_index", "_held")
 
     def __init__(self, device, stream: Optional[torch.cuda.Stream]):
-        if stream is not None and stream.device != device:
-            raise ValueError(f"stream is on {stream.device}, the operands on {device}")
-        self._held = ()
+        self._index = device.index
+        self._held = None
         if stream is not None:
-            self._held = (torch.cuda.stream(stream),)  # makes its device current as well
+            if stream.device != device:
+                raise ValueError(f"stream is on {stream.device}, the operands on {device}")
+            self._held = torch.cuda.stream(stream)  # makes its device current as well
         elif device.index != torch.cuda.current_device():
-            self._held = (torch.cuda.device(device),)
+            self._held = torch.cuda.device(device)
 
     def __enter__(self) -> int:
-        for c in self._held:
-            c.__enter__()
-        return torch.cuda.current_stream().cuda_stream
+        if self._held is not None:
+            self._held.__enter__()
+        return _raw_stream(self._index)
 
     def __exit__(self, *exc) -> None:
-        for c in reversed(self._held):
-            c.__exit__(*exc)
+        if self._held is not None:
+            self._held.__exit__(*exc)
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -228,10 +237,10 @@ def sbl_norm(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor]
     with _LaunchOn(x.device, stream) as st:
         if y is None:
             y = torch.empty_like(x)
-        _need_cuda(y, "y", x.dtype, (T, K), x.device)
-        stat = lambda: torch.empty((T,), dtype=torch.float32, device=x.device)
-        mean = stat() if with_stats and kind == "layer" else None
-        rstd = stat() if with_stats else None
+        else:
+            _need_cuda(y, "y", x.dtype, (T, K), x.device)
+        mean = weight.new_empty((T,)) if with_stats and kind == "layer" else None
+        rstd = weight.new_empty((T,)) if with_stats else None
         check(lib.sbl_norm(x.data_ptr(), _DTYPES[x.dtype], T, K, _NORM_KINDS[kind], weight.data_ptr(), _ptr(bias),
                            float(eps), y.data_ptr(), _ptr(mean), _ptr(rstd), st), "sbl_norm")
     return (y, mean, rstd) if with_stats else y
@@ -260,8 +269,8 @@ def sbl_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, m
         raise ValueError("ask for dx, dweight or dbias")
     with _LaunchOn(dev, stream) as st:
         dx = torch.empty_like(x) if need_dx else None
-        dw = torch.empty((K,), dtype=torch.float32, device=dev) if need_dw else None
-        db = torch.empty((K,), dtype=torch.float32, device=dev) if need_db else None
+        dw = torch.empty_like(weight) if need_dw else None
+        db = torch.empty_like(weight) if need_db else None
         ws = None
         if need_dw or need_db:
             ws = _scratch(sbl_norm_backward_workspace_bytes(T, K, x.dtype), workspace, dev)
@@ -557,11 +566,12 @@ def _need_ffn(x: torch.Tensor, gate: PreparedWeights, up: PreparedWeights, act: 
         raise ValueError(f"act must be one of {sorted(_ACTS)}, got {act!r}")
     T, K = _need_2d(x, "x")
     _need_cuda(x, "x", torch.bfloat16)
-    for w in (gate, up):
-        if w.K != K or w.O != gate.O or (w.n, w.m) != (gate.n, gate.m):
-            raise ValueError("gate and up must have the activations' K, one number of rows and one N:M pattern")
-        _need_weights(w, x.device)
-    return T, K, gate.O
+    F = gate.O
+    if gate.K != K or up.K != K or up.O != F or up.n != gate.n or up.m != gate.m:
+        raise ValueError("gate and up must have the activations' K, one number of rows and one N:M pattern")
+    _need_weights(gate, x.device)
+    _need_weights(up, x.device)
+    return T, K, F
 
 
 def sbl_ffn_gated_workspace_bytes(T: int, K: int, F: int) -> int:
@@ -576,11 +586,12 @@ def sbl_ffn_gated(x: torch.Tensor, gate: PreparedWeights, up: PreparedWeights, a
     two prepared matrices of one shape; ``act`` is "silu" or "relu2" (max(g, 0)^2)."""
     T, K, F = _need_ffn(x, gate, up, act)
     with _LaunchOn(x.device, stream) as st:
-        if h is None:
-            h = torch.empty((T, F), dtype=out_dtype, device=x.device)
-        if h.dtype not in _DTYPES:
+        if (out_dtype if h is None else h.dtype) not in _DTYPES:
             raise ValueError("h must be float32 or bfloat16")
-        _need_cuda(h, "h", h.dtype, (T, F), x.device)
+        if h is None:
+            h = x.new_empty((T, F), dtype=out_dtype)
+        else:
+            _need_cuda(h, "h", h.dtype, (T, F), x.device)
         need = sbl_ffn_gated_workspace_bytes(T, K, F)
         ws = _scratch(need, workspace, x.device) if need or workspace is not None else None
         check(lib.sbl_ffn_gated(x.data_ptr(), T, K, gate.packed.data_ptr(), gate.row_scale.data_ptr(),
@@ -640,7 +651,8 @@ def sbl_linear_cross_entropy(x: torch.Tensor, W: torch.Tensor, target: torch.Ten
     [T]; tokens whose target is ``ignore_index`` have loss 0."""
     T, D, V = _need_xent(x, W, target)
     with _LaunchOn(x.device, stream) as st:
-        loss, lse = torch.empty((2, (T + 3) // 4 * 4), dtype=torch.float32, device=x.device)[:, :T].unbind()
+        loss = x.new_empty((T,), dtype=torch.float32)
+        lse = torch.empty_like(loss)
         ws = _scratch(sbl_linear_cross_entropy_workspace_bytes(T, V), workspace, x.device)
         check(lib.sbl_linear_cross_entropy(x.data_ptr(), T, D, W.data_ptr(), V, target.data_ptr(), ignore_index,
                                            loss.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel(), st),

@@ -70,7 +70,7 @@ cudaError_t launch_norm_fwd(const void* x, int bf16, int layer, const float* w, 
                             long long K, void* y, float* mean, float* rstd, int num_sms, cudaStream_t st);
 cudaError_t launch_norm_bwd(const void* dy, const void* x, int bf16, int layer, const float* w, const float* mean,
                             const float* rstd, long long T, long long K, void* dx, float* dw, float* db, float* part,
-                            int num_sms, cudaStream_t st);
+                            unsigned* status, int num_sms, cudaStream_t st);
 size_t ffn_workspace_bytes(long long T, long long K, long long F);
 size_t ffn_backward_workspace_bytes(long long T, long long K, long long F, int need_dx, int need_dw);
 cudaError_t launch_ffn(const uint16_t* x, long long T, long long K, const uint8_t* pg, const float* scale_g,
@@ -294,7 +294,7 @@ sbl_status sbl_norm_backward(const void* dy, const void* x, int dtype, int64_t T
     if (sums && workspace_bytes < sbl::norm_bwd_part_bytes(T, K, dtype == SBL_BF16, d->num_sms))
         return SBL_ERR_WORKSPACE;
     return from_cuda(sbl::launch_norm_bwd(dy, x, dtype == SBL_BF16, kind == SBL_NORM_LAYER, weight, mean, rstd, T, K, dx,
-                                          dweight, dbias, static_cast<float*>(workspace), d->num_sms, st));
+                                          dweight, dbias, static_cast<float*>(workspace), d->status, d->num_sms, st));
 }
 
 sbl_status sbl_mask_monitor(const uint8_t* old_bits, const uint8_t* new_bits, int64_t O, int64_t K, int n, int m,
