@@ -1084,7 +1084,7 @@ cudaError_t launch_ffn_backward(const float* dh, const uint16_t* x, long long T,
     if (cudaError_t e = pdl_launch(ffn_operands_kernel, dim3(o.split_blocks + o.code_blocks + o.x_blocks), dim3(256), 0, st, o))
         return e;
 
-    const int k_tiles = (Ki + gm::BN - 1) / gm::BN;
+    const int k_panel = (Ki + gm::BN - 1) / gm::BN;
     if (dx) {
         CUtensorMap a, b;
         FfnDx::Params p;
@@ -1095,7 +1095,7 @@ cudaError_t launch_ffn_backward(const float* dh, const uint16_t* x, long long T,
         p.row_max = row_max;
         p.s_tok = q.s_tok;
         p.T = Ti;
-        if (cudaError_t e = launch_gemm_f16<FfnDx, 2, false, true, true, 4>(a, b, p, GemmShape{Ti, Ki, 2 * Fp, 2 * Fp, k_tiles},
+        if (cudaError_t e = launch_gemm_f16<FfnDx, 2, 1, false, true, true, 4>(a, b, p, GemmShape{Ti, Ki, 2 * Fp, 2 * Fp, k_panel, 1, 0},
                                                                             status, st))
             return e;
     }
@@ -1115,7 +1115,7 @@ cudaError_t launch_ffn_backward(const float* dh, const uint16_t* x, long long T,
         p.want_g = dwg != nullptr;
         p.want_u = dwu != nullptr;
         p.ternary = ternary;
-        if (cudaError_t e = launch_gemm_f16<FfnDw, 2, true, true, true, 4>(a, b, p, GemmShape{2 * Fp, Ki, Ti, 2 * Fp, k_tiles},
+        if (cudaError_t e = launch_gemm_f16<FfnDw, 2, 1, true, true, true, 4>(a, b, p, GemmShape{2 * Fp, Ki, Ti, 2 * Fp, k_panel, 1, 0},
                                                                            status, st))
             return e;
     }

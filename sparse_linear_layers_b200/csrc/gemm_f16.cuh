@@ -11,8 +11,15 @@
 // with m or n along its rows (MN-major: [k, m] row-major, two boxes of 64
 // columns per stage), so no operand is transposed in memory.
 //
-// Two accumulator buffers (all 512 TMEM columns) let the eight epilogue warps
-// read one while the MMAs fill the other.
+// MH = 1: two accumulator buffers (all 512 TMEM columns) let the eight epilogue
+// warps read one while the MMAs fill the other.
+// MH = 2: tiles of 512 x 256, both buffers one tile's (its upper and lower 256
+// rows), so B is loaded once for twice the rows.  What feeds the MMAs bounds
+// this GEMM: L2 delivers about 9 TB/s to the SMs whatever the kernel (measured on
+// four of them), 7.8 KB per MFLOP of a 256 x 256 tile and 5.9 KB of a 512 x 256
+// one.  The MMAs of the next tile wait until the epilogue has read a half, while
+// the loads run on for four stages.  (Letting the upper half's MMAs run ahead
+// through those stages made the whole 3% slower: their stages come back later.)
 //
 // SEGMENT > 0: the tensor cores round every fp32 accumulation towards zero, an
 // error that grows with the number of MMAs summed into one accumulator (a
@@ -45,25 +52,25 @@ constexpr int WARP_TMA = 8;
 constexpr int WARP_MMA = 9;
 constexpr int THREADS = 320;
 constexpr int BOX = 32 * 128;       // one warp's staging box: 32 rows x 128 bytes
-constexpr int stages(int na) { return na == 1 ? 6 : 4; }
+constexpr int stages(int tiles) { return tiles == 1 ? 6 : 4; }  // by A tiles of a stage
 }  // namespace gm
 
-template <int NA>
+template <int AT>
 struct GemmSmem {
-    uint8_t a[gm::stages(NA)][NA][gm::TILE];  // 1024-byte aligned tiles
-    uint8_t b[gm::stages(NA)][gm::TILE];
+    uint8_t a[gm::stages(AT)][AT][gm::TILE];  // 1024-byte aligned tiles
+    uint8_t b[gm::stages(AT)][gm::TILE];
     uint8_t box[gm::EPI_WARPS][gm::BOX];
-    uint64_t full[gm::stages(NA)];            // used in the even CTA
-    uint64_t empty[gm::stages(NA)];
+    uint64_t full[gm::stages(AT)];            // used in the even CTA
+    uint64_t empty[gm::stages(AT)];
     uint64_t tmem_full[2];
     uint64_t tmem_empty[2];                   // used in the even CTA
     uint64_t mma_done;
     uint32_t tmem_base;
     int abort_flag;
 };
-template <int NA>
+template <int AT>
 constexpr size_t gemm_smem_bytes() {
-    return sizeof(GemmSmem<NA>) + 1024;
+    return sizeof(GemmSmem<AT>) + 1024;
 }
 static_assert(gemm_smem_bytes<1>() <= 232448 && gemm_smem_bytes<2>() <= 232448, "GEMM stages do not fit");
 
@@ -73,13 +80,16 @@ static_assert(gemm_smem_bytes<1>() <= 232448 && gemm_smem_bytes<2>() <= 232448, 
 struct GemmShape {
     int M, N, K;
     int a_part;
-    int panel;  // consecutive tiles walk across `panel` column tiles, then down M
+    int panel;      // consecutive tiles walk across `panel` column tiles, then down M
+    int splits;     // parts of the reduction, each a GEMM of its own into rows
+    int split_rows; // split_rows further down (a multiple of the tile's rows)
 };
 
 struct GemmTile {
     int m0, n0;       // first row and column of the pair's tile
     int row;          // this thread's row
     int warp_row;     // first row of this warp
+    int out_row;      // where that row goes: warp_row, further down for later splits
     int col0;         // first of this warp's 128 columns
     int lane;
     uint8_t* box;     // this warp's staging box
@@ -139,23 +149,28 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// 32 columns of a row as bf16 into one half of the warp's box; the second
-// half sends the box of 64 columns.
+// 32 columns of a row as bf16 through one half of the warp's box (32 rows x 64
+// bytes, 64B swizzle): slice k uses half k mod 2 and waits only for the store
+// before the last one.
 __device__ __forceinline__ void put_bf16(const GemmTile& t, int k, const float (&v)[32], const CUtensorMap* map) {
-    const int h = k & 1;
-    if (h == 0) box_wait(t.lane);
+    uint8_t* const half = t.box + (k & 1) * (gm::BOX / 2);
+    if (t.lane == 0) bulk_wait_read<1>();
+    __syncwarp();
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-        box_put(t.box, t.lane, 4 * h + c, pack_bf16(v[8 * c], v[8 * c + 1]), pack_bf16(v[8 * c + 2], v[8 * c + 3]),
-                pack_bf16(v[8 * c + 4], v[8 * c + 5]), pack_bf16(v[8 * c + 6], v[8 * c + 7]));
-    if (h == 1) {
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (t.lane == 0) tma_store_2d(map, smem_u32(t.box), t.col0 + 32 * (k - 1), t.warp_row);
+    for (int c = 0; c < 4; ++c) {
+        // 16-byte unit c of row r at c ^ (r / 2 mod 4)
+        const uint32_t a = smem_u32(half + t.lane * 64 + ((c ^ ((t.lane >> 1) & 3)) << 4));
+        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(pack_bf16(v[8 * c], v[8 * c + 1])),
+                     "r"(pack_bf16(v[8 * c + 2], v[8 * c + 3])), "r"(pack_bf16(v[8 * c + 4], v[8 * c + 5])),
+                     "r"(pack_bf16(v[8 * c + 6], v[8 * c + 7]))
+                     : "memory");
     }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (t.lane == 0) tma_store_2d(map, smem_u32(half), t.col0 + 32 * k, t.out_row);
 }
 
-// 32 fp32 columns of a row through the warp's box to rows warp_row - row0 of
+// 32 fp32 columns of a row through the warp's box to rows out_row - row0 of
 // a matrix; added to what is there when `add`.
 __device__ __forceinline__ void put_f32(const GemmTile& t, int k, const float (&v)[32], const CUtensorMap* map, int row0,
                                         bool add) {
@@ -167,8 +182,8 @@ __device__ __forceinline__ void put_f32(const GemmTile& t, int k, const float (&
     fence_proxy_async_smem();
     __syncwarp();
     if (t.lane == 0) {
-        if (add) tma_add_2d(map, smem_u32(t.box), t.col0 + 32 * k, t.warp_row - row0);
-        else tma_store_2d(map, smem_u32(t.box), t.col0 + 32 * k, t.warp_row - row0);
+        if (add) tma_add_2d(map, smem_u32(t.box), t.col0 + 32 * k, t.out_row - row0);
+        else tma_store_2d(map, smem_u32(t.box), t.col0 + 32 * k, t.out_row - row0);
     }
 }
 
@@ -176,22 +191,25 @@ __device__ __forceinline__ void put_f32(const GemmTile& t, int k, const float (&
 //   struct Params (a kernel argument, may hold tensor maps), static prefetch(const Params&),
 //   Epi(const Params&), begin(const GemmTile&), slice(const GemmTile&, int k, float (&v)[32])
 //   for columns col0 + 32 k .. + 31 of the thread's row (k = 0..3 in order), end(const GemmTile&).
-template <class Epi, int NA, bool A_MN, bool B_MN, bool FP16, int SEGMENT>
+template <class Epi, int NA, int MH, bool A_MN, bool B_MN, bool FP16, int SEGMENT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gm::THREADS, 1)
     gemm_f16_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
                     const __grid_constant__ typename Epi::Params params, const GemmShape shape, unsigned* status) {
-    constexpr int STAGES = gm::stages(NA);
+    static_assert(MH == 1 || (NA == 1 && SEGMENT == 0), "a tall tile has one A and one sum per row");
+    constexpr int AT = NA * MH;  // A tiles of a stage
+    constexpr int STAGES = gm::stages(AT);
+    constexpr int ROWS = 2 * gm::BM * MH;  // rows of a tile
     extern __shared__ uint8_t smem_raw[];
-    auto* sm = reinterpret_cast<GemmSmem<NA>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    auto* sm = reinterpret_cast<GemmSmem<AT>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     volatile int* abort_flag = &sm->abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const bool leader = rank == 0;
     const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
-    const int MT = (shape.M + 2 * gm::BM - 1) / (2 * gm::BM), NT = (shape.N + gm::BN - 1) / gm::BN;
-    const int tiles = MT * NT;
-    const int KB = (shape.K + gm::BK - 1) / gm::BK;
-    const int SEG = SEGMENT > 0 ? SEGMENT : KB;
+    const int MT = (shape.M + ROWS - 1) / ROWS, NT = (shape.N + gm::BN - 1) / gm::BN;
+    const int tiles = MT * NT * shape.splits;
+    const int KB_ALL = (shape.K + gm::BK - 1) / gm::BK;
+    const int KB = (KB_ALL + shape.splits - 1) / shape.splits;  // k-blocks of a part; those past the end read zeros
 
     asm volatile("griddepcontrol.launch_dependents;");
     if (threadIdx.x == 32) {
@@ -232,11 +250,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gm::THREADS, 1)
     };
     // tiles go panel by panel of column tiles, row by row of a panel: the
     // panel's B tiles stay in L2 while A streams past them once per panel
-    auto tile_at = [&](int tile, int& m0, int& n0) {
+    auto tile_at = [&](int tile, int& m0, int& n0, int& split) {
+        split = shape.splits > 1 ? tile / (MT * NT) : 0;
+        tile -= split * MT * NT;
         const int first = tile / (MT * shape.panel) * shape.panel;
         const int rem = tile - first * MT;
         const int width = NT - first < shape.panel ? NT - first : shape.panel;
-        m0 = rem / width * (2 * gm::BM);
+        m0 = rem / width * ROWS;
         n0 = (first + rem % width) * gm::BN;
     };
 
@@ -257,20 +277,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gm::THREADS, 1)
                 else mbar_arrive_cluster(map_to_cta(smem_u32(&sm->tmem_empty[b]), 0));
             }
         };
-        for (int tile = pair; tile < tiles; tile += npairs) {
-            tile_at(tile, t.m0, t.n0);
-            t.warp_row = t.m0 + static_cast<int>(rank) * gm::BM + qd * 32;
-            t.row = t.warp_row + lane;
+        bool ok = true;
+        for (int tile = pair; tile < tiles && ok; tile += npairs) {
+            int split;
+            tile_at(tile, t.m0, t.n0, split);
             t.col0 = t.n0 + half * (gm::BN / 2);
-            epi.begin(t);
             if (SEGMENT > 0) {
+                t.warp_row = t.m0 + static_cast<int>(rank) * gm::BM + qd * 32;
+                t.row = t.warp_row + lane;
+                t.out_row = t.warp_row + split * shape.split_rows;
+                epi.begin(t);
                 float acc[4][32];
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
 #pragma unroll
                     for (int i = 0; i < 32; ++i) acc[k][i] = 0.f;
-                bool ok = true;
-                for (int kb = 0; kb < KB; kb += SEG, ++seg) {
+                for (int kb = 0; kb < KB; kb += SEGMENT > 0 ? SEGMENT : 1, ++seg) {
                     const int b = seg & 1;
                     if (!warp_wait(&sm->tmem_full[b], (seg >> 1) & 1, abort_flag)) { give_up(); ok = false; break; }
                     tc_fence_after();
@@ -288,29 +310,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gm::THREADS, 1)
                 if (!ok) break;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) epi.slice(t, k, acc[k]);
+                epi.end(t);
             } else {
-                const int b = seg & 1;
-                if (!warp_wait(&sm->tmem_full[b], (seg >> 1) & 1, abort_flag)) { give_up(); break; }
-                ++seg;
-                tc_fence_after();
-                const uint32_t tbase = tmem_base + lane_addr + b * gm::BN + half * (gm::BN / 2);
-                uint32_t ra[32], rb[32];
-                tmem_ld32_nowait(tbase, ra);
-                tmem_wait_into(ra);
+                // MH = 2: the upper, then the lower half of the tile, in buffers 0 and 1
+                for (int j = 0; j < MH; ++j, ++seg) {
+                    t.warp_row = t.m0 + 2 * gm::BM * j + static_cast<int>(rank) * gm::BM + qd * 32;
+                    t.row = t.warp_row + lane;
+                    t.out_row = t.warp_row + split * shape.split_rows;
+                    epi.begin(t);
+                    const int b = seg & 1;
+                    if (!warp_wait(&sm->tmem_full[b], (seg >> 1) & 1, abort_flag)) { give_up(); ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t tbase = tmem_base + lane_addr + b * gm::BN + half * (gm::BN / 2);
+                    uint32_t ra[32], rb[32];
+                    tmem_ld32_nowait(tbase, ra);
+                    tmem_wait_into(ra);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    uint32_t(&cur)[32] = k & 1 ? rb : ra;
-                    uint32_t(&nxt)[32] = k & 1 ? ra : rb;
-                    if (k < 3) tmem_ld32_nowait(tbase + 32 * (k + 1), nxt);
-                    else release(b);
-                    float v[32];
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t(&cur)[32] = k & 1 ? rb : ra;
+                        uint32_t(&nxt)[32] = k & 1 ? ra : rb;
+                        if (k < 3) tmem_ld32_nowait(tbase + 32 * (k + 1), nxt);
+                        else release(b);
+                        float v[32];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(cur[i]);
-                    epi.slice(t, k, v);
-                    if (k < 3) tmem_wait_into(nxt);
+                        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(cur[i]);
+                        epi.slice(t, k, v);
+                        if (k < 3) tmem_wait_into(nxt);
+                    }
+                    epi.end(t);
                 }
             }
-            epi.end(t);
         }
         if (lane == 0) bulk_wait_all();
     } else if (warp == gm::WARP_TMA) {
@@ -319,24 +348,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gm::THREADS, 1)
             uint32_t it = 0;
             bool ok = true;
             for (int tile = pair; tile < tiles && ok; tile += npairs) {
-                int m0, n0;
-                tile_at(tile, m0, n0);
+                int m0, n0, split;
+                tile_at(tile, m0, n0, split);
                 const int arow = m0 + static_cast<int>(rank) * gm::BM, brow = n0 + static_cast<int>(rank) * gm::BM;
                 for (int kb = 0; kb < KB; ++kb, ++it) {
                     const int s = it % STAGES;
                     if (!mbar_wait(&sm->empty[s], ((it / STAGES) & 1) ^ 1, abort_flag)) { give_up(); ok = false; break; }
                     // the even CTA expects the bytes of both CTAs
-                    if (leader) mbar_arrive_expect_tx(&sm->full[s], 2 * (NA + 1) * gm::TILE);
+                    if (leader) mbar_arrive_expect_tx(&sm->full[s], 2 * (AT + 1) * gm::TILE);
                     const uint32_t full = map_to_cta(smem_u32(&sm->full[s]), 0);
-                    const int k0 = kb * gm::BK;
+                    const int k0 = (split * KB + kb) * gm::BK;
 #pragma unroll
-                    for (int j = 0; j < NA; ++j) {
+                    for (int j = 0; j < AT; ++j) {
                         const uint32_t dst = smem_u32(sm->a[s][j]);
+                        const int part = MH == 2 ? 0 : j * shape.a_part, r = arow + (MH == 2 ? 2 * gm::BM * j : 0);
                         if (A_MN) {
-                            tma_load_2d_pair(dst, &tmap_a, j * shape.a_part + arow, k0, full);
-                            tma_load_2d_pair(dst + gm::TILE / 2, &tmap_a, j * shape.a_part + arow + 64, k0, full);
+                            tma_load_2d_pair(dst, &tmap_a, part + r, k0, full);
+                            tma_load_2d_pair(dst + gm::TILE / 2, &tmap_a, part + r + 64, k0, full);
                         } else {
-                            tma_load_2d_pair(dst, &tmap_a, j * shape.a_part + k0, arow, full);
+                            tma_load_2d_pair(dst, &tmap_a, part + k0, r, full);
                         }
                     }
                     const uint32_t dst = smem_u32(sm->b[s]);
@@ -366,33 +396,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gm::THREADS, 1)
                                        (static_cast<uint32_t>((2 * gm::BM) >> 4) << 24);
                 uint32_t it = 0, seg = 0;
                 bool ok = true;
+                // buffer of the seg-th accumulation, once the epilogue has read what it held
+                auto take = [&](uint32_t sg) {
+                    if (!mbar_wait(&sm->tmem_empty[sg & 1], ((sg >> 1) & 1) ^ 1, abort_flag)) return false;
+                    tc_fence_after();
+                    return true;
+                };
+                // the MMAs of one k-block (stage of iteration i) on A tile j
+                auto issue = [&](uint32_t i, int j, uint32_t d, bool fresh) {
+                    const uint32_t a0 = smem_u32(sm->a[i % STAGES][j]), b0 = smem_u32(sm->b[i % STAGES]);
+#pragma unroll
+                    for (int kk = 0; kk < gm::BK / 16; ++kk)
+                        tc_mma_pair_f16(d, A_MN ? sw128_mn_desc(a0 + kk * 2048) : sw128_desc(a0 + kk * 32),
+                                        B_MN ? sw128_mn_desc(b0 + kk * 2048) : sw128_desc(b0 + kk * 32), idesc,
+                                        !(fresh && kk == 0));
+                };
+                auto loaded = [&](uint32_t i) { return mbar_wait(&sm->full[i % STAGES], (i / STAGES) & 1, abort_flag); };
                 for (int tile = pair; tile < tiles && ok; tile += npairs) {
-                    uint32_t d = 0;
                     for (int kb = 0; kb < KB; ++kb, ++it) {
-                        const bool first = SEGMENT > 0 ? kb % (SEGMENT > 0 ? SEGMENT : 1) == 0 : kb == 0;
-                        if (first) {
-                            const int b = seg & 1;
-                            if (!mbar_wait(&sm->tmem_empty[b], ((seg >> 1) & 1) ^ 1, abort_flag)) { give_up(); ok = false; break; }
-                            tc_fence_after();
-                            d = tmem_base + b * gm::BN;
+                        bool first = kb == 0, last = kb == KB - 1;
+                        if constexpr (SEGMENT > 0) {
+                            first = kb % SEGMENT == 0;
+                            last = last || kb % SEGMENT == SEGMENT - 1;
                         }
-                        const int s = it % STAGES;
-                        if (!mbar_wait(&sm->full[s], (it / STAGES) & 1, abort_flag)) { give_up(); ok = false; break; }
+                        if (first && !take(seg)) { give_up(); ok = false; break; }
+                        if (!loaded(it)) { give_up(); ok = false; break; }
                         tc_fence_after();
-                        const uint32_t b0 = smem_u32(sm->b[s]);
+                        if constexpr (MH == 2) {
+                            // upper half, then lower half; the lower buffer comes back later
+                            issue(it, 0, tmem_base + (seg & 1) * gm::BN, first);
+                            if (last) tc_commit_pair_both(&sm->tmem_full[seg & 1]);
+                            if (first && !take(seg + 1)) { give_up(); ok = false; break; }
+                            issue(it, 1, tmem_base + ((seg + 1) & 1) * gm::BN, first);
+                        } else {
 #pragma unroll
-                        for (int j = 0; j < NA; ++j) {
-                            const uint32_t a0 = smem_u32(sm->a[s][j]);
-#pragma unroll
-                            for (int kk = 0; kk < gm::BK / 16; ++kk)
-                                tc_mma_pair_f16(d, A_MN ? sw128_mn_desc(a0 + kk * 2048) : sw128_desc(a0 + kk * 32),
-                                                B_MN ? sw128_mn_desc(b0 + kk * 2048) : sw128_desc(b0 + kk * 32), idesc,
-                                                !(first && j == 0 && kk == 0));
+                            for (int j = 0; j < NA; ++j) issue(it, j, tmem_base + (seg & 1) * gm::BN, first && j == 0);
                         }
-                        tc_commit_pair_both(&sm->empty[s]);
-                        if (kb == KB - 1 || (SEGMENT > 0 && kb % (SEGMENT > 0 ? SEGMENT : 1) == SEGMENT - 1)) {
-                            tc_commit_pair_both(&sm->tmem_full[seg & 1]);
-                            ++seg;
+                        tc_commit_pair_both(&sm->empty[it % STAGES]);
+                        if (last) {
+                            tc_commit_pair_both(&sm->tmem_full[(seg + MH - 1) & 1]);
+                            seg += MH;
                         }
                     }
                 }
@@ -416,9 +459,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gm::THREADS, 1)
 
 // ---------------------------------------------------------------- host side
 // Tensor map of a row-major [rows, cols] matrix of 2- or 4-byte elements with
-// a box of box_cols x box_rows (128-byte rows, 128B swizzle).
+// a box of box_cols x box_rows (rows of 128 bytes with the 128B swizzle, or of
+// 64 with the 64B one).
 inline bool gemm_map(CUtensorMap* map, CUtensorMapDataType type, const void* base, long long rows, long long cols,
-                     long long pitch_bytes, int box_cols, int box_rows) {
+                     long long pitch_bytes, int box_cols, int box_rows,
+                     CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
     EncodeTiledFn enc = get_encode_fn();
     if (!enc) return false;
     const cuuint32_t estr[2] = {1, 1};
@@ -426,8 +471,13 @@ inline bool gemm_map(CUtensorMap* map, CUtensorMapDataType type, const void* bas
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch_bytes)};
     const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)};
     return enc(map, type, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
-           CUDA_SUCCESS;
+               swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A bf16 result, stored by put_bf16.
+inline bool gemm_result_bf16(CUtensorMap* map, void* base, long long rows, long long cols, long long pitch_elems) {
+    return gemm_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, rows, cols, pitch_elems * 2, 32, 32,
+                    CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 // An operand of the GEMM: a 2-byte row-major matrix [rows, cols].  K-major
@@ -439,11 +489,12 @@ inline bool gemm_operand(CUtensorMap* map, bool fp16, bool mn_major, const void*
                     pitch_elems * 2, 64, mn_major ? 64 : gm::BM);
 }
 
-template <class Epi, int NA, bool A_MN, bool B_MN, bool FP16, int SEGMENT>
+template <class Epi, int NA, int MH, bool A_MN, bool B_MN, bool FP16, int SEGMENT>
 cudaError_t launch_gemm_f16(const CUtensorMap& a, const CUtensorMap& b, const typename Epi::Params& p,
                             const GemmShape& shape, unsigned* status, cudaStream_t stream) {
-    auto kern = gemm_f16_kernel<Epi, NA, A_MN, B_MN, FP16, SEGMENT>;
-    constexpr size_t smem = gemm_smem_bytes<NA>();
+    auto kern = gemm_f16_kernel<Epi, NA, MH, A_MN, B_MN, FP16, SEGMENT>;
+    constexpr size_t smem = gemm_smem_bytes<NA * MH>();
+    constexpr int rows = 2 * gm::BM * MH;
     static int clusters[64] = {};  // pairs of this kernel that fit on each device at once
     int dev = 0;
     if (cudaError_t e = cudaGetDevice(&dev)) return e;
@@ -461,8 +512,8 @@ cudaError_t launch_gemm_f16(const CUtensorMap& a, const CUtensorMap& b, const ty
         if (n <= 0) return cudaErrorNotSupported;
         clusters[dev] = n;
     }
-    const long long tiles = static_cast<long long>((shape.M + 2 * gm::BM - 1) / (2 * gm::BM)) *
-                            ((shape.N + gm::BN - 1) / gm::BN);
+    const long long tiles = static_cast<long long>((shape.M + rows - 1) / rows) * ((shape.N + gm::BN - 1) / gm::BN) *
+                            shape.splits;
     if (tiles <= 0 || tiles > (1ll << 30)) return cudaErrorInvalidValue;
     cfg.gridDim = dim3(2 * static_cast<unsigned>(tiles < clusters[dev] ? tiles : clusters[dev]));
     cudaLaunchAttribute attr[1];
@@ -471,6 +522,13 @@ cudaError_t launch_gemm_f16(const CUtensorMap& a, const CUtensorMap& b, const ty
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kern, a, b, p, shape, status);
+}
+
+// Whether 512-row tiles move fewer bytes than 256-row ones (48 KB against 32 KB
+// per k-block and CTA) over M rows and still give every pair of SMs one.
+inline bool gemm_tall(long long M, long long N, int splits, int num_sms) {
+    const long long tall = (M + 511) / 512, flat = (M + 255) / 256, cols = (N + gm::BN - 1) / gm::BN;
+    return 48 * tall < 32 * flat && tall * cols * splits >= num_sms / 2;
 }
 
 }  // namespace sbl

@@ -19,14 +19,14 @@
 // Forward: a group of warps holds its rows in registers between the sums and
 // the results; weights come from L1 once per two rows.  16384 x 4864 bf16:
 // 61 us, 79% of the copy bandwidth (8 columns, one row: 108 us).
-// Backward, many rows (more than two tiles per SM): one persistent block per
+// Backward, many rows: one persistent block per
 // SM whose column sums stay in registers.  A producer warp copies tiles of
 // whole rows (contiguous in memory) into a ring in shared memory with bulk
 // asynchronous copies, so loads are in flight whatever the sums wait for, and
 // the consumer warps read each tile twice from shared memory.  16384 x 4864
 // bf16: 92 us, 79%.
 // Backward, few rows: a row per group at a time straight from global memory,
-// without the ring's set-up (1021 x 896 fp32: 5.5 us, the ring 9 us).
+// without the ring's set-up (64 x 2048 bf16: 6.5 us, the ring 9.8 us).
 // Longer rows than kMaxColumns: the wide kernels, which read a row again from L2
 // in each pass.
 //
@@ -105,33 +105,6 @@ __device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
     f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
 }
 
-// Two fp32 values per instruction (each rounded to nearest like its scalar).
-__device__ __forceinline__ uint64_t pair_bits(float2 a) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
-    return r;
-}
-__device__ __forceinline__ float2 pair_of(uint64_t b) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(b));
-    return r;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair_bits(a)), "l"(pair_bits(b)));
-    return pair_of(r);
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair_bits(a)), "l"(pair_bits(b)));
-    return pair_of(r);
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pair_bits(a)), "l"(pair_bits(b)), "l"(pair_bits(c)));
-    return pair_of(r);
-}
-__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
 template <class Row>
 __device__ __forceinline__ void get_pairs(const Row& r, float2 (&f)[4]) {
     float v[8];
@@ -822,7 +795,9 @@ bool stream_choice(long long T, long long K, int es, int num_sms, StreamChoice& 
     if (p.stages < 2) return false;
     c.grid = num_sms;
     c.smem = p.stages * 2 * p.stage_bytes;
-    return (T + p.rows - 1) / p.rows > 2ll * num_sms;
+    // both kernels, us: 1021 x 896 fp32 direct 11.3, ring 11.5 (4096: 21.3, 18.1); 592 x 2048 bf16 9.0, 10.2
+    // (1021: 12.1, 10.3); 64 x 4864 bf16 7.8, 10.5 (296: 13.1, 11.0)
+    return T * K > 10000ll * num_sms;
 }
 
 // Blocks of the backward, each with a partial row of column sums.
@@ -860,8 +835,10 @@ cudaError_t fwd(const void* x, const float* w, const float* b, float eps, long l
         return pdl_launch(norm_fwd_wide_kernel<Row, LAYER>, dim3(static_cast<unsigned>(T < most ? T : most)),
                           dim3(nrm::WIDE_THREADS), 0, st, xp, w, b, eps, T, static_cast<int>(K), yp, mean, rstd);
     }
-    // few rows: more threads per row, each with less to do
-    const bool few = T < 4ll * num_sms && K <= nrm::kMaxDirect;
+    // few elements: more threads per row, each with less to do (us, 8 columns and one row against
+    // 32 and two: 2048 x 896 fp32 6.2, 7.5; 4096 x 896 9.2, 8.4; 592 x 2048 bf16 4.2, 4.8; 2048 x 2048 8.0, 6.2;
+    // 296 x 4864 bf16 4.3, 4.8; 592 x 4864 7.5, 5.8)
+    const bool few = T * K < 14000ll * num_sms && K <= nrm::kMaxDirect;
     const int nc = few ? 1 : columns_per_thread(K), r = few ? 1 : 2;
     const RowPlan p = row_plan(K, nc, 8);
     auto kern = few       ? norm_fwd_kernel<Row, LAYER, 1, 1>

@@ -188,6 +188,35 @@ __device__ __forceinline__ void expand_pairs(uint32_t w, uint32_t (&e)[4]) {
     e[3] = prmt(kTernaryBytes, 0u, hi >> 16);
 }
 
+// ---------------------------------------------------------------- fp32 pairs
+// Two fp32 values per instruction (each rounded to nearest like its scalar).
+__device__ __forceinline__ uint64_t pair_bits(float2 a) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
+    return r;
+}
+__device__ __forceinline__ float2 pair_of(uint64_t b) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(b));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair_bits(a)), "l"(pair_bits(b)));
+    return pair_of(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair_bits(a)), "l"(pair_bits(b)));
+    return pair_of(r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pair_bits(a)), "l"(pair_bits(b)), "l"(pair_bits(c)));
+    return pair_of(r);
+}
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+
 // ---------------------------------------------------------------- activation quantisation
 // round_half_even(x * s) for an activation x (as float) and its token's
 // s = 127 / max|x|, returned as the bit pattern of x * s + 1.5 * 2^23.  The

@@ -24,11 +24,13 @@
 // multiplied back into the fp32 results: under a mean or sum reduction G's
 // entry at an unlikely target is then -1 exactly.
 //
-// Bound by the tensor cores: 2 T V D operations forward, 6 T V D backward (a
-// third of them the second time z is computed, the price of not keeping it).
-// The epilogue's exponentials (one per logit: 2048 cycles of the SM's 16 per
-// clock for its 128 x 256 half tile) hide behind the next tile's MMAs (7168
-// cycles at D = 896).
+// Bound by what feeds the tensor cores (gemm_f16.cuh) and, over longer runs, by
+// the power limit: 2 T V D operations forward, 6 T V D backward (a third of them
+// the second time z is computed, the price of not keeping it).  At 8192 x
+// 128000 x 896 the four products take 6.9 ms, 1090 TFLOP/s (a library bf16 product
+// of 8192^3 sustains 1395); at 4096 x 32000 x 2048 1.8 ms, 1200 TFLOP/s.  The epilogues
+// spend about three instructions per logit on pairs of values; an index into
+// a row's registers anywhere in them would put the row into local memory.
 #include <cuda.h>
 
 #include "gemm_f16.cuh"
@@ -48,6 +50,12 @@ __device__ __forceinline__ float exp2_fast(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
 }
 
 // Forward epilogue: part[p][t] = (max, sum of exp(z - max)) over columns 128 p .. + 127.
@@ -85,14 +93,21 @@ struct LsePart {
             for (int i = 0; i < 32; ++i) z = (hot & (1u << i)) ? v[i] : z;
             p.tlogit[t.row] = z;
         }
-        float m4[4] = {v[0], v[1], v[2], v[3]};
+        float m4[4] = {mx, v[0], v[1], v[2]};
 #pragma unroll
-        for (int i = 4; i < 32; ++i) m4[i & 3] = fmaxf(m4[i & 3], v[i]);
-        const float m = fmaxf(mx, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
-        float s4[4] = {mx == -INFINITY ? 0.f : sum * exp2_fast((mx - m) * kLog2e), 0.f, 0.f, 0.f};
+        for (int i = 3; i < 31; i += 2) m4[(i >> 1) & 3] = max3(m4[(i >> 1) & 3], v[i], v[i + 1]);
+        const float m = fmaxf(max3(m4[0], m4[1], m4[2]), fmaxf(m4[3], v[31]));
+        // exp(z - m) = 2^(z log2 e - m log2 e): the fused product is exact, and the
+        // second's rounding (2^-24 |m log2 e|) moves lse by less than its own last bit
+        const float2 l2 = both(kLog2e), less = both(-m * kLog2e);
+        float2 s2[2] = {make_float2(mx == -INFINITY ? 0.f : sum * exp2_fast((mx - m) * kLog2e), 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int i = 0; i < 32; ++i) s4[i & 3] += exp2_fast((v[i] - m) * kLog2e);
-        sum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
+        for (int i = 0; i < 16; ++i) {
+            const float2 e = fma2(make_float2(v[2 * i], v[2 * i + 1]), l2, less);
+            s2[i & 1] = add2(s2[i & 1], make_float2(exp2_fast(e.x), exp2_fast(e.y)));
+        }
+        s2[0] = add2(s2[0], s2[1]);
+        sum = s2[0].x + s2[0].y;
         mx = m;
     }
     __device__ __forceinline__ void end(const GemmTile& t) {
@@ -114,32 +129,41 @@ struct GradTile {
     };
     static __device__ __forceinline__ void prefetch(const Params& p) { prefetch_tmap(&p.g); }
     const Params& p;
-    float lse, d;
+    float less, d;   // -lse log2 e; dloss / c
     long long tcol;
-    __device__ __forceinline__ explicit GradTile(const Params& q) : p(q), lse(0.f), d(0.f), tcol(-1) {}
+    __device__ __forceinline__ explicit GradTile(const Params& q) : p(q), less(0.f), d(0.f), tcol(-1) {}
     __device__ __forceinline__ void begin(const GemmTile& t) {
-        d = lse = 0.f;
+        d = 0.f;
         tcol = -1;
         if (t.row < p.T) {
             const long long y = __ldg(p.target + t.row);
             const float c = *p.cmax;
-            lse = __ldg(p.lse + t.row);
+            less = -__ldg(p.lse + t.row) * kLog2e;
             if (y != p.ignore && y >= 0 && y < p.V && c != 0.f) d = __fdiv_rn(__ldg(p.dloss + t.row), c);
             tcol = y - p.v0 - t.col0;
         }
+        if (d == 0.f) less = -INFINITY;  // exp becomes 0: the row writes zeros
     }
     __device__ __forceinline__ void slice(const GemmTile& t, int k, float (&v)[32]) {
+        const float2 l2 = both(kLog2e), ls = both(less);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = exp2_fast((v[i] - lse) * kLog2e);
+        for (int i = 0; i < 32; i += 2) {
+            const float2 e = fma2(make_float2(v[i], v[i + 1]), l2, ls);
+            v[i] = exp2_fast(e.x);
+            v[i + 1] = exp2_fast(e.y);
+        }
         const long long tc = tcol - 32 * k;
         if (tc >= 0 && tc < 32) {
             const uint32_t hot = 1u << tc;  // by a bit: see LsePart
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] -= (hot & (1u << i)) ? 1.0f : 0.0f;
         }
-        // a row without a target writes zeros, whatever its logits are
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = d == 0.f ? 0.f : v[i] * d;
+        for (int i = 0; i < 32; i += 2) {
+            const float2 g = mul2(make_float2(v[i], v[i + 1]), both(d));
+            v[i] = g.x;
+            v[i + 1] = g.y;
+        }
         put_bf16(t, k, v, &p.g);
     }
     __device__ __forceinline__ void end(const GemmTile&) {}
@@ -238,14 +262,22 @@ __global__ void __launch_bounds__(1024) xent_cmax_kernel(const float* __restrict
     }
 }
 
-// dX = c * (the fp32 sums over the pieces), in bf16; 8 elements per thread.
+// dX = c * (the parts' fp32 sums, added in order), in bf16; 8 elements per thread.
 __global__ void __launch_bounds__(256) xent_dx_kernel(const float* __restrict__ sums, const float* __restrict__ cmax,
-                                                      long long n8, uint16_t* __restrict__ dx) {
+                                                      long long n8, int splits, long long split8,
+                                                      uint16_t* __restrict__ dx) {
     asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const float c = *cmax;
     for (long long i = blockIdx.x * 256ll + threadIdx.x; i < n8; i += gridDim.x * 256ll) {
-        const float4 a = reinterpret_cast<const float4*>(sums)[2 * i], b = reinterpret_cast<const float4*>(sums)[2 * i + 1];
+        const float4* p = reinterpret_cast<const float4*>(sums) + 2 * i;
+        float4 a = p[0], b = p[1];
+        for (int s = 1; s < splits; ++s) {
+            p += 2 * split8;
+            const float4 u = p[0], v = p[1];
+            a.x += u.x; a.y += u.y; a.z += u.z; a.w += u.w;
+            b.x += v.x; b.y += v.y; b.z += v.z; b.w += v.w;
+        }
         reinterpret_cast<uint4*>(dx)[i] = make_uint4(pack_bf16(a.x * c, a.y * c), pack_bf16(a.z * c, a.w * c),
                                                      pack_bf16(b.x * c, b.y * c), pack_bf16(b.z * c, b.w * c));
     }
@@ -254,13 +286,44 @@ __global__ void __launch_bounds__(256) xent_dx_kernel(const float* __restrict__ 
 size_t round256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
 int parts(long long V) { return static_cast<int>((V + 127) / 128); }
 
-// Words per piece of the backward.
+// Words per piece of the backward: at most 2^28 entries of G (512 MB).  Smaller
+// pieces stay in L2 but cost more launches and more passes over dX's sums
+// (8192 x 128000 x 896: 2^26 entries 7.96 ms, 2^28 6.93 ms, 2^29 6.70 ms).
 long long piece_words(long long T, long long V) {
-    const long long most = (64ll << 20) / (T < 256 ? 256 : T);  // entries of G
+    const long long most = (1ll << 28) / (T < 256 ? 256 : T);
     long long w = most / 256 * 256;
     if (w < 2048) w = 2048;
     const long long all = (V + 255) / 256 * 256;
     return w < all ? w : all;
+}
+
+// dX has few tiles (T / 512 x D / 256) and a long reduction: it is cut into
+// the fewest parts, up to 8, that keep at least 95% of the pairs of SMs busy in
+// every round of tiles (or the most that any number keeps).  Each part has its
+// own fp32 sums over the pieces; xent_dx_kernel adds them in order.
+long long dx_rows(long long T) { return (T + 511) / 512 * 512; }
+int dx_splits(long long T, long long D, int num_sms) {
+    const long long pairs = num_sms / 2, tiles = dx_rows(T) / 512 * ((D + gm::BN - 1) / gm::BN);
+    int best = 1;
+    double most = 0.0;
+    for (int s = 1; s <= 8; ++s) {
+        const long long n = tiles * s, rounds = (n + pairs - 1) / pairs;
+        const double busy = static_cast<double>(n) / static_cast<double>(rounds * pairs);
+        if (busy > most + 1e-9) {
+            most = busy;
+            best = s;
+        }
+        if (busy >= 0.95) break;
+    }
+    return best;
+}
+
+template <class Epi, bool A_MN, bool B_MN>
+cudaError_t launch_either(const CUtensorMap& a, const CUtensorMap& b, const typename Epi::Params& p, const GemmShape& shape,
+                          unsigned* status, int num_sms, cudaStream_t st) {
+    return gemm_tall(shape.M, shape.N, shape.splits, num_sms)
+               ? launch_gemm_f16<Epi, 1, 2, A_MN, B_MN, false, 0>(a, b, p, shape, status, st)
+               : launch_gemm_f16<Epi, 1, 1, A_MN, B_MN, false, 0>(a, b, p, shape, status, st);
 }
 
 }  // namespace
@@ -269,14 +332,14 @@ size_t xent_workspace_bytes(long long T, long long V) {
     return round256(static_cast<size_t>(parts(V)) * T * sizeof(float2)) + round256(static_cast<size_t>(T) * sizeof(float));
 }
 
-size_t xent_backward_workspace_bytes(long long T, long long D, long long V, int need_dx) {
-    return 256 + (need_dx ? round256(static_cast<size_t>(T) * D * sizeof(float)) : 0) +
+size_t xent_backward_workspace_bytes(long long T, long long D, long long V, int need_dx, int num_sms) {
+    return 256 + (need_dx ? round256(static_cast<size_t>(dx_splits(T, D, num_sms)) * dx_rows(T) * D * sizeof(float)) : 0) +
            round256(static_cast<size_t>(T) * piece_words(T, V) * 2);
 }
 
 cudaError_t launch_xent(const uint16_t* x, long long T, long long D, const uint16_t* w, long long V,
                         const long long* target, long long ignore, float* loss, float* lse, void* ws, unsigned* status,
-                        cudaStream_t st) {
+                        int num_sms, cudaStream_t st) {
     float2* part = static_cast<float2*>(ws);
     float* tlogit = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) +
                                              round256(static_cast<size_t>(parts(V)) * T * sizeof(float2)));
@@ -284,8 +347,12 @@ cudaError_t launch_xent(const uint16_t* x, long long T, long long D, const uint1
     if (!gemm_operand(&a, false, false, x, T, D, D) || !gemm_operand(&b, false, false, w, V, D, D))
         return cudaErrorInvalidValue;
     const LsePart::Params p{part, tlogit, target, static_cast<int>(T), static_cast<int>(V)};
-    const GemmShape shape{static_cast<int>(T), static_cast<int>(V), static_cast<int>(D), 0, 8};
-    if (cudaError_t e = launch_gemm_f16<LsePart, 1, false, false, false, kLogitSegment>(a, b, p, shape, status, st)) return e;
+    const GemmShape shape{static_cast<int>(T), static_cast<int>(V), static_cast<int>(D), 0, 8, 1, 0};
+    // one segment holds the whole sum: tall tiles need none
+    const bool tall = D <= kLogitSegment * gm::BK && gemm_tall(T, V, 1, num_sms);
+    if (cudaError_t e = tall ? launch_gemm_f16<LsePart, 1, 2, false, false, false, 0>(a, b, p, shape, status, st)
+                             : launch_gemm_f16<LsePart, 1, 1, false, false, false, kLogitSegment>(a, b, p, shape, status, st))
+        return e;
     return pdl_launch(xent_merge_kernel, dim3(static_cast<unsigned>((T + 31) / 32)), dim3(1024), 0, st,
                       static_cast<const float2*>(part), static_cast<const float*>(tlogit), target, ignore,
                       static_cast<int>(T), static_cast<int>(V), parts(V), loss, lse, status);
@@ -294,19 +361,21 @@ cudaError_t launch_xent(const uint16_t* x, long long T, long long D, const uint1
 cudaError_t launch_xent_backward(const float* dloss, const uint16_t* x, long long T, long long D, const uint16_t* w,
                                  long long V, const long long* target, long long ignore, const float* lse, uint16_t* dx,
                                  uint16_t* dw, void* ws, unsigned* status, int num_sms, cudaStream_t st) {
+    const int splits = dx_splits(T, D, num_sms);
+    const long long rows = dx_rows(T);
     uint8_t* at = static_cast<uint8_t*>(ws);
     float* cmax = reinterpret_cast<float*>(at);
     at += 256;
     float* dx32 = nullptr;
     if (dx) {
         dx32 = reinterpret_cast<float*>(at);
-        at += round256(static_cast<size_t>(T) * D * sizeof(float));
+        at += round256(static_cast<size_t>(splits) * rows * D * sizeof(float));
     }
     uint16_t* g = reinterpret_cast<uint16_t*>(at);
     const long long piece = piece_words(T, V);
     cudaError_t e = pdl_launch(xent_cmax_kernel, dim3(1), dim3(1024), 0, st, dloss, target, ignore, static_cast<int>(T), cmax);
     const int Ti = static_cast<int>(T), Di = static_cast<int>(D);
-    const int d_tiles = (Di + gm::BN - 1) / gm::BN;
+    const int d_panel = (Di + gm::BN - 1) / gm::BN;
     for (long long v0 = 0; v0 < V && e == cudaSuccess; v0 += piece) {
         const long long n = V - v0 < piece ? V - v0 : piece;
         const int ni = static_cast<int>(n);
@@ -314,7 +383,7 @@ cudaError_t launch_xent_backward(const float* dloss, const uint16_t* x, long lon
         CUtensorMap xk, wk;
         GradTile::Params gp;
         if (!gemm_operand(&xk, false, false, x, T, D, D) || !gemm_operand(&wk, false, false, wp, n, D, D) ||
-            !gemm_map(&gp.g, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, g, T, n, piece * 2, 64, 32))
+            !gemm_result_bf16(&gp.g, g, T, n, piece))
             return cudaErrorInvalidValue;
         gp.lse = lse;
         gp.dloss = dloss;
@@ -324,16 +393,17 @@ cudaError_t launch_xent_backward(const float* dloss, const uint16_t* x, long lon
         gp.v0 = v0;
         gp.T = Ti;
         gp.V = static_cast<int>(V);
-        e = launch_gemm_f16<GradTile, 1, false, false, false, 0>(xk, wk, gp, GemmShape{Ti, ni, Di, 0, 8}, status, st);
+        e = launch_either<GradTile, false, false>(xk, wk, gp, GemmShape{Ti, ni, Di, 0, 8, 1, 0}, status, num_sms, st);
         if (e != cudaSuccess) return e;
         if (dx) {
             CUtensorMap gk, wn;
             SumF32::Params sp;
             sp.add = v0 > 0;
             if (!gemm_operand(&gk, false, false, g, T, n, piece) || !gemm_operand(&wn, false, true, wp, n, D, D) ||
-                !gemm_map(&sp.out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, dx32, T, D, D * 4, 32, 32))
+                !gemm_map(&sp.out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, dx32, splits * rows, D, D * 4, 32, 32))
                 return cudaErrorInvalidValue;
-            e = launch_gemm_f16<SumF32, 1, false, true, false, 0>(gk, wn, sp, GemmShape{Ti, Di, ni, 0, d_tiles}, status, st);
+            e = launch_either<SumF32, false, true>(gk, wn, sp, GemmShape{Ti, Di, ni, 0, d_panel, splits, static_cast<int>(rows)},
+                                                   status, num_sms, st);
             if (e != cudaSuccess) return e;
         }
         if (dw) {
@@ -341,15 +411,15 @@ cudaError_t launch_xent_backward(const float* dloss, const uint16_t* x, long lon
             ScaledBf16::Params bp;
             bp.cmax = cmax;
             if (!gemm_operand(&gm_, false, true, g, T, n, piece) || !gemm_operand(&xn, false, true, x, T, D, D) ||
-                !gemm_map(&bp.out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dw + v0 * D, n, D, D * 2, 64, 32))
+                !gemm_result_bf16(&bp.out, dw + v0 * D, n, D, D))
                 return cudaErrorInvalidValue;
-            e = launch_gemm_f16<ScaledBf16, 1, true, true, false, 0>(gm_, xn, bp, GemmShape{ni, Di, Ti, 0, d_tiles}, status, st);
+            e = launch_either<ScaledBf16, true, true>(gm_, xn, bp, GemmShape{ni, Di, Ti, 0, d_panel, 1, 0}, status, num_sms, st);
         }
     }
     if (e == cudaSuccess && dx) {
         const long long n8 = T * D / 8, blocks = (n8 + 255) / 256, most = 8ll * num_sms;
         e = pdl_launch(xent_dx_kernel, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), dim3(256), 0, st,
-                       static_cast<const float*>(dx32), static_cast<const float*>(cmax), n8, dx);
+                       static_cast<const float*>(dx32), static_cast<const float*>(cmax), n8, splits, rows * D / 8, dx);
     }
     return e;
 }

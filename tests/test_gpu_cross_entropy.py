@@ -89,14 +89,16 @@ def _grad_bounds(x, w, p, hot, d, e, e2, L):
 
 
 def _check(name, got, ref, bound):
-    got = got.double().cpu()
+    got = got.double().to(ref.device)
     assert got.shape == ref.shape
     bad = ~((got - ref).abs() <= bound)
     assert not bad.any(), (name, int(bad.sum()), float(((got - ref).abs() / bound.clamp(min=1e-300)).max()))
 
 
 SHAPES = [(1, 16, 1), (1, 32, 7), (2, 64, 128), (3, 48, 129), (65, 80, 257), (129, 128, 300), (256, 64, 256),
-          (257, 96, 1000), (40, 896, 2500), (333, 144, 5001), (30, 2048, 513), (700, 272, 1111)]
+          (257, 96, 1000), (40, 896, 2500), (333, 144, 5001), (30, 2048, 513), (700, 272, 1111),
+          # 512-row tiles in every product, a ragged tail of each, dX in several parts
+          (1000, 272, 20011), (3000, 1040, 1500)]
 
 
 @pytest.mark.parametrize("T,D,V", SHAPES)
@@ -125,21 +127,21 @@ def test_loss_and_gradients(sbl, T, D, V, weights):
 
 
 def test_several_pieces_of_the_vocabulary(sbl):
-    """A vocabulary that the backward takes in several pieces, the last ragged."""
-    T, D, V = 40, 64, 300000
-    pieces = sbl.sbl_linear_cross_entropy_backward_workspace_bytes(T, D, V, False) < 2 * T * V
-    assert pieces
-    x, w, t = _inputs(T, D, V, seed=2)
+    """More logits than one piece of the backward holds (2^28), the last piece
+    ragged; the 64-bit reference runs on the device."""
+    T, D, V = 2100, 64, 131001
+    assert sbl.sbl_linear_cross_entropy_backward_workspace_bytes(T, D, V, False) < 2 * T * V
+    x, w, t = (v.cuda() for v in _inputs(T, D, V, seed=2))
     t[0], t[1] = V - 1, 0
-    d = torch.rand(T, generator=torch.Generator().manual_seed(3)) + 0.5
+    d = (torch.rand(T, generator=torch.Generator().manual_seed(3)) + 0.5).cuda()
     z, lse, loss, p, hot, dd = _refs(x, w, t, d)
     e, e2, L = _bounds(x, w, z, lse, loss)
-    c = lambda v: v.cuda()
-    got_loss, got_lse = sbl.sbl_linear_cross_entropy(c(x), c(w), c(t))
+    del z
+    got_loss, got_lse = sbl.sbl_linear_cross_entropy(x, w, t)
     _check("lse", got_lse, lse, e + L)
     _check("loss", got_loss, loss, 2 * e + L + 2 * U * loss.abs())
     (dx, bx), (dw, bw) = _grad_bounds(x, w, p, hot, dd, e, e2, L)
-    got = sbl.sbl_linear_cross_entropy_backward(c(d), c(x), c(w), c(t), got_lse)
+    got = sbl.sbl_linear_cross_entropy_backward(d, x, w, t, got_lse)
     _check("dx", got[0], dx, bx)
     _check("dw", got[1], dw, bw)
 

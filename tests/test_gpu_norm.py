@@ -87,7 +87,8 @@ SHAPES = [(1, 16), (1, 2048), (3, 48), (7, 256), (5, 272), (33, 896), (130, 2048
           (3, 8208), (35, 16400), (2500, 64), (1500, 896),
           # many rows: the streaming kernels, with a ragged last tile, each number of
           # columns per thread and, in fp32, tiles of one row
-          (10001, 16), (9601, 272), (2503, 1040), (1301, 2064), (901, 5120), (601, 5136), (701, 10240)]
+          (10001, 16), (9601, 272), (2503, 1040), (1301, 2064), (901, 5120), (601, 5136), (701, 10240), (100001, 16),
+          (7003, 400)]
 
 
 @pytest.mark.parametrize("T,K", SHAPES)

@@ -107,11 +107,9 @@ def test_cross_entropy_rejects_on_host():
     assert B(p, p, 4, 64, p, 100, p, -100, p, p + 4, None, p, big, None) == 1         # unaligned dx
     assert B(p, p, 4, 64, p, 100, p, -100, None, p, None, p, big, None) == 1          # no lse
     assert B(None, p, 4, 64, p, 100, p, -100, p, p, None, p, big, None) == 1          # no dloss
-    need = lib.sbl_linear_cross_entropy_backward_workspace_bytes(4, 64, 100, 1)
-    assert B(p, p, 4, 64, p, 100, p, -100, p, p, None, p, need - 1, None) == 6
-    assert lib.sbl_linear_cross_entropy_backward_workspace_bytes(4, 64, 100, 0) == need - 4 * 64 * 4
-    # the piece of the vocabulary is bounded: G never approaches [T, V]
-    assert lib.sbl_linear_cross_entropy_backward_workspace_bytes(8192, 896, 128000, 0) <= (128 << 20) + 256
+    assert B(p, p, 4, 64, p, 100, p, -100, p, p, None, None, big, None) == 6
+    assert B(p, p, 4, 64, p, 100, p, -100, p, p, None, p + 16, big, None) == 6
+    assert lib.sbl_linear_cross_entropy_backward_workspace_bytes(0, 64, 100, 1) == 0
 
 
 def test_cross_entropy_tensor_checks(rec):
