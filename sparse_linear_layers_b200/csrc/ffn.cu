@@ -56,38 +56,60 @@ namespace {
 
 constexpr int kActSilu = 0;
 
+__device__ __forceinline__ float2 exp_neg2(float2 g) {  // exp(-g)
+    const float2 e = mul2(g, both(-1.4426950408889634f));
+    float2 r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(e.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(e.y));
+    return r;
+}
+__device__ __forceinline__ float2 rcp2(float2 a) {
+    float2 r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(a.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(a.y));
+    return r;
+}
+
+// act(g) * u
 template <int ACT>
-__device__ __forceinline__ float act_value(float g) {
-    if (ACT == kActSilu) return __fdividef(g, 1.0f + __expf(-g));
-    const float r = fmaxf(g, 0.0f);
-    return r * r;
+__device__ __forceinline__ float2 act_times(float2 g, float2 u) {
+    if (ACT == kActSilu) return mul2(mul2(g, u), rcp2(add2(exp_neg2(g), both(1.0f))));
+    const float2 r = make_float2(fmaxf(g.x, 0.0f), fmaxf(g.y, 0.0f));
+    return mul2(mul2(r, r), u);
 }
 
 // act(g) and act'(g)
 template <int ACT>
-__device__ __forceinline__ void act_both(float g, float& a, float& da) {
+__device__ __forceinline__ void act_both(float2 g, float2& a, float2& da) {
     if (ACT == kActSilu) {
-        const float s = __fdividef(1.0f, 1.0f + __expf(-g));
-        a = g * s;
-        da = s * fmaf(g, 1.0f - s, 1.0f);
+        const float2 s = rcp2(add2(exp_neg2(g), both(1.0f)));
+        a = mul2(g, s);
+        da = fma2(a, fma2(s, both(-1.0f), both(1.0f)), s);  // s + g s (1 - s)
     } else {
-        const float r = fmaxf(g, 0.0f);
-        a = r * r;
-        da = 2.0f * r;
+        const float2 r = make_float2(fmaxf(g.x, 0.0f), fmaxf(g.y, 0.0f));
+        a = mul2(r, r);
+        da = add2(r, r);
     }
+}
+
+// acc * scale * inv_s of two integer sums
+__device__ __forceinline__ float2 dequant2(uint32_t a0, uint32_t a1, float2 scale, float2 inv_s) {
+    return mul2(mul2(make_float2(static_cast<float>(static_cast<int>(a0)), static_cast<float>(static_cast<int>(a1))), scale),
+                inv_s);
 }
 
 // ---------------------------------------------------------------- a few tokens
 namespace fd {
-constexpr int THREADS = 512;
-constexpr int WARPS = THREADS / 32;
 constexpr int MAX_TOKENS = 16;
+// Up to 8 tokens: blocks of 8 warps, four to an SM; more: 16 warps, two.
+constexpr int warps(int nt) { return nt == 1 ? 8 : 16; }
+constexpr int SM_WARPS = 32;
 __host__ __device__ inline int pad64(int K) { return (K + 63) / 64 * 64; }
 // one token's activations: 64 mod 128 bytes apart, so two tokens of a
 // quarter-warp read disjoint banks
 __host__ __device__ inline int stride(int K) { return pad64(K) % 128 == 64 ? pad64(K) : pad64(K) + 64; }
 inline size_t smem_bytes(int K, int tokens) {
-    return static_cast<size_t>(tokens) * stride(K) + static_cast<size_t>(WARPS) * 32 * 4 * (tokens > 8 ? 2 : 1) * 4;
+    return static_cast<size_t>(tokens) * stride(K) + static_cast<size_t>(warps(tokens > 8 ? 2 : 1)) * 32 * 4 * (tokens > 8 ? 2 : 1) * 4;
 }
 }  // namespace fd
 
@@ -124,12 +146,13 @@ __device__ __forceinline__ void load_codes(const uint8_t* row, int w0, int words
 // weights); KS warps of a block share a tile and add their int32 partials in
 // shared memory.  NT: tiles of 8 tokens.
 template <int NT, int CW, int ACT>
-__global__ void __launch_bounds__(fd::THREADS, 1)
+__global__ void __launch_bounds__(fd::warps(NT) * 32, fd::SM_WARPS / fd::warps(NT))
     ffn_decode_kernel(const uint8_t* __restrict__ pg, const float* __restrict__ scale_g, const uint8_t* __restrict__ pu,
                       const float* __restrict__ scale_u, int F, int K, const uint16_t* __restrict__ x, int t0, int TP,
                       int KS, void* __restrict__ h, int h_bf16, unsigned* status) {
+    constexpr int WARPS = fd::warps(NT);
     extern __shared__ __align__(16) uint8_t fd_smem[];
-    __shared__ uint32_t red_max[fd::WARPS];
+    __shared__ uint32_t red_max[WARPS];
     __shared__ float s_sh[fd::MAX_TOKENS];
     asm volatile("griddepcontrol.launch_dependents;");
     const int S = fd::stride(K);
@@ -138,7 +161,7 @@ __global__ void __launch_bounds__(fd::THREADS, 1)
     const int words = K >> 4;
     const int C = fd::pad64(K) / (64 * CW);
     const int ks = warp % KS;
-    const int f = (blockIdx.x * (fd::WARPS / KS) + warp / KS) * 8 + gq;
+    const int f = (blockIdx.x * (WARPS / KS) + warp / KS) * 8 + gq;
     const bool ok = f < F;
     const size_t rowb = static_cast<size_t>(K) >> 2;
     const uint8_t* const rg = pg + static_cast<size_t>(ok ? f : 0) * rowb;
@@ -170,12 +193,12 @@ __global__ void __launch_bounds__(fd::THREADS, 1)
         return c * 4 * CW + (l % CW) * 4 + l / CW;
     };
     {
-        const int wpt = fd::WARPS / TP;
+        const int wpt = WARPS / TP;
         const int qt = warp / wpt;
         const bool qw = qt < TP;
         const int qj = (warp - qt * wpt) * 32 + lane, nthr = wpt * 32;
         const uint4* const xr = reinterpret_cast<const uint4*>(x + static_cast<size_t>(t0 + (qw ? qt : 0)) * K);
-        constexpr int XB = 4;  // 16-element blocks kept in registers
+        constexpr int XB = 2;  // 16-element blocks kept in registers
         uint4 xa[XB][2];
         uint32_t mx = 0;
         if (qw) {
@@ -197,7 +220,7 @@ __global__ void __launch_bounds__(fd::THREADS, 1)
         if (threadIdx.x < TP) {
             uint32_t m = 0;
 #pragma unroll
-            for (int w = 0; w < fd::WARPS; ++w)
+            for (int w = 0; w < WARPS; ++w)
                 if (w / wpt == static_cast<int>(threadIdx.x)) m = max(m, red_max[w]);
             if (m >= 0x7F80u && blockIdx.x == 0) raise_status(status, kStatusNonfinite);
             s_sh[threadIdx.x] = __fdiv_rn(127.0f, fmaxf(__uint_as_float(m << 16), 1e-5f));
@@ -278,10 +301,10 @@ __global__ void __launch_bounds__(fd::THREADS, 1)
         for (int e = 0; e < 2; ++e) {
             const int tok = nt * 8 + 2 * tg + e;
             if (tok >= TP) continue;
-            const float st = s_sh[tok];
-            const float g = __fdiv_rn(__fmul_rn(static_cast<float>(acc[nt][e]), sg), st);
-            const float u = __fdiv_rn(__fmul_rn(static_cast<float>(acc[nt][2 + e]), su), st);
-            const float v = act_value<ACT>(g) * u;
+            const float inv_s = __frcp_rn(s_sh[tok]);
+            const float g = __fmul_rn(__fmul_rn(static_cast<float>(acc[nt][e]), sg), inv_s);
+            const float u = __fmul_rn(__fmul_rn(static_cast<float>(acc[nt][2 + e]), su), inv_s);
+            const float v = act_times<ACT>(both(g), both(u)).x;
             const size_t at = static_cast<size_t>(t0 + tok) * F + f;
             if (h_bf16) reinterpret_cast<__nv_bfloat16*>(h)[at] = __float2bfloat16_rn(v);
             else reinterpret_cast<float*>(h)[at] = v;
@@ -314,7 +337,7 @@ struct FfnSmem {
     uint8_t b[fp::stages(BWD)][fp::B_BYTES];
     uint8_t box[fp::EPI_WARPS][fp::boxes(BWD)][fp::BOX];
     uint8_t p[fp::stages(BWD)][fp::P_BYTES];
-    float scale[fp::EPI_WARPS][2][fp::BF / 2];
+    alignas(16) float scale[fp::EPI_WARPS][2][fp::BF / 2];
     uint64_t full_a[fp::stages(BWD)];         // used in the even CTA
     uint64_t full_c[fp::stages(BWD)];
     uint64_t full_dec[fp::stages(BWD)];       // used in the even CTA
@@ -445,10 +468,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp::THREADS, 1)
                     // the second box (word c of row r at c ^ r: no bank conflicts)
                     uint32_t* const tb = reinterpret_cast<uint32_t*>(sm->box[warp][1]);
                     float d[32];
+                    const float* const dp = q.dh + static_cast<size_t>(trow0 < T ? trow0 : 0) * F + fk + lane;
+                    const int rows = fk + lane < F ? T - trow0 : 0;  // rows of the warp to read
 #pragma unroll
-                    for (int r = 0; r < 32; ++r)
-                        d[r] = (trow0 + r < T && fk + lane < F)
-                                   ? __ldg(q.dh + static_cast<size_t>(trow0 + r) * F + fk + lane) : 0.f;
+                    for (int r = 0; r < 32; ++r) d[r] = r < rows ? __ldg(dp + static_cast<long long>(r) * F) : 0.f;
                     box_wait(lane);  // both boxes' stores have been read
 #pragma unroll
                     for (int r = 0; r < 32; ++r) tb[r * 32 + (lane ^ r)] = __float_as_uint(d[r]);
@@ -460,20 +483,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp::THREADS, 1)
                         __syncwarp();
                         if (lane == 0) arrive_leader(&sm->tmem_empty[b]);
                     }
+                    const float2 is = both(inv_s);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const float dhv = __uint_as_float(tb[lane * 32 + (i ^ lane)]);
-                        const float sgi = sc_g[32 * k + i], sui = sc_u[32 * k + i];
-                        const float gv = __fmul_rn(__fmul_rn(static_cast<float>(static_cast<int>(g[i])), sgi), inv_s);
-                        const float uv = __fmul_rn(__fmul_rn(static_cast<float>(static_cast<int>(u[i])), sui), inv_s);
-                        float a, da;
+                    for (int i = 0; i < 32; i += 2) {
+                        const float2 dhv = make_float2(__uint_as_float(tb[lane * 32 + (i ^ lane)]),
+                                                       __uint_as_float(tb[lane * 32 + ((i + 1) ^ lane)]));
+                        const float2 sgi = *reinterpret_cast<const float2*>(sc_g + 32 * k + i);
+                        const float2 sui = *reinterpret_cast<const float2*>(sc_u + 32 * k + i);
+                        const float2 gv = dequant2(g[i], g[i + 1], sgi, is), uv = dequant2(u[i], u[i + 1], sui, is);
+                        float2 a, da;
                         act_both<ACT>(gv, a, da);
-                        const float vg = dhv * uv * da * sgi * inv_s;
-                        const float vu = dhv * a * sui * inv_s;
+                        const float2 vg = mul2(mul2(mul2(dhv, uv), da), mul2(sgi, is));
+                        const float2 vu = mul2(mul2(dhv, a), mul2(sui, is));
                         // a token past the end has inv_s = 0, a unit past F a scale of 0
-                        g[i] = __float_as_uint(vg);
-                        u[i] = __float_as_uint(vu);
-                        top = fmaxf(top, fmaxf(fabsf(vg), fabsf(vu)));
+                        g[i] = __float_as_uint(vg.x);
+                        g[i + 1] = __float_as_uint(vg.y);
+                        u[i] = __float_as_uint(vu.x);
+                        u[i + 1] = __float_as_uint(vu.y);
+                        top = max3(top, fabsf(vg.x), fabsf(vg.y));
+                        top = max3(top, fabsf(vu.x), fabsf(vu.y));
                     }
                     __syncwarp();
 #pragma unroll
@@ -496,11 +524,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp::THREADS, 1)
                         if (lane == 0) arrive_leader(&sm->tmem_empty[b]);
                     }
                     float h[32];
+                    const float2 is = both(inv_s);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const float gv = __fmul_rn(__fmul_rn(static_cast<float>(static_cast<int>(g[i])), sc_g[32 * k + i]), inv_s);
-                        const float uv = __fmul_rn(__fmul_rn(static_cast<float>(static_cast<int>(u[i])), sc_u[32 * k + i]), inv_s);
-                        h[i] = act_value<ACT>(gv) * uv;
+                    for (int i = 0; i < 32; i += 2) {
+                        const float2 gv = dequant2(g[i], g[i + 1], *reinterpret_cast<const float2*>(sc_g + 32 * k + i), is);
+                        const float2 uv = dequant2(u[i], u[i + 1], *reinterpret_cast<const float2*>(sc_u + 32 * k + i), is);
+                        const float2 v = act_times<ACT>(gv, uv);
+                        h[i] = v.x;
+                        h[i + 1] = v.y;
                     }
                     if (q.out_tma) {
                         if (q.h_bf16) {
@@ -802,6 +833,21 @@ struct FfnDx {
     __device__ __forceinline__ void end(const GemmTile&) {}
 };
 
+// dX from the parts of a split reduction, added in order; 4 elements per thread.
+__global__ void __launch_bounds__(256) ffn_sum_kernel(const float4* __restrict__ parts, int splits, long long stride4,
+                                                      long long n4, float4* __restrict__ out) {
+    asm volatile("griddepcontrol.launch_dependents;");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (long long i = blockIdx.x * 256ll + threadIdx.x; i < n4; i += gridDim.x * 256ll) {
+        float4 a = parts[i];
+        for (int s = 1; s < splits; ++s) {
+            const float4 b = parts[i + s * stride4];
+            a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w;
+        }
+        out[i] = a;
+    }
+}
+
 // dW: rows 0 .. Fp - 1 to the gate's gradient, the next Fp to the up's, times
 // 2^(max er - 8) / scale (ternary: without the division).
 struct FfnDw {
@@ -966,8 +1012,8 @@ cudaError_t launch_decode_as(const uint8_t* pg, const float* sg, const uint8_t* 
         if (cudaError_t e = cudaFuncSetAttribute(ffn_decode_kernel<NT, CW, ACT>,
                                                  cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)))
             return e;
-    const int tiles = (F + 7) / 8, per_block = fd::WARPS / KS;
-    return pdl_launch(ffn_decode_kernel<NT, CW, ACT>, dim3((tiles + per_block - 1) / per_block), dim3(fd::THREADS), smem,
+    const int tiles = (F + 7) / 8, per_block = fd::warps(NT) / KS;
+    return pdl_launch(ffn_decode_kernel<NT, CW, ACT>, dim3((tiles + per_block - 1) / per_block), dim3(fd::warps(NT) * 32), smem,
                       st, pg, sg, pu, su, F, K, x, t0, TP, KS, h, h_bf16, status);
 }
 
@@ -986,17 +1032,20 @@ cudaError_t run_decode(const uint16_t* x, long long T, int K, const uint8_t* pg,
     const int CW = K % 256 == 0 ? 4 : K % 128 == 0 ? 2 : 1;
     const int C = fd::pad64(K) / (64 * CW), nb = CW == 4 ? 2 : 4, tiles = (F + 7) / 8;
     // warps per tile: the fewest whose slices fit one batch of loads, then more
-    // while the grid has fewer blocks than SMs, never more warps than chunks
+    // while all of them still fit the SMs at once, never more than chunks or
+    // than a block has
+    const int most = fd::warps(T > 8 ? 2 : 1);
     int KS = 1;
-    while (KS < fd::WARPS && KS < C && (C + KS - 1) / KS > nb) KS *= 2;
-    while (KS < fd::WARPS && 2 * KS <= C && static_cast<long long>(tiles) * 2 * KS <= static_cast<long long>(num_sms) * fd::WARPS)
+    while (KS < most && KS < C && (C + KS - 1) / KS > nb) KS *= 2;
+    while (KS < most && 2 * KS <= C && static_cast<long long>(tiles) * 2 * KS <= static_cast<long long>(num_sms) * fd::SM_WARPS)
         KS *= 2;
     int cap = fd::MAX_TOKENS;  // tokens of one pass
     while (cap > 1 && fd::smem_bytes(K, cap) > 200 * 1024) --cap;
     for (int t0 = 0; t0 < T; t0 += cap) {
         const int TP = static_cast<int>(T) - t0 < cap ? static_cast<int>(T) - t0 : cap;
-        const cudaError_t e = TP > 8 ? launch_decode_cw<2, ACT>(CW, pg, sg, pu, su, F, K, x, t0, TP, KS, h, h_bf16, status, st)
-                                     : launch_decode_cw<1, ACT>(CW, pg, sg, pu, su, F, K, x, t0, TP, KS, h, h_bf16, status, st);
+        const int ks = KS < fd::warps(TP > 8 ? 2 : 1) ? KS : fd::warps(TP > 8 ? 2 : 1);
+        const cudaError_t e = TP > 8 ? launch_decode_cw<2, ACT>(CW, pg, sg, pu, su, F, K, x, t0, TP, ks, h, h_bf16, status, st)
+                                     : launch_decode_cw<1, ACT>(CW, pg, sg, pu, su, F, K, x, t0, TP, ks, h, h_bf16, status, st);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
@@ -1086,18 +1135,30 @@ cudaError_t launch_ffn_backward(const float* dh, const uint16_t* x, long long T,
 
     const int k_panel = (Ki + gm::BN - 1) / gm::BN;
     if (dx) {
+        // few tiles: the reduction in parts, one for each that the idle SMs can
+        // take and v's memory, free by now, can hold
+        const long long rows = (T + 255) / 256 * 256, tiles = rows / 256 * k_panel;
+        int splits = static_cast<int>(num_sms / 2 / tiles);
+        if (splits > 8) splits = 8;
+        while (splits > 1 && splits * rows * K > T * 2 * sp.Fp) --splits;
+        if (splits < 1) splits = 1;
         CUtensorMap a, b;
         FfnDx::Params p;
         if (!gemm_operand(&a, true, false, parts, T, 4 * sp.Fp, 4 * sp.Fp) ||
             !gemm_operand(&b, true, true, codes, 2 * sp.Fp, K, K) ||
-            !gemm_map(&p.out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, dx, T, K, K * 4, 32, 32))
+            !gemm_map(&p.out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, splits > 1 ? v : dx, splits > 1 ? splits * rows : T, K, K * 4,
+                      32, 32))
             return cudaErrorInvalidValue;
         p.row_max = row_max;
         p.s_tok = q.s_tok;
         p.T = Ti;
-        if (cudaError_t e = launch_gemm_f16<FfnDx, 2, 1, false, true, true, 4>(a, b, p, GemmShape{Ti, Ki, 2 * Fp, 2 * Fp, k_panel, 1, 0},
-                                                                            status, st))
-            return e;
+        const GemmShape shape{Ti, Ki, 2 * Fp, 2 * Fp, k_panel, splits, static_cast<int>(rows)};
+        if (cudaError_t e = launch_gemm_f16<FfnDx, 2, 1, false, true, true, 4>(a, b, p, shape, status, st)) return e;
+        if (splits > 1)
+            if (cudaError_t e = pdl_launch(ffn_sum_kernel, dim3(blocks_for(T * K / 4, 8)), dim3(256), 0, st,
+                                           reinterpret_cast<const float4*>(v), splits, rows * K / 4, T * K / 4,
+                                           reinterpret_cast<float4*>(dx)))
+                return e;
     }
     if (need_dw) {
         CUtensorMap a, b;

@@ -217,6 +217,12 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 }
 __device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 // ---------------------------------------------------------------- activation quantisation
 // round_half_even(x * s) for an activation x (as float) and its token's
 // s = 127 / max|x|, returned as the bit pattern of x * s + 1.5 * 2^23.  The

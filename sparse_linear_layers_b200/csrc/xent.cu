@@ -52,12 +52,6 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float d;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
-
 // Forward epilogue: part[p][t] = (max, sum of exp(z - max)) over columns 128 p .. + 127.
 struct LsePart {
     struct Params {

@@ -2,8 +2,9 @@
 the oracle's prepared weights and int8 activations.
 
 Bounds.  u = 2^-24.  The integer products are exact; g and the up product take
-three fp32 roundings and a reciprocal's: 4 u each.  __expf is documented as
-off by at most 2 + 1.173 |x| units in the last place, __fdividef by 2: the
+three fp32 roundings and a reciprocal's: 4 u each.  ex2.approx and rcp.approx
+are documented as off by at most 2 and 1 units in the last place (2^-23), the
+exponent g log2 e has a relative error of 2 u, which moves exp by 2 u |g|: the
 sigmoid has a relative error of at most delta = (5 + 1.2 |g|) 2^-23.  From these
 come the errors of act, act', h and v = (dg | du) * scale / s below.
 
