@@ -149,25 +149,34 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// 32 columns of a row as bf16 through one half of the warp's box (32 rows x 64
-// bytes, 64B swizzle): slice k uses half k mod 2 and waits only for the store
-// before the last one.
-__device__ __forceinline__ void put_bf16(const GemmTile& t, int k, const float (&v)[32], const CUtensorMap* map) {
-    uint8_t* const half = t.box + (k & 1) * (gm::BOX / 2);
+// 32 columns of a row as bf16 (four 16-byte units) through half h of the warp's
+// box (32 rows x 64 bytes, 64B swizzle) to columns col0 + 32 k; calls alternate
+// between the halves and wait only for the store before the last one.
+__device__ __forceinline__ void put_bf16(const GemmTile& t, int k, int h, const uint4 (&w)[4], const CUtensorMap* map) {
+    uint8_t* const half = t.box + h * (gm::BOX / 2);
     if (t.lane == 0) bulk_wait_read<1>();
     __syncwarp();
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
         // 16-byte unit c of row r at c ^ (r / 2 mod 4)
         const uint32_t a = smem_u32(half + t.lane * 64 + ((c ^ ((t.lane >> 1) & 3)) << 4));
-        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(pack_bf16(v[8 * c], v[8 * c + 1])),
-                     "r"(pack_bf16(v[8 * c + 2], v[8 * c + 3])), "r"(pack_bf16(v[8 * c + 4], v[8 * c + 5])),
-                     "r"(pack_bf16(v[8 * c + 6], v[8 * c + 7]))
+        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(w[c].x), "r"(w[c].y), "r"(w[c].z), "r"(w[c].w)
                      : "memory");
     }
     fence_proxy_async_smem();
     __syncwarp();
     if (t.lane == 0) tma_store_2d(map, smem_u32(half), t.col0 + 32 * k, t.out_row);
+}
+__device__ __forceinline__ void to_bf16(const float (&v)[32], uint4 (&w)[4]) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        w[c] = make_uint4(pack_bf16(v[8 * c], v[8 * c + 1]), pack_bf16(v[8 * c + 2], v[8 * c + 3]),
+                          pack_bf16(v[8 * c + 4], v[8 * c + 5]), pack_bf16(v[8 * c + 6], v[8 * c + 7]));
+}
+__device__ __forceinline__ void put_bf16(const GemmTile& t, int k, const float (&v)[32], const CUtensorMap* map) {
+    uint4 w[4];
+    to_bf16(v, w);
+    put_bf16(t, k, k & 1, w, map);
 }
 
 // 32 fp32 columns of a row through the warp's box to rows out_row - row0 of

@@ -22,7 +22,8 @@
 // term, at most sqrt(2) times the output's own rounding in the 2-norm.  To keep
 // the largest terms out of it, c = max_t |dloss[t]| is taken out of G and
 // multiplied back into the fp32 results: under a mean or sum reduction G's
-// entry at an unlikely target is then -1 exactly.
+// entry at an unlikely target is then -1 exactly.  A few tokens, whose errors do
+// not average out, take two bf16 parts (kPartsTokens).
 //
 // Bound by what feeds the tensor cores (gemm_f16.cuh) and, over longer runs, by
 // the power limit: 2 T V D operations forward, 6 T V D backward (a third of them
@@ -32,6 +33,8 @@
 // spend about three instructions per logit on pairs of values; an index into
 // a row's registers anywhere in them would put the row into local memory.
 #include <cuda.h>
+
+#include <type_traits>
 
 #include "gemm_f16.cuh"
 #include "sbl_common.cuh"
@@ -110,16 +113,18 @@ struct LsePart {
 };
 
 // Backward epilogue of the logits: G / c in bf16, columns counted from the
-// piece's first word v0.
+// piece's first word v0.  PARTS: as two bf16 values, the second what the first
+// rounds off.
+template <bool PARTS>
 struct GradTile {
     struct Params {
-        CUtensorMap g;
+        CUtensorMap g, g_low;
         const float* lse;
         const float* dloss;
         const float* cmax;
         const long long* target;
         long long ignore, v0;
-        int T, V;
+        int T, V, n;  // n: words of the piece
     };
     static __device__ __forceinline__ void prefetch(const Params& p) { prefetch_tmap(&p.g); }
     const Params& p;
@@ -158,7 +163,31 @@ struct GradTile {
             v[i] = g.x;
             v[i + 1] = g.y;
         }
-        put_bf16(t, k, v, &p.g);
+        if constexpr (PARTS) {
+            // the products read whole tiles of both parts: zeros past the last word
+            const int valid = p.n - (t.col0 + 32 * k);
+            if (valid < 32) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (i >= valid) v[i] = 0.f;
+            }
+            uint4 w[4];
+            to_bf16(v, w);
+            put_bf16(t, k, 0, w, &p.g);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const uint32_t h[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    v[8 * c + 2 * j] -= __uint_as_float(h[j] << 16);
+                    v[8 * c + 2 * j + 1] -= __uint_as_float(h[j] & 0xFFFF0000u);
+                }
+            }
+            to_bf16(v, w);
+            put_bf16(t, k, 1, w, &p.g_low);
+        } else {
+            put_bf16(t, k, v, &p.g);
+        }
     }
     __device__ __forceinline__ void end(const GemmTile&) {}
 };
@@ -291,6 +320,14 @@ long long piece_words(long long T, long long V) {
     return w < all ? w : all;
 }
 
+// Up to this many tokens G goes as two bf16 parts: the rounding of a token's
+// one large entry, its target's, moves a whole row of dX and dW together, and
+// over a few tokens such errors do not average out (1 to 8 tokens: up to 1.75
+// times the error that rounding the results alone leaves).  These sizes are bound by
+// reading W and writing dW, which hides the second part's MMAs.
+constexpr int kPartsTokens = 128;
+bool g_parts(long long T) { return T <= kPartsTokens; }
+
 // dX has few tiles (T / 512 x D / 256) and a long reduction: it is cut into
 // the fewest parts, up to 8, that keep at least 95% of the pairs of SMs busy in
 // every round of tiles (or the most that any number keeps).  Each part has its
@@ -328,7 +365,7 @@ size_t xent_workspace_bytes(long long T, long long V) {
 
 size_t xent_backward_workspace_bytes(long long T, long long D, long long V, int need_dx, int num_sms) {
     return 256 + (need_dx ? round256(static_cast<size_t>(dx_splits(T, D, num_sms)) * dx_rows(T) * D * sizeof(float)) : 0) +
-           round256(static_cast<size_t>(T) * piece_words(T, V) * 2);
+           round256(static_cast<size_t>(T) * piece_words(T, V) * (g_parts(T) ? 4 : 2));
 }
 
 cudaError_t launch_xent(const uint16_t* x, long long T, long long D, const uint16_t* w, long long V,
@@ -367,6 +404,8 @@ cudaError_t launch_xent_backward(const float* dloss, const uint16_t* x, long lon
     }
     uint16_t* g = reinterpret_cast<uint16_t*>(at);
     const long long piece = piece_words(T, V);
+    const bool parts = g_parts(T);
+    const long long pitch = parts ? 2 * piece : piece;
     cudaError_t e = pdl_launch(xent_cmax_kernel, dim3(1), dim3(1024), 0, st, dloss, target, ignore, static_cast<int>(T), cmax);
     const int Ti = static_cast<int>(T), Di = static_cast<int>(D);
     const int d_panel = (Di + gm::BN - 1) / gm::BN;
@@ -375,39 +414,53 @@ cudaError_t launch_xent_backward(const float* dloss, const uint16_t* x, long lon
         const int ni = static_cast<int>(n);
         const uint16_t* wp = w + v0 * D;
         CUtensorMap xk, wk;
-        GradTile::Params gp;
-        if (!gemm_operand(&xk, false, false, x, T, D, D) || !gemm_operand(&wk, false, false, wp, n, D, D) ||
-            !gemm_result_bf16(&gp.g, g, T, n, piece))
+        if (!gemm_operand(&xk, false, false, x, T, D, D) || !gemm_operand(&wk, false, false, wp, n, D, D))
             return cudaErrorInvalidValue;
-        gp.lse = lse;
-        gp.dloss = dloss;
-        gp.cmax = cmax;
-        gp.target = target;
-        gp.ignore = ignore;
-        gp.v0 = v0;
-        gp.T = Ti;
-        gp.V = static_cast<int>(V);
-        e = launch_either<GradTile, false, false>(xk, wk, gp, GemmShape{Ti, ni, Di, 0, 8, 1, 0}, status, num_sms, st);
+        auto logits = [&](auto parts_tag) -> cudaError_t {
+            constexpr bool PARTS = decltype(parts_tag)::value;
+            typename GradTile<PARTS>::Params gp;
+            if (!gemm_result_bf16(&gp.g, g, T, PARTS ? piece : n, pitch) ||
+                !gemm_result_bf16(&gp.g_low, g + (PARTS ? piece : 0), T, PARTS ? piece : n, pitch))
+                return cudaErrorInvalidValue;
+            gp.lse = lse;
+            gp.dloss = dloss;
+            gp.cmax = cmax;
+            gp.target = target;
+            gp.ignore = ignore;
+            gp.v0 = v0;
+            gp.T = Ti;
+            gp.V = static_cast<int>(V);
+            gp.n = ni;
+            const GemmShape shape{Ti, ni, Di, 0, 8, 1, 0};
+            if constexpr (PARTS) return launch_gemm_f16<GradTile<true>, 1, 1, false, false, false, 0>(xk, wk, gp, shape, status, st);
+            else return launch_either<GradTile<false>, false, false>(xk, wk, gp, shape, status, num_sms, st);
+        };
+        e = parts ? logits(std::true_type{}) : logits(std::false_type{});
         if (e != cudaSuccess) return e;
+        const long long g_cols = parts ? piece + n : n;
+        const int low = static_cast<int>(piece);  // columns from a part to the next
         if (dx) {
             CUtensorMap gk, wn;
             SumF32::Params sp;
             sp.add = v0 > 0;
-            if (!gemm_operand(&gk, false, false, g, T, n, piece) || !gemm_operand(&wn, false, true, wp, n, D, D) ||
+            if (!gemm_operand(&gk, false, false, g, T, g_cols, pitch) || !gemm_operand(&wn, false, true, wp, n, D, D) ||
                 !gemm_map(&sp.out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, dx32, splits * rows, D, D * 4, 32, 32))
                 return cudaErrorInvalidValue;
-            e = launch_either<SumF32, false, true>(gk, wn, sp, GemmShape{Ti, Di, ni, 0, d_panel, splits, static_cast<int>(rows)},
-                                                   status, num_sms, st);
+            const GemmShape shape{Ti, Di, ni, low, d_panel, splits, static_cast<int>(rows)};
+            e = parts ? launch_gemm_f16<SumF32, 2, 1, false, true, false, 0>(gk, wn, sp, shape, status, st)
+                      : launch_either<SumF32, false, true>(gk, wn, sp, shape, status, num_sms, st);
             if (e != cudaSuccess) return e;
         }
         if (dw) {
             CUtensorMap gm_, xn;
             ScaledBf16::Params bp;
             bp.cmax = cmax;
-            if (!gemm_operand(&gm_, false, true, g, T, n, piece) || !gemm_operand(&xn, false, true, x, T, D, D) ||
+            if (!gemm_operand(&gm_, false, true, g, T, g_cols, pitch) || !gemm_operand(&xn, false, true, x, T, D, D) ||
                 !gemm_result_bf16(&bp.out, dw + v0 * D, n, D, D))
                 return cudaErrorInvalidValue;
-            e = launch_either<ScaledBf16, true, true>(gm_, xn, bp, GemmShape{ni, Di, Ti, 0, d_panel, 1, 0}, status, num_sms, st);
+            const GemmShape shape{ni, Di, Ti, low, d_panel, 1, 0};
+            e = parts ? launch_gemm_f16<ScaledBf16, 2, 1, true, true, false, 0>(gm_, xn, bp, shape, status, st)
+                      : launch_either<ScaledBf16, true, true>(gm_, xn, bp, shape, status, num_sms, st);
         }
     }
     if (e == cudaSuccess && dx) {

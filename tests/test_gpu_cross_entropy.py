@@ -77,12 +77,14 @@ def _grad_bounds(x, w, p, hot, d, e, e2, L):
     eps = (torch.expm1(e + e2 + L) + 2.0 ** -20)[:, None]
     G = (p - hot) * d
     # p's error before the subtraction, then the bf16 rounding and two fp32 ones
-    dG = (p * eps * d.abs()) * (1 + BF16) + G.abs() * (BF16 + 4 * U)
-    Ga = G.abs() + dG
+    # up to 128 tokens G goes as two bf16 parts, which keep all but 2^-16 of it
     T, V = p.shape
+    dG = (p * eps * d.abs()) * (1 + BF16) + G.abs() * ((BF16 if T > 128 else BF16 ** 2) + 4 * U)
+    Ga = G.abs() + dG
     ref = G @ w.double(), G.T @ x.double()
-    bx = dG @ wa + (2 * V / 16 + 64) * U * (Ga @ wa)
-    bw = dG.T @ xa + (2 * T / 16 + 8) * U * (Ga.T @ xa)
+    n = 2 if T > 128 else 4  # units of 2^-24 per 16 terms: one or two MMAs
+    bx = dG @ wa + (n * V / 16 + 64) * U * (Ga @ wa)
+    bw = dG.T @ xa + (n * T / 16 + 8) * U * (Ga.T @ xa)
     out = BF16  # the results' own rounding
     tiny = 1e-30
     return (ref[0], bx * (1 + 2 * out) + out * ref[0].abs() + tiny), (ref[1], bw * (1 + 2 * out) + out * ref[1].abs() + tiny)
@@ -95,7 +97,7 @@ def _check(name, got, ref, bound):
     assert not bad.any(), (name, int(bad.sum()), float(((got - ref).abs() / bound.clamp(min=1e-300)).max()))
 
 
-SHAPES = [(1, 16, 1), (1, 32, 7), (2, 64, 128), (3, 48, 129), (65, 80, 257), (129, 128, 300), (256, 64, 256),
+SHAPES = [(1, 16, 1), (1, 896, 3000), (128, 64, 700), (1, 32, 7), (2, 64, 128), (3, 48, 129), (65, 80, 257), (129, 128, 300), (256, 64, 256),
           (257, 96, 1000), (40, 896, 2500), (333, 144, 5001), (30, 2048, 513), (700, 272, 1111),
           # 512-row tiles in every product, a ragged tail of each, dX in several parts
           (1000, 272, 20011), (3000, 1040, 1500)]
