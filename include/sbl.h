@@ -191,7 +191,8 @@ enum { SBL_NORM_RMS = 0, SBL_NORM_LAYER = 1 };
  *            not overlap x.
  *   weight   fp32 [K]; bias fp32 [K] or NULL.
  *   eps      finite, >= 0.
- *   mean     fp32 [T] (output) or NULL; rstd fp32 [T] (output) or NULL: the
+ *   mean     fp32 [T] (output) or NULL; rstd fp32 [T] (output) or NULL (4-byte
+ *            aligned): the
  *            statistics sbl_norm_backward reads (mean is not written for
  *            SBL_NORM_RMS).
  * NaN and Inf in a row pass to that row's outputs.  Asynchronous on `stream`;
@@ -325,7 +326,8 @@ enum { SBL_ACT_SILU = 0, SBL_ACT_RELU2 = 1 };
  *   x_bf16    bf16 bit patterns [T, K].
  *   packed_gate, scale_gate, packed_up, scale_up
  *             the two prepared matrices, uint8 [F, K/4] and fp32 [F] each, one
- *             N:M pattern (n, m).
+ *             N:M pattern (n, m); scales positive, as sbl_prepare_weights
+ *             writes them.
  *   h         [T, F] (output), fp32 (SBL_F32) or bf16 (SBL_BF16, rounded once).
  *   workspace sbl_ffn_gated_workspace_bytes(T, K, F) bytes, 256-byte aligned;
  *             0 bytes (NULL allowed) for up to 16 tokens.  Calls that share it
@@ -348,7 +350,7 @@ sbl_status sbl_ffn_gated(const uint16_t* x_bf16, int64_t T, int64_t K, const uin
  *   with SBL_BWD_DW_TERNARY the rows of both times their row scale once more.
  * Nothing of the forward is kept but x: g and u are computed again.
  *
- *   dh        fp32 [T, F], finite: gradient with respect to h.
+ *   dh        fp32 [T, F] (4-byte aligned), finite: gradient with respect to h.
  *   dX        fp32 [T, K]; dW_gate, dW_up fp32 [F, K] (outputs), each may be
  *             NULL, not all; overwritten (zeros for empty sums).
  *   workspace sbl_ffn_gated_backward_workspace_bytes(T, K, F, dX != NULL,
@@ -376,13 +378,14 @@ sbl_status sbl_ffn_gated_backward(const float* dh, const uint16_t* x_bf16, int64
  *
  *   x_bf16    bf16 bit patterns [T, D]: the hidden states.
  *   w_bf16    bf16 bit patterns [V, D]: one row per word; V >= 1.
- *   target    int64 [T]: the word of each token, or ignore_index (any value).
+ *   target    int64 [T] (8-byte aligned): the word of each token, or ignore_index
+ *             (any value).
  *             Another target outside [0, V) sets SBL_ERR_INVALID_ARG in the
  *             device status word; that token's loss is NaN.
- *   loss, lse fp32 [T] (outputs); lse also for ignored tokens.
+ *   loss, lse fp32 [T] (outputs, 4-byte aligned); lse also for ignored tokens.
  *   workspace sbl_linear_cross_entropy_workspace_bytes(T, V) bytes, 256-byte
  *             aligned (8 bytes per token and 128 words).
- * D % 16 == 0; T, D, V up to 2^24, else SBL_ERR_UNSUPPORTED.  x and W finite
+ * D % 16 == 0; T, D, V up to 2^24 and T * V below 2^46, else SBL_ERR_UNSUPPORTED.  x and W finite
  * (also in ignored rows).  Asynchronous on `stream`.
  */
 size_t sbl_linear_cross_entropy_workspace_bytes(int64_t T, int64_t V);
@@ -395,7 +398,7 @@ sbl_status sbl_linear_cross_entropy(const uint16_t* x_bf16, int64_t T, int64_t D
  *   G[t, v] = (exp(z[t, v] - lse[t]) - [v == target[t]]) * dloss[t], 0 for
  *   ignored tokens; dX = G . W, dW = G^T . x.
  *
- *   dloss     fp32 [T], finite; lse as sbl_linear_cross_entropy wrote it.
+ *   dloss     fp32 [T] (4-byte aligned), finite; lse as sbl_linear_cross_entropy wrote it.
  *   dx, dw    bf16 [T, D] and [V, D] (outputs), each may be NULL, not both;
  *             overwritten (dw with zeros for T == 0).
  *   workspace sbl_linear_cross_entropy_backward_workspace_bytes(T, D, V, dx != NULL)

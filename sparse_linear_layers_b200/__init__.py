@@ -4,7 +4,9 @@ y = dequant(int8(x) . ternary_NM(W)^T) behind a C ABI (include/sbl.h) with
 hand-written CUDA kernels: fused weight preparation, per-token activation
 quantisation (optionally after RMSNorm, as the guide's module does), decode
 paths on CUDA cores and the warp-level MMA, tcgen05 tensor-core prefill, a
-mask monitor and the straight-through backward of the training path.
+mask monitor and the straight-through backward of the training path.  Around
+the layer: norms, the gated feed-forward block and the cross entropy of a
+vocabulary projection, each with its gradients.
 
 The library entry points (sbl_prepare_weights, sbl_quant_act, sbl_linear, ...)
 load libsbl.so on first use and raise ImportError if it has not been built;
@@ -20,7 +22,8 @@ _API = ("PreparedWeights", "copy_to_device", "copy_to_host", "sbl_decode_max_tok
         "sbl_rmsnorm_quant_act", "sbl_selftest_bounded_wait", "workspace_for", "RMSNORM_EPS_F32", "SblError")
 
 
-_TRAIN = ("SparseBitLinear", "SparseBitLinearFunction")
+_TRAIN = ("LinearCrossEntropy", "LinearCrossEntropyFunction", "SparseBitFeedForward", "SparseBitGatedFunction",
+          "SparseBitLinear", "SparseBitLinearFunction", "SparseBitNorm", "SparseBitNormFunction")
 
 
 def __getattr__(name):

@@ -253,9 +253,9 @@ sbl_status sbl_norm(const void* x, int dtype, int64_t T, int64_t K, int kind, co
     if (!(eps >= 0.0f) || !(eps < 3.0e38f)) return SBL_ERR_INVALID_ARG;
     if (T == 0) return SBL_OK;
     if (!x || !weight || !y || x == y) return SBL_ERR_INVALID_ARG;
-    for (const void* p : {x, static_cast<const void*>(weight), static_cast<const void*>(bias),
-                          static_cast<const void*>(y), static_cast<const void*>(mean), static_cast<const void*>(rstd)})
+    for (const void* p : {x, static_cast<const void*>(weight), static_cast<const void*>(bias), static_cast<const void*>(y)})
         if (!aligned(p, 16)) return SBL_ERR_INVALID_ARG;
+    if (!aligned(mean, 4) || !aligned(rstd, 4)) return SBL_ERR_INVALID_ARG;
     DeviceInfo* d;
     if (sbl_status s = device_info(&d)) return s;
     return from_cuda(sbl::launch_norm_fwd(x, dtype == SBL_BF16, kind == SBL_NORM_LAYER, weight, bias, eps, T, K, y,
@@ -284,9 +284,9 @@ sbl_status sbl_norm_backward(const void* dy, const void* x, int dtype, int64_t T
     }
     if (!dy || !x || !weight || !rstd || (kind == SBL_NORM_LAYER && !mean) || dx == x || dx == dy)
         return SBL_ERR_INVALID_ARG;
-    for (const void* p : {dy, x, static_cast<const void*>(weight), static_cast<const void*>(mean),
-                          static_cast<const void*>(rstd), static_cast<const void*>(dx)})
+    for (const void* p : {dy, x, static_cast<const void*>(weight), static_cast<const void*>(dx)})
         if (!aligned(p, 16)) return SBL_ERR_INVALID_ARG;
+    if (!aligned(mean, 4) || !aligned(rstd, 4)) return SBL_ERR_INVALID_ARG;
     const bool sums = dweight || dbias;
     if (sums && (!workspace || !aligned(workspace, 256))) return SBL_ERR_WORKSPACE;
     DeviceInfo* d;
@@ -426,8 +426,8 @@ sbl_status sbl_ffn_gated_backward(const float* dh, const uint16_t* x_bf16, int64
             if (w && F > 0 && e == cudaSuccess) e = cudaMemsetAsync(w, 0, static_cast<size_t>(F) * K * sizeof(float), st);
         return from_cuda(e);
     }
-    for (const void* p : {static_cast<const void*>(dh), static_cast<const void*>(x_bf16),
-                          static_cast<const void*>(packed_gate), static_cast<const void*>(scale_gate),
+    if (!dh || !aligned(dh, 4)) return SBL_ERR_INVALID_ARG;
+    for (const void* p : {static_cast<const void*>(x_bf16), static_cast<const void*>(packed_gate), static_cast<const void*>(scale_gate),
                           static_cast<const void*>(packed_up), static_cast<const void*>(scale_up)})
         if (!p || !aligned(p, 16)) return SBL_ERR_INVALID_ARG;
     const size_t need = sbl::ffn_backward_workspace_bytes(T, K, F, dX != nullptr, dW_gate || dW_up);
@@ -443,8 +443,15 @@ sbl_status sbl_ffn_gated_backward(const float* dh, const uint16_t* x_bf16, int64
 static sbl_status check_xent(int64_t T, int64_t D, int64_t V) {
     constexpr long long most = 1ll << 24;
     if (T < 0 || V < 1 || D <= 0 || D % 16 != 0) return SBL_ERR_INVALID_ARG;
-    if (T > most || V > most || D > most) return SBL_ERR_UNSUPPORTED;
+    if (T > most || V > most || D > most || (T / 256 + 1) * (V / 256 + 1) > (1ll << 30)) return SBL_ERR_UNSUPPORTED;
     return SBL_OK;
+}
+
+// What the cross entropy reads: matrices through TMA, the rest one element at
+// a time (labels shifted by one are a view at an odd element).
+static bool xent_inputs_ok(const void* x, const void* w, const void* target, const void* a, const void* b) {
+    return x && aligned(x, 16) && w && aligned(w, 16) && target && aligned(target, 8) && a && aligned(a, 4) && b &&
+           aligned(b, 4);
 }
 
 size_t sbl_linear_cross_entropy_workspace_bytes(int64_t T, int64_t V) {
@@ -456,10 +463,7 @@ sbl_status sbl_linear_cross_entropy(const uint16_t* x_bf16, int64_t T, int64_t D
                                     void* workspace, size_t workspace_bytes, void* stream) {
     if (sbl_status s = check_xent(T, D, V)) return s;
     if (T == 0) return SBL_OK;
-    for (const void* p : {static_cast<const void*>(x_bf16), static_cast<const void*>(w_bf16),
-                          static_cast<const void*>(target), static_cast<const void*>(loss),
-                          static_cast<const void*>(lse)})
-        if (!p || !aligned(p, 16)) return SBL_ERR_INVALID_ARG;
+    if (!xent_inputs_ok(x_bf16, w_bf16, target, loss, lse)) return SBL_ERR_INVALID_ARG;
     if (!workspace || !aligned(workspace, 256) || workspace_bytes < sbl::xent_workspace_bytes(T, V))
         return SBL_ERR_WORKSPACE;
     DeviceInfo* d;
@@ -483,10 +487,7 @@ sbl_status sbl_linear_cross_entropy_backward(const float* dloss, const uint16_t*
     if (!aligned(dx, 16) || !aligned(dw, 16)) return SBL_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (T == 0) return dw ? from_cuda(cudaMemsetAsync(dw, 0, static_cast<size_t>(V) * D * 2, st)) : SBL_OK;
-    for (const void* p : {static_cast<const void*>(dloss), static_cast<const void*>(x_bf16),
-                          static_cast<const void*>(w_bf16), static_cast<const void*>(target),
-                          static_cast<const void*>(lse)})
-        if (!p || !aligned(p, 16)) return SBL_ERR_INVALID_ARG;
+    if (!xent_inputs_ok(x_bf16, w_bf16, target, dloss, lse)) return SBL_ERR_INVALID_ARG;
     if (!workspace || !aligned(workspace, 256)) return SBL_ERR_WORKSPACE;
     DeviceInfo* d;
     if (sbl_status s = device_info(&d)) return s;

@@ -50,8 +50,12 @@ class Case:
         if x is None:
             bits, _ = synthetic.activations(T, K, seed=seed + 1, tag="ffn", outlier_p=0.01)
             x = torch.from_numpy(bits.view(np.int16)).view(torch.bfloat16)
-        self.x_cpu = x
         self.x = x.cuda()
+        self.finish(x)
+
+    def finish(self, x):
+        """The reference's values on x (bf16, on the host) and the matrices."""
+        act = self.act
         xq, s = oracle.quant_act(x.float().numpy())
         self.xq, self.s = torch.from_numpy(xq).double(), torch.from_numpy(s).double()[:, None]
         self.g = (self.xq @ self.Wg.T) * self.sg / self.s

@@ -98,6 +98,9 @@ def test_cross_entropy_rejects_on_host():
     assert F(p, 1 << 25, 64, p, 100, p, -100, p, p, p, big, None) == 2
     assert F(p, 4, 64, None, 100, p, -100, p, p, p, big, None) == 1                   # missing W
     assert F(p + 8, 4, 64, p, 100, p, -100, p, p, p, big, None) == 1                  # unaligned x
+    assert F(p, 4, 64, p, 100, p + 4, -100, p, p, p, big, None) == 1                  # unaligned target
+    assert F(p, 4, 64, p, 100, p + 8, -100, p + 4, p + 4, None, big, None) == 6       # any element will do
+    assert F(p, 1 << 24, 64, p, 1 << 24, p, -100, p, p, p, big, None) == 2            # too many tiles
     assert F(p, 4, 64, p, 100, p, -100, p, p, None, big, None) == 6
     assert F(p, 4, 64, p, 100, p, -100, p, p, p + 16, big, None) == 6
     need = lib.sbl_linear_cross_entropy_workspace_bytes(4, 100)
