@@ -354,6 +354,17 @@ constexpr size_t ffn_smem_bytes() {
 }
 static_assert(ffn_smem_bytes<false>() <= 232448 && ffn_smem_bytes<true>() <= 232448, "feed-forward tile does not fit");
 
+// 16 bytes (unit c) of this lane's row in a 32-row x 128-byte staging box, 128B swizzle.
+__device__ __forceinline__ void box_put(uint8_t* box, int lane, int c, uint32_t w0, uint32_t w1, uint32_t w2,
+                                        uint32_t w3) {
+    const uint32_t a = smem_u32(box + lane * 128 + ((c ^ (lane & 7)) << 4));
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(w0), "r"(w1), "r"(w2), "r"(w3) : "memory");
+}
+__device__ __forceinline__ void box_wait(int lane) {  // the stores sent so far have read their boxes
+    if (lane == 0) bulk_wait_read<0>();
+    __syncwarp();
+}
+
 struct FfnParams {
     CUtensorMap x, wg, wu;     // int8 activations [T, K]; 2-bit codes [F, K / 4]
     CUtensorMap out;           // h [T, F] (forward, when out_tma), v [T, 2 Fp] (backward)
@@ -825,7 +836,7 @@ struct FfnDx {
             s = __ldg(p.s_tok + t.row);
         }
     }
-    __device__ __forceinline__ void slice(const GemmTile& t, int k, float (&v)[32]) {
+    __device__ __forceinline__ void slice(GemmTile& t, int k, float (&v)[32]) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = (v[i] * e) * s;
         put_f32(t, k, v, &p.out, 0, false);
@@ -872,7 +883,7 @@ struct FfnDw {
         s = f < p.F ? (p.ternary ? 1.0f : __frcp_rn(__ldg((up ? p.scale_u : p.scale_g) + f))) : 0.f;
         s *= 0.00390625f;  // x_q came times 2^8
     }
-    __device__ __forceinline__ void slice(const GemmTile& t, int k, float (&v)[32]) {
+    __device__ __forceinline__ void slice(GemmTile& t, int k, float (&v)[32]) {
         if (up ? !p.want_u : !p.want_g) return;
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = (v[i] * e) * s;
@@ -1146,8 +1157,7 @@ cudaError_t launch_ffn_backward(const float* dh, const uint16_t* x, long long T,
         FfnDx::Params p;
         if (!gemm_operand(&a, true, false, parts, T, 4 * sp.Fp, 4 * sp.Fp) ||
             !gemm_operand(&b, true, true, codes, 2 * sp.Fp, K, K) ||
-            !gemm_map(&p.out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, splits > 1 ? v : dx, splits > 1 ? splits * rows : T, K, K * 4,
-                      32, 32))
+            !gemm_result_f32(&p.out, splits > 1 ? v : dx, splits > 1 ? splits * rows : T, K))
             return cudaErrorInvalidValue;
         p.row_max = row_max;
         p.s_tok = q.s_tok;
@@ -1165,8 +1175,8 @@ cudaError_t launch_ffn_backward(const float* dh, const uint16_t* x, long long T,
         FfnDw::Params p;
         memset(&p, 0, sizeof(p));
         if (!gemm_operand(&a, true, true, parts, T, 4 * sp.Fp, 4 * sp.Fp) || !gemm_operand(&b, true, true, xs, T, K, K) ||
-            (dwg && !gemm_map(&p.out_g, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, dwg, F, K, K * 4, 32, 32)) ||
-            (dwu && !gemm_map(&p.out_u, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, dwu, F, K, K * 4, 32, 32)))
+            (dwg && !gemm_result_f32(&p.out_g, dwg, F, K)) ||
+            (dwu && !gemm_result_f32(&p.out_u, dwu, F, K)))
             return cudaErrorInvalidValue;
         p.all_max = all_max;
         p.scale_g = scale_g;

@@ -18,7 +18,8 @@
 // this GEMM: L2 delivers about 9 TB/s to the SMs whatever the kernel (measured on
 // four of them), 7.8 KB per MFLOP of a 256 x 256 tile and 5.9 KB of a 512 x 256
 // one.  The MMAs of the next tile wait until the epilogue has read a half, while
-// the loads run on for four stages.  (Letting the upper half's MMAs run ahead
+// the loads run on for four stages; sixteen epilogue warps read both halves at
+// once to keep that wait short.  (Letting the upper half's MMAs run ahead
 // through those stages made the whole 3% slower: their stages come back later.)
 //
 // SEGMENT > 0: the tensor cores round every fp32 accumulation towards zero, an
@@ -29,9 +30,9 @@
 // Costs one 128-column TMEM read and 128 additions per thread and segment,
 // hidden behind the next segment's MMAs.
 //
-// Warps (320 threads): 0-7 epilogue (warp w: TMEM lanes 32 (w % 4) .. + 31,
-// columns 128 (w / 4) .. + 127), 8 TMA producer, 9 TMEM allocation and, in the
-// even CTA, MMA issue.  Every wait is bounded; a CTA that gives up records a
+// Warps: 8 MH epilogue (warp w: TMEM lanes 32 (w % 4) .. + 31, columns
+// 128 (w / 4 % 2) .. + 127 of buffer w / 8), one TMA producer, one for TMEM
+// allocation and, in the even CTA, MMA issue.  Every wait is bounded; a CTA that gives up records a
 // timeout, lets its loads land and its MMAs finish (bounded) and exits.
 #pragma once
 
@@ -47,11 +48,10 @@ constexpr int BM = 128;             // rows per CTA (pair: 256)
 constexpr int BN = 256;             // columns per pair tile
 constexpr int BK = 64;              // reduction elements per stage (128 bytes)
 constexpr int TILE = BM * BK * 2;   // one operand tile of one CTA: 16 KB
-constexpr int EPI_WARPS = 8;
-constexpr int WARP_TMA = 8;
-constexpr int WARP_MMA = 9;
-constexpr int THREADS = 320;
-constexpr int BOX = 32 * 128;       // one warp's staging box: 32 rows x 128 bytes
+constexpr int EPI_WARPS = 8;        // per accumulator half of a tall tile
+constexpr int threads(int mh) { return (EPI_WARPS * mh + 2) * 32; }
+constexpr int BOX = 32 * 64;        // a staging box: 32 rows x 64 bytes; 2 / MH per epilogue warp
+constexpr int BOXES = 16;
 constexpr int stages(int tiles) { return tiles == 1 ? 6 : 4; }  // by A tiles of a stage
 }  // namespace gm
 
@@ -59,7 +59,7 @@ template <int AT>
 struct GemmSmem {
     uint8_t a[gm::stages(AT)][AT][gm::TILE];  // 1024-byte aligned tiles
     uint8_t b[gm::stages(AT)][gm::TILE];
-    uint8_t box[gm::EPI_WARPS][gm::BOX];
+    uint8_t box[gm::BOXES][gm::BOX];
     uint64_t full[gm::stages(AT)];            // used in the even CTA
     uint64_t empty[gm::stages(AT)];
     uint64_t tmem_full[2];
@@ -92,7 +92,9 @@ struct GemmTile {
     int out_row;      // where that row goes: warp_row, further down for later splits
     int col0;         // first of this warp's 128 columns
     int lane;
-    uint8_t* box;     // this warp's staging box
+    uint8_t* box;     // this warp's staging boxes
+    int boxes;        // one or two
+    int stores;       // stores sent so far
 };
 
 // MN-major, 128-byte swizzle: 64 columns x 8 k per 1024-byte atom, atoms along
@@ -134,38 +136,36 @@ __device__ __forceinline__ void tma_add_2d(const CUtensorMap* map, uint32_t src,
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 
-__device__ __forceinline__ void box_put(uint8_t* box, int lane, int c, uint32_t w0, uint32_t w1, uint32_t w2,
-                                        uint32_t w3) {
-    const uint32_t a = smem_u32(box + lane * 128 + ((c ^ (lane & 7)) << 4));
-    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(w0), "r"(w1), "r"(w2), "r"(w3) : "memory");
-}
-__device__ __forceinline__ void box_wait(int lane) {  // the box's previous store has read it
-    if (lane == 0) bulk_wait_read<0>();
-    __syncwarp();
-}
-
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// 32 columns of a row as bf16 (four 16-byte units) through half h of the warp's
-// box (32 rows x 64 bytes, 64B swizzle) to columns col0 + 32 k; calls alternate
-// between the halves and wait only for the store before the last one.
-__device__ __forceinline__ void put_bf16(const GemmTile& t, int k, int h, const uint4 (&w)[4], const CUtensorMap* map) {
-    uint8_t* const half = t.box + h * (gm::BOX / 2);
-    if (t.lane == 0) bulk_wait_read<1>();
+// 64 bytes of a row (four 16-byte units: 32 bf16 or 16 fp32 columns) through one
+// of the warp's boxes (64B swizzle) to column `col` of the output; a box is
+// written again once its last store has read it.
+template <bool ADD = false>
+__device__ __forceinline__ void put_64(GemmTile& t, int col, int row0, const uint4 (&w)[4], const CUtensorMap* map) {
+    uint8_t* const box = t.box + (t.boxes == 2 ? t.stores & 1 : 0) * gm::BOX;
+    ++t.stores;
+    if (t.lane == 0) {
+        if (t.boxes == 2) bulk_wait_read<1>();
+        else bulk_wait_read<0>();
+    }
     __syncwarp();
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
         // 16-byte unit c of row r at c ^ (r / 2 mod 4)
-        const uint32_t a = smem_u32(half + t.lane * 64 + ((c ^ ((t.lane >> 1) & 3)) << 4));
+        const uint32_t a = smem_u32(box + t.lane * 64 + ((c ^ ((t.lane >> 1) & 3)) << 4));
         asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(w[c].x), "r"(w[c].y), "r"(w[c].z), "r"(w[c].w)
                      : "memory");
     }
     fence_proxy_async_smem();
     __syncwarp();
-    if (t.lane == 0) tma_store_2d(map, smem_u32(half), t.col0 + 32 * k, t.out_row);
+    if (t.lane == 0) {
+        if (ADD) tma_add_2d(map, smem_u32(box), col, t.out_row - row0);
+        else tma_store_2d(map, smem_u32(box), col, t.out_row - row0);
+    }
 }
 __device__ __forceinline__ void to_bf16(const float (&v)[32], uint4 (&w)[4]) {
 #pragma unroll
@@ -173,41 +173,43 @@ __device__ __forceinline__ void to_bf16(const float (&v)[32], uint4 (&w)[4]) {
         w[c] = make_uint4(pack_bf16(v[8 * c], v[8 * c + 1]), pack_bf16(v[8 * c + 2], v[8 * c + 3]),
                           pack_bf16(v[8 * c + 4], v[8 * c + 5]), pack_bf16(v[8 * c + 6], v[8 * c + 7]));
 }
-__device__ __forceinline__ void put_bf16(const GemmTile& t, int k, const float (&v)[32], const CUtensorMap* map) {
+// Slice k (32 columns) of a row in bf16.
+__device__ __forceinline__ void put_bf16(GemmTile& t, int k, const float (&v)[32], const CUtensorMap* map) {
     uint4 w[4];
     to_bf16(v, w);
-    put_bf16(t, k, k & 1, w, map);
+    put_64(t, t.col0 + 32 * k, 0, w, map);
 }
-
-// 32 fp32 columns of a row through the warp's box to rows out_row - row0 of
-// a matrix; added to what is there when `add`.
-__device__ __forceinline__ void put_f32(const GemmTile& t, int k, const float (&v)[32], const CUtensorMap* map, int row0,
+// Slice k of a row in fp32, to rows out_row - row0 of a matrix; added to what
+// is there when `add`.
+__device__ __forceinline__ void put_f32(GemmTile& t, int k, const float (&v)[32], const CUtensorMap* map, int row0,
                                         bool add) {
-    box_wait(t.lane);
 #pragma unroll
-    for (int c = 0; c < 8; ++c)
-        box_put(t.box, t.lane, c, __float_as_uint(v[4 * c]), __float_as_uint(v[4 * c + 1]),
-                __float_as_uint(v[4 * c + 2]), __float_as_uint(v[4 * c + 3]));
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (t.lane == 0) {
-        if (add) tma_add_2d(map, smem_u32(t.box), t.col0 + 32 * k, t.out_row - row0);
-        else tma_store_2d(map, smem_u32(t.box), t.col0 + 32 * k, t.out_row - row0);
+    for (int h = 0; h < 2; ++h) {
+        uint4 w[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const int i = 16 * h + 4 * c;
+            w[c] = make_uint4(__float_as_uint(v[i]), __float_as_uint(v[i + 1]), __float_as_uint(v[i + 2]),
+                              __float_as_uint(v[i + 3]));
+        }
+        if (add) put_64<true>(t, t.col0 + 32 * k + 16 * h, row0, w, map);
+        else put_64(t, t.col0 + 32 * k + 16 * h, row0, w, map);
     }
 }
 
 // Epi: a struct with
 //   struct Params (a kernel argument, may hold tensor maps), static prefetch(const Params&),
-//   Epi(const Params&), begin(const GemmTile&), slice(const GemmTile&, int k, float (&v)[32])
+//   Epi(const Params&), begin(const GemmTile&), slice(GemmTile&, int k, float (&v)[32])
 //   for columns col0 + 32 k .. + 31 of the thread's row (k = 0..3 in order), end(const GemmTile&).
 template <class Epi, int NA, int MH, bool A_MN, bool B_MN, bool FP16, int SEGMENT>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gm::THREADS, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gm::threads(MH), 1)
     gemm_f16_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
                     const __grid_constant__ typename Epi::Params params, const GemmShape shape, unsigned* status) {
     static_assert(MH == 1 || (NA == 1 && SEGMENT == 0), "a tall tile has one A and one sum per row");
     constexpr int AT = NA * MH;  // A tiles of a stage
     constexpr int STAGES = gm::stages(AT);
     constexpr int ROWS = 2 * gm::BM * MH;  // rows of a tile
+    constexpr int EPI = gm::EPI_WARPS * MH, WARP_TMA = EPI, WARP_MMA = EPI + 1;
     extern __shared__ uint8_t smem_raw[];
     auto* sm = reinterpret_cast<GemmSmem<AT>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     volatile int* abort_flag = &sm->abort_flag;
@@ -239,7 +241,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gm::THREADS, 1)
         sm->abort_flag = 0;
         fence_barrier_init();
     }
-    if (warp == gm::WARP_MMA) {
+    if (warp == WARP_MMA) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm->tmem_base)),
                      "r"(2 * gm::BN)
                      : "memory");
@@ -269,14 +271,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gm::THREADS, 1)
         n0 = (first + rem % width) * gm::BN;
     };
 
-    if (warp < gm::EPI_WARPS) {
+    if (warp < EPI) {
         // ------------------------------------------------------------ epilogue
-        const int qd = warp & 3, half = warp >> 2;
+        const int qd = warp & 3, half = (warp >> 2) & 1;
         const uint32_t lane_addr = static_cast<uint32_t>(qd * 32) << 16;
         Epi epi(params);
         GemmTile t;
         t.lane = lane;
-        t.box = sm->box[warp];
+        t.boxes = 2 / MH;
+        t.stores = 0;
+        t.box = sm->box[warp * t.boxes];
         uint32_t seg = 0;  // accumulator buffers taken so far
         auto release = [&](int b) {  // every load of the buffer has completed
             tc_fence_before();
@@ -321,16 +325,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gm::THREADS, 1)
                 for (int k = 0; k < 4; ++k) epi.slice(t, k, acc[k]);
                 epi.end(t);
             } else {
-                // MH = 2: the upper, then the lower half of the tile, in buffers 0 and 1
-                for (int j = 0; j < MH; ++j, ++seg) {
-                    t.warp_row = t.m0 + 2 * gm::BM * j + static_cast<int>(rank) * gm::BM + qd * 32;
-                    t.row = t.warp_row + lane;
-                    t.out_row = t.warp_row + split * shape.split_rows;
-                    epi.begin(t);
-                    const int b = seg & 1;
-                    if (!warp_wait(&sm->tmem_full[b], (seg >> 1) & 1, abort_flag)) { give_up(); ok = false; break; }
-                    tc_fence_after();
-                    const uint32_t tbase = tmem_base + lane_addr + b * gm::BN + half * (gm::BN / 2);
+                // MH = 2: this warp's half of the tile is in buffer j
+                const int j = MH == 2 ? warp >> 3 : 0, b = MH == 2 ? j : seg & 1;
+                const uint32_t phase = MH == 2 ? seg & 1 : (seg >> 1) & 1;
+                ++seg;
+                t.warp_row = t.m0 + 2 * gm::BM * j + static_cast<int>(rank) * gm::BM + qd * 32;
+                t.row = t.warp_row + lane;
+                t.out_row = t.warp_row + split * shape.split_rows;
+                epi.begin(t);
+                if (!warp_wait(&sm->tmem_full[b], phase, abort_flag)) { give_up(); break; }
+                tc_fence_after();
+                const uint32_t tbase = tmem_base + lane_addr + b * gm::BN + half * (gm::BN / 2);
+                if constexpr (MH == 2) {
+                    // sixteen warps hide each other's loads
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t r[32];
+                        tmem_ld32_nowait(tbase + 32 * k, r);
+                        tmem_wait_into(r);
+                        if (k == 3) release(b);
+                        float v[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+                        epi.slice(t, k, v);
+                    }
+                } else {
                     uint32_t ra[32], rb[32];
                     tmem_ld32_nowait(tbase, ra);
                     tmem_wait_into(ra);
@@ -346,12 +365,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gm::THREADS, 1)
                         epi.slice(t, k, v);
                         if (k < 3) tmem_wait_into(nxt);
                     }
-                    epi.end(t);
                 }
+                epi.end(t);
             }
         }
         if (lane == 0) bulk_wait_all();
-    } else if (warp == gm::WARP_TMA) {
+    } else if (warp == WARP_TMA) {
         // ------------------------------------------------------------ TMA producer
         if (lane == 0) {
             uint32_t it = 0;
@@ -459,7 +478,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gm::THREADS, 1)
 
     tc_fence_before();
     cluster_sync();  // neither CTA leaves while the other may still touch its shared memory
-    if (warp == gm::WARP_MMA) {
+    if (warp == WARP_MMA) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(2 * gm::BN)
                      : "memory");
@@ -481,6 +500,11 @@ inline bool gemm_map(CUtensorMap* map, CUtensorMapDataType type, const void* bas
     const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)};
     return enc(map, type, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// An fp32 result, stored by put_f32.
+inline bool gemm_result_f32(CUtensorMap* map, void* base, long long rows, long long cols) {
+    return gemm_map(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, base, rows, cols, cols * 4, 16, 32, CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 // A bf16 result, stored by put_bf16.
@@ -510,7 +534,7 @@ cudaError_t launch_gemm_f16(const CUtensorMap& a, const CUtensorMap& b, const ty
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2);
-    cfg.blockDim = dim3(gm::THREADS);
+    cfg.blockDim = dim3(gm::threads(MH));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     if (clusters[dev] == 0) {

@@ -55,13 +55,13 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
-// Forward epilogue: part[p][t] = (max, sum of exp(z - max)) over columns 128 p .. + 127.
+// Forward epilogue: part[t][p] = (max, sum of exp(z - max)) over columns 128 p .. + 127.
 struct LsePart {
     struct Params {
         float2* part;
         float* tlogit;
         const long long* target;
-        int T, V;
+        int T, V, P;  // P: parts of a row
     };
     static __device__ __forceinline__ void prefetch(const Params&) {}
     const Params& p;
@@ -73,7 +73,7 @@ struct LsePart {
         sum = 0.f;
         tcol = t.row < p.T ? __ldg(p.target + t.row) - t.col0 : -1;
     }
-    __device__ __forceinline__ void slice(const GemmTile& t, int k, float (&v)[32]) {
+    __device__ __forceinline__ void slice(GemmTile& t, int k, float (&v)[32]) {
         const int valid = p.V - (t.col0 + 32 * k);
         if (valid <= 0) return;
         if (valid < 32) {
@@ -108,7 +108,7 @@ struct LsePart {
         mx = m;
     }
     __device__ __forceinline__ void end(const GemmTile& t) {
-        if (t.row < p.T && t.col0 < p.V) p.part[static_cast<size_t>(t.col0 >> 7) * p.T + t.row] = make_float2(mx, sum);
+        if (t.row < p.T && t.col0 < p.V) p.part[static_cast<size_t>(t.row) * p.P + (t.col0 >> 7)] = make_float2(mx, sum);
     }
 };
 
@@ -143,7 +143,7 @@ struct GradTile {
         }
         if (d == 0.f) less = -INFINITY;  // exp becomes 0: the row writes zeros
     }
-    __device__ __forceinline__ void slice(const GemmTile& t, int k, float (&v)[32]) {
+    __device__ __forceinline__ void slice(GemmTile& t, int k, float (&v)[32]) {
         const float2 l2 = both(kLog2e), ls = both(less);
 #pragma unroll
         for (int i = 0; i < 32; i += 2) {
@@ -173,7 +173,7 @@ struct GradTile {
             }
             uint4 w[4];
             to_bf16(v, w);
-            put_bf16(t, k, 0, w, &p.g);
+            put_64(t, t.col0 + 32 * k, 0, w, &p.g);
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const uint32_t h[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
@@ -184,7 +184,7 @@ struct GradTile {
                 }
             }
             to_bf16(v, w);
-            put_bf16(t, k, 1, w, &p.g_low);
+            put_64(t, t.col0 + 32 * k, 0, w, &p.g_low);
         } else {
             put_bf16(t, k, v, &p.g);
         }
@@ -202,7 +202,7 @@ struct SumF32 {
     const Params& p;
     __device__ __forceinline__ explicit SumF32(const Params& q) : p(q) {}
     __device__ __forceinline__ void begin(const GemmTile&) {}
-    __device__ __forceinline__ void slice(const GemmTile& t, int k, float (&v)[32]) {
+    __device__ __forceinline__ void slice(GemmTile& t, int k, float (&v)[32]) {
         put_f32(t, k, v, &p.out, 0, p.add != 0);
     }
     __device__ __forceinline__ void end(const GemmTile&) {}
@@ -219,7 +219,7 @@ struct ScaledBf16 {
     float c;
     __device__ __forceinline__ explicit ScaledBf16(const Params& q) : p(q), c(*q.cmax) {}
     __device__ __forceinline__ void begin(const GemmTile&) {}
-    __device__ __forceinline__ void slice(const GemmTile& t, int k, float (&v)[32]) {
+    __device__ __forceinline__ void slice(GemmTile& t, int k, float (&v)[32]) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] *= c;
         put_bf16(t, k, v, &p.out);
@@ -227,30 +227,42 @@ struct ScaledBf16 {
     __device__ __forceinline__ void end(const GemmTile&) {}
 };
 
-// Joins the P parts of 32 rows per block (lane = row, warp = every 32nd part),
-// in a fixed order.
-__global__ void __launch_bounds__(1024)
+// Joins the P parts of a row in one warp, in a fixed order.
+__global__ void __launch_bounds__(256)
     xent_merge_kernel(const float2* __restrict__ part, const float* __restrict__ tlogit,
                       const long long* __restrict__ target, long long ignore, int T, int V, int P,
                       float* __restrict__ loss, float* __restrict__ lse_out, unsigned* status) {
-    __shared__ float2 s[32][33];
     asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
-    const int t = blockIdx.x * 32 + lane;
+    const int lane = threadIdx.x & 31;
+    const long long t = blockIdx.x * 8ll + (threadIdx.x >> 5);
+    if (t >= T) return;
+    const float2* const row = part + static_cast<size_t>(t) * P;
+    // every part has a column, so its sum has a term 1 (or is NaN); the empty
+    // start of a lane past the last part has the sum 0
     float m = -INFINITY, sum = 0.f;
-    auto join = [&](float2 q) {
-        if (q.y == 0.f) return;  // no columns (a sum of exponentials has a term 1; NaN passes)
-        const float n = fmaxf(m, q.x);
-        sum = (sum == 0.f ? 0.f : sum * exp2_fast((m - n) * kLog2e)) + q.y * exp2_fast((q.x - n) * kLog2e);
+    auto join = [&](float qm, float qs) {
+        const float n = fmaxf(m, qm);
+        sum = (sum == 0.f ? 0.f : sum * exp2_fast((m - n) * kLog2e)) + (qs == 0.f ? 0.f : qs * exp2_fast((qm - n) * kLog2e));
         m = n;
     };
-    if (t < T)
-        for (int p = slice; p < P; p += 32) join(__ldg(part + static_cast<size_t>(p) * T + t));
-    s[slice][lane] = make_float2(m, sum);
-    __syncthreads();
-    if (slice != 0 || t >= T) return;
-    for (int i = 1; i < 32; ++i) join(s[i][lane]);
+    int p = lane;
+    for (; p + 96 < P; p += 128) {  // four loads in flight
+        const float2 a = __ldg(row + p), b = __ldg(row + p + 32), c = __ldg(row + p + 64), d = __ldg(row + p + 96);
+        const float n = fmaxf(fmaxf(m, fmaxf(a.x, b.x)), fmaxf(c.x, d.x));
+        const float s0 = a.y * exp2_fast((a.x - n) * kLog2e) + b.y * exp2_fast((b.x - n) * kLog2e);
+        const float s1 = c.y * exp2_fast((c.x - n) * kLog2e) + d.y * exp2_fast((d.x - n) * kLog2e);
+        sum = (sum == 0.f ? 0.f : sum * exp2_fast((m - n) * kLog2e)) + (s0 + s1);
+        m = n;
+    }
+    for (; p < P; p += 32) {
+        const float2 q = __ldg(row + p);
+        join(q.x, q.y);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+        join(__shfl_xor_sync(0xFFFFFFFFu, m, off), __shfl_xor_sync(0xFFFFFFFFu, sum, off));
+    if (lane != 0) return;
     const float lse = m + logf(sum);
     const long long y = target[t];
     float l = 0.f;
@@ -328,23 +340,25 @@ long long piece_words(long long T, long long V) {
 constexpr int kPartsTokens = 128;
 bool g_parts(long long T) { return T <= kPartsTokens; }
 
-// dX has few tiles (T / 512 x D / 256) and a long reduction: it is cut into
-// the fewest parts, up to 8, that keep at least 95% of the pairs of SMs busy in
-// every round of tiles (or the most that any number keeps).  Each part has its
-// own fp32 sums over the pieces; xent_dx_kernel adds them in order.
+// dX has few tiles (T / 512 x D / 256) and a long reduction: it may be cut into
+// up to 8 parts, so that the last round of tiles keeps more pairs of SMs busy.
+// Each part has its own fp32 sums over the pieces, which xent_dx_kernel adds in
+// order; a cut has to save more of the product's time (at 1.3 PFLOP/s) than twice
+// what reading the sums costs (at 6 TB/s).  8192 x 128000 x 896: 8 parts save 209
+// us, their sums cost 39 us; 4096 x 32000 x 2048: 62 us and 45 us, not cut.
 long long dx_rows(long long T) { return (T + 511) / 512 * 512; }
-int dx_splits(long long T, long long D, int num_sms) {
+int dx_splits(long long T, long long D, long long V, int num_sms) {
     const long long pairs = num_sms / 2, tiles = dx_rows(T) / 512 * ((D + gm::BN - 1) / gm::BN);
+    const double product = 2.0 * T * V * D / 1.3e15, sums = 4.0 * dx_rows(T) * D / 6e12;
     int best = 1;
-    double most = 0.0;
+    double least = 0.0;
     for (int s = 1; s <= 8; ++s) {
         const long long n = tiles * s, rounds = (n + pairs - 1) / pairs;
-        const double busy = static_cast<double>(n) / static_cast<double>(rounds * pairs);
-        if (busy > most + 1e-9) {
-            most = busy;
+        const double cost = product * static_cast<double>(rounds * pairs) / static_cast<double>(n) + 2.0 * s * sums;
+        if (s == 1 || cost < least) {
+            least = cost;
             best = s;
         }
-        if (busy >= 0.95) break;
     }
     return best;
 }
@@ -364,7 +378,7 @@ size_t xent_workspace_bytes(long long T, long long V) {
 }
 
 size_t xent_backward_workspace_bytes(long long T, long long D, long long V, int need_dx, int num_sms) {
-    return 256 + (need_dx ? round256(static_cast<size_t>(dx_splits(T, D, num_sms)) * dx_rows(T) * D * sizeof(float)) : 0) +
+    return 256 + (need_dx ? round256(static_cast<size_t>(dx_splits(T, D, V, num_sms)) * dx_rows(T) * D * sizeof(float)) : 0) +
            round256(static_cast<size_t>(T) * piece_words(T, V) * (g_parts(T) ? 4 : 2));
 }
 
@@ -377,14 +391,14 @@ cudaError_t launch_xent(const uint16_t* x, long long T, long long D, const uint1
     CUtensorMap a, b;
     if (!gemm_operand(&a, false, false, x, T, D, D) || !gemm_operand(&b, false, false, w, V, D, D))
         return cudaErrorInvalidValue;
-    const LsePart::Params p{part, tlogit, target, static_cast<int>(T), static_cast<int>(V)};
+    const LsePart::Params p{part, tlogit, target, static_cast<int>(T), static_cast<int>(V), parts(V)};
     const GemmShape shape{static_cast<int>(T), static_cast<int>(V), static_cast<int>(D), 0, 8, 1, 0};
     // one segment holds the whole sum: tall tiles need none
     const bool tall = D <= kLogitSegment * gm::BK && gemm_tall(T, V, 1, num_sms);
     if (cudaError_t e = tall ? launch_gemm_f16<LsePart, 1, 2, false, false, false, 0>(a, b, p, shape, status, st)
                              : launch_gemm_f16<LsePart, 1, 1, false, false, false, kLogitSegment>(a, b, p, shape, status, st))
         return e;
-    return pdl_launch(xent_merge_kernel, dim3(static_cast<unsigned>((T + 31) / 32)), dim3(1024), 0, st,
+    return pdl_launch(xent_merge_kernel, dim3(static_cast<unsigned>((T + 7) / 8)), dim3(256), 0, st,
                       static_cast<const float2*>(part), static_cast<const float*>(tlogit), target, ignore,
                       static_cast<int>(T), static_cast<int>(V), parts(V), loss, lse, status);
 }
@@ -392,7 +406,7 @@ cudaError_t launch_xent(const uint16_t* x, long long T, long long D, const uint1
 cudaError_t launch_xent_backward(const float* dloss, const uint16_t* x, long long T, long long D, const uint16_t* w,
                                  long long V, const long long* target, long long ignore, const float* lse, uint16_t* dx,
                                  uint16_t* dw, void* ws, unsigned* status, int num_sms, cudaStream_t st) {
-    const int splits = dx_splits(T, D, num_sms);
+    const int splits = dx_splits(T, D, V, num_sms);
     const long long rows = dx_rows(T);
     uint8_t* at = static_cast<uint8_t*>(ws);
     float* cmax = reinterpret_cast<float*>(at);
@@ -444,7 +458,7 @@ cudaError_t launch_xent_backward(const float* dloss, const uint16_t* x, long lon
             SumF32::Params sp;
             sp.add = v0 > 0;
             if (!gemm_operand(&gk, false, false, g, T, g_cols, pitch) || !gemm_operand(&wn, false, true, wp, n, D, D) ||
-                !gemm_map(&sp.out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, dx32, splits * rows, D, D * 4, 32, 32))
+                !gemm_result_f32(&sp.out, dx32, splits * rows, D))
                 return cudaErrorInvalidValue;
             const GemmShape shape{Ti, Di, ni, low, d_panel, splits, static_cast<int>(rows)};
             e = parts ? launch_gemm_f16<SumF32, 2, 1, false, true, false, 0>(gk, wn, sp, shape, status, st)
