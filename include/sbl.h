@@ -403,8 +403,7 @@ sbl_status sbl_linear_cross_entropy(const uint16_t* x_bf16, int64_t T, int64_t D
  *             overwritten (dw with zeros for T == 0).
  *   workspace sbl_linear_cross_entropy_backward_workspace_bytes(T, D, V, dx != NULL)
  *             bytes, 256-byte aligned (at most 512 MB for the gradient of one
- *             piece of the logits, more only for T > 2^17, and fp32 sums of dx;
- *             depends on the current device's SM count).
+ *             piece of the logits, more only for T > 2^17, and fp32 sums of dx).
  * The logits are computed again, one piece of the vocabulary at a time.  G is
  * rounded to bf16 for the tensor cores (relative to max |dloss|, so a uniform
  * dloss is exact); sums are fp32, and dx and dw are rounded once.  The same

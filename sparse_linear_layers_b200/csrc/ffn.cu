@@ -737,7 +737,7 @@ struct FfnOperands {
     int split_blocks, code_blocks, x_blocks;
 };
 
-// Three copies in one launch: blocks split into ranges, 256 threads, items of 8 or 16 elements.
+// Up to three copies in one launch: blocks split into ranges, 256 threads, items of 8 or 16 elements.
 __global__ void __launch_bounds__(256) ffn_operands_kernel(const FfnOperands q) {
     asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -839,12 +839,12 @@ struct FfnDx {
     __device__ __forceinline__ void slice(GemmTile& t, int k, float (&v)[32]) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = (v[i] * e) * s;
-        put_f32(t, k, v, &p.out, 0, false);
+        if (t.warp_row < p.T) put_f32(t, k, v, &p.out, 0, false);  // later rows are the next part's
     }
     __device__ __forceinline__ void end(const GemmTile&) {}
 };
 
-// dX from the parts of a split reduction, added in order; 4 elements per thread.
+// The parts of a split reduction, added in order; 4 elements per thread.
 __global__ void __launch_bounds__(256) ffn_sum_kernel(const float4* __restrict__ parts, int splits, long long stride4,
                                                       long long n4, float4* __restrict__ out) {
     asm volatile("griddepcontrol.launch_dependents;");
@@ -867,7 +867,7 @@ struct FfnDw {
         const unsigned* all_max;
         const float* scale_g;
         const float* scale_u;
-        int F, Fp, want_g, want_u, ternary;
+        int F, Fp, up_row, want_g, want_u, ternary;  // up_row: row of the up's first in its output
     };
     static __device__ __forceinline__ void prefetch(const Params& p) {
         if (p.want_g) prefetch_tmap(&p.out_g);
@@ -887,7 +887,7 @@ struct FfnDw {
         if (up ? !p.want_u : !p.want_g) return;
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = (v[i] * e) * s;
-        put_f32(t, k, v, up ? &p.out_u : &p.out_g, up ? p.Fp : 0, false);
+        put_f32(t, k, v, up ? &p.out_u : &p.out_g, up ? p.up_row : 0, false);
     }
     __device__ __forceinline__ void end(const GemmTile&) {}
 };
@@ -912,10 +912,19 @@ FfnSpace ffn_space(long long T, long long K, long long F) {
     return s;
 }
 
+// Parts of the two gradients' reductions (over 2 Fp hidden units, over T).
+int dx_splits(long long T, long long K, long long Fp) {
+    return gemm_splits((T + 255) / 256 * ((K + gm::BN - 1) / gm::BN), 2 * Fp / gm::BK, 4.0 * T * K, 0.8, 32);
+}
+int dw_splits(long long T, long long K, long long Fp) {
+    return gemm_splits((2 * Fp + 255) / 256 * ((K + gm::BN - 1) / gm::BN), (T + gm::BK - 1) / gm::BK, 8.0 * Fp * K, 0.8, 32);
+}
+
 struct FfnBwdSpace {
     FfnSpace fwd;
-    size_t maxima, v, parts, codes, xs, end;
-    long long Fp, nmax16;
+    size_t maxima, v, parts, codes, xs, sums, end;
+    long long Fp, nmax16, dx_rows;
+    int dx_splits, dw_splits;
 };
 FfnBwdSpace ffn_bwd_space(long long T, long long K, long long F, int need_dx, int need_dw) {
     FfnBwdSpace s;
@@ -927,7 +936,14 @@ FfnBwdSpace ffn_bwd_space(long long T, long long K, long long F, int need_dx, in
     s.parts = s.v + round256(static_cast<size_t>(T) * 2 * s.Fp * 4);
     s.codes = s.parts + round256(static_cast<size_t>(T) * 4 * s.Fp * 2);
     s.xs = s.codes + (need_dx ? round256(static_cast<size_t>(2) * s.Fp * K * 2) : 0);
-    s.end = s.xs + (need_dw ? round256(static_cast<size_t>(T) * K * 2) : 0);
+    s.sums = s.xs + (need_dw ? round256(static_cast<size_t>(T) * K * 2) : 0);
+    // the parts of a split reduction; dX's have been added before dW's are written
+    s.dx_rows = (T + 31) / 32 * 32;
+    s.dx_splits = need_dx ? dx_splits(T, K, s.Fp) : 1;
+    s.dw_splits = need_dw ? dw_splits(T, K, s.Fp) : 1;
+    const size_t a = s.dx_splits > 1 ? static_cast<size_t>(s.dx_splits) * s.dx_rows * K * 4 : 0;
+    const size_t b = s.dw_splits > 1 ? static_cast<size_t>(s.dw_splits) * 2 * s.Fp * K * 4 : 0;
+    s.end = s.sums + round256(a > b ? a : b);
     return s;
 }
 
@@ -1110,13 +1126,10 @@ cudaError_t launch_ffn_backward(const float* dh, const uint16_t* x, long long T,
     float* const v = reinterpret_cast<float*>(base + sp.v);
     unsigned* const row_max = reinterpret_cast<unsigned*>(base + sp.maxima);
     unsigned* const all_max = row_max + T;
-    q.dh = dh;
-    q.row_max = row_max;
+    const int8_t* const xq = reinterpret_cast<const int8_t*>(base + sp.fwd.xq);
+    const float* const s_tok = q.s_tok;
     q.all_max = all_max;
     q.Fp = Fp;
-    if (!gemm_map(&q.out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, v, T, 2 * sp.Fp, 2 * sp.Fp * 4, 32, 32)) return cudaErrorInvalidValue;
-    if (cudaError_t e = act == kActSilu ? launch_pair<true, 0>(q, status, st) : launch_pair<true, 1>(q, status, st)) return e;
-
     __half* const parts = reinterpret_cast<__half*>(base + sp.parts);
     __half* const codes = reinterpret_cast<__half*>(base + sp.codes);
     __half* const xs = reinterpret_cast<__half*>(base + sp.xs);
@@ -1126,18 +1139,22 @@ cudaError_t launch_ffn_backward(const float* dh, const uint16_t* x, long long T,
     };
     FfnOperands o;
     o.v = v;
-    o.row_max = row_max;
     o.all_max = all_max;
     o.pg = pg;
     o.pu = pu;
-    o.xq = reinterpret_cast<const int8_t*>(base + sp.fwd.xq);
-    o.parts = parts;
+    o.xq = xq;
     o.codes = codes;
     o.xs = xs;
-    o.T = Ti;
     o.K = Ki;
     o.F = Fi;
     o.Fp = Fp;
+    q.dh = dh;
+    q.row_max = row_max;
+    if (!gemm_map(&q.out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, v, T, 2 * sp.Fp, 2 * sp.Fp * 4, 32, 32)) return cudaErrorInvalidValue;
+    if (cudaError_t e = act == kActSilu ? launch_pair<true, 0>(q, status, st) : launch_pair<true, 1>(q, status, st)) return e;
+    o.row_max = row_max;
+    o.parts = parts;
+    o.T = Ti;
     o.split_blocks = blocks_for(T * (2 * sp.Fp / 8), 8);
     o.code_blocks = dx ? blocks_for(2 * sp.Fp * (K / 16), 4) : 0;
     o.x_blocks = need_dw ? blocks_for(T * (K / 16), 4) : 0;
@@ -1145,50 +1162,54 @@ cudaError_t launch_ffn_backward(const float* dh, const uint16_t* x, long long T,
         return e;
 
     const int k_panel = (Ki + gm::BN - 1) / gm::BN;
+    float* const sums = reinterpret_cast<float*>(base + sp.sums);
+    // adds the parts of `rows` rows that start at row0 of each
+    auto join = [&](int splits, long long split_rows, long long row0, long long rows, float* out) {
+        return pdl_launch(ffn_sum_kernel, dim3(blocks_for(rows * K / 4, 8)), dim3(256), 0, st,
+                          reinterpret_cast<const float4*>(sums + row0 * K), splits, split_rows * K / 4, rows * K / 4,
+                          reinterpret_cast<float4*>(out));
+    };
     if (dx) {
-        // few tiles: the reduction in parts, one for each that the idle SMs can
-        // take and v's memory, free by now, can hold
-        const long long rows = (T + 255) / 256 * 256, tiles = rows / 256 * k_panel;
-        int splits = static_cast<int>(num_sms / 2 / tiles);
-        if (splits > 8) splits = 8;
-        while (splits > 1 && splits * rows * K > T * 2 * sp.Fp) --splits;
-        if (splits < 1) splits = 1;
         CUtensorMap a, b;
         FfnDx::Params p;
+        const int splits = sp.dx_splits;
         if (!gemm_operand(&a, true, false, parts, T, 4 * sp.Fp, 4 * sp.Fp) ||
             !gemm_operand(&b, true, true, codes, 2 * sp.Fp, K, K) ||
-            !gemm_result_f32(&p.out, splits > 1 ? v : dx, splits > 1 ? splits * rows : T, K))
+            !gemm_result_f32(&p.out, splits > 1 ? sums : dx, splits > 1 ? splits * sp.dx_rows : T, K))
             return cudaErrorInvalidValue;
         p.row_max = row_max;
-        p.s_tok = q.s_tok;
+        p.s_tok = s_tok;
         p.T = Ti;
-        const GemmShape shape{Ti, Ki, 2 * Fp, 2 * Fp, k_panel, splits, static_cast<int>(rows)};
+        const GemmShape shape{Ti, Ki, 2 * Fp, 2 * Fp, k_panel, splits, static_cast<int>(sp.dx_rows)};
         if (cudaError_t e = launch_gemm_f16<FfnDx, 2, 1, false, true, true, 4>(a, b, p, shape, status, st)) return e;
         if (splits > 1)
-            if (cudaError_t e = pdl_launch(ffn_sum_kernel, dim3(blocks_for(T * K / 4, 8)), dim3(256), 0, st,
-                                           reinterpret_cast<const float4*>(v), splits, rows * K / 4, T * K / 4,
-                                           reinterpret_cast<float4*>(dx)))
-                return e;
+            if (cudaError_t e = join(splits, sp.dx_rows, 0, T, dx)) return e;
     }
     if (need_dw) {
         CUtensorMap a, b;
         FfnDw::Params p;
         memset(&p, 0, sizeof(p));
-        if (!gemm_operand(&a, true, true, parts, T, 4 * sp.Fp, 4 * sp.Fp) || !gemm_operand(&b, true, true, xs, T, K, K) ||
-            (dwg && !gemm_result_f32(&p.out_g, dwg, F, K)) ||
-            (dwu && !gemm_result_f32(&p.out_u, dwu, F, K)))
+        const int splits = sp.dw_splits;
+        if (!gemm_operand(&a, true, true, parts, T, 4 * sp.Fp, 4 * sp.Fp) || !gemm_operand(&b, true, true, xs, T, K, K))
+            return cudaErrorInvalidValue;
+        if (splits > 1 ? !gemm_result_f32(&p.out_g, sums, splits * 2 * sp.Fp, K) || !gemm_result_f32(&p.out_u, sums, splits * 2 * sp.Fp, K)
+                       : (dwg && !gemm_result_f32(&p.out_g, dwg, F, K)) || (dwu && !gemm_result_f32(&p.out_u, dwu, F, K)))
             return cudaErrorInvalidValue;
         p.all_max = all_max;
         p.scale_g = scale_g;
         p.scale_u = scale_u;
         p.F = Fi;
         p.Fp = Fp;
+        p.up_row = splits > 1 ? 0 : Fp;
         p.want_g = dwg != nullptr;
         p.want_u = dwu != nullptr;
         p.ternary = ternary;
-        if (cudaError_t e = launch_gemm_f16<FfnDw, 2, 1, true, true, true, 4>(a, b, p, GemmShape{2 * Fp, Ki, Ti, 2 * Fp, k_panel, 1, 0},
-                                                                           status, st))
-            return e;
+        const GemmShape shape{2 * Fp, Ki, Ti, 2 * Fp, k_panel, splits, 2 * Fp};
+        if (cudaError_t e = launch_gemm_f16<FfnDw, 2, 1, true, true, true, 4>(a, b, p, shape, status, st)) return e;
+        if (splits > 1 && dwg)
+            if (cudaError_t e = join(splits, 2 * sp.Fp, 0, F, dwg)) return e;
+        if (splits > 1 && dwu)
+            if (cudaError_t e = join(splits, 2 * sp.Fp, sp.Fp, F, dwu)) return e;
     }
     return cudaSuccess;
 }

@@ -82,7 +82,7 @@ struct GemmShape {
     int a_part;
     int panel;      // consecutive tiles walk across `panel` column tiles, then down M
     int splits;     // parts of the reduction, each a GEMM of its own into rows
-    int split_rows; // split_rows further down (a multiple of the tile's rows)
+    int split_rows; // split_rows further down (whole staging boxes: a multiple of 32)
 };
 
 struct GemmTile {
@@ -555,6 +555,27 @@ cudaError_t launch_gemm_f16(const CUtensorMap& a, const CUtensorMap& b, const ty
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kern, a, b, p, shape, status);
+}
+
+// Parts that a reduction of KB k-blocks is best cut into, when each part's fp32
+// result (part_bytes) is written and read back: `tiles` tiles take rounds of 74
+// pairs of SMs, a k-block of a tile about us_per_block (what L2 feeds a pair:
+// 0.55 us for 256 rows and one A, 0.8 us for 512 rows or two A), the sum over
+// the parts 3 us and its bytes at 6 TB/s.  1 token, 2 tiles of 619 k-blocks: 37 parts
+// (one part took 200 us); 1001 tokens, 16 tiles of 88: 4 parts (59 us -> 25 us).
+inline int gemm_splits(long long tiles, long long KB, double part_bytes, double us_per_block, int most) {
+    int best = 1;
+    double least = 0.0;
+    for (int s = 1; s <= most && s <= KB; ++s) {
+        const double rounds = static_cast<double>((tiles * s + 73) / 74);
+        const double cost = rounds * static_cast<double>((KB + s - 1) / s) * us_per_block +
+                            (s > 1 ? 3.0 + s * 2.0 * part_bytes / 6e6 : 0.0);
+        if (s == 1 || cost < least) {
+            least = cost;
+            best = s;
+        }
+    }
+    return best;
 }
 
 // Whether 512-row tiles move fewer bytes than 256-row ones (48 KB against 32 KB

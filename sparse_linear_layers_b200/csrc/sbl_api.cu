@@ -81,7 +81,7 @@ cudaError_t launch_ffn_backward(const float* dh, const uint16_t* x, long long T,
                                 float* dx, float* dwg, float* dwu, int ternary, void* ws, unsigned* status, int num_sms,
                                 cudaStream_t st);
 size_t xent_workspace_bytes(long long T, long long V);
-size_t xent_backward_workspace_bytes(long long T, long long D, long long V, int need_dx, int num_sms);
+size_t xent_backward_workspace_bytes(long long T, long long D, long long V, int need_dx);
 cudaError_t launch_xent(const uint16_t* x, long long T, long long D, const uint16_t* w, long long V,
                         const long long* target, long long ignore, float* loss, float* lse, void* ws, unsigned* status,
                         int num_sms, cudaStream_t st);
@@ -473,9 +473,7 @@ sbl_status sbl_linear_cross_entropy(const uint16_t* x_bf16, int64_t T, int64_t D
 }
 
 size_t sbl_linear_cross_entropy_backward_workspace_bytes(int64_t T, int64_t D, int64_t V, int need_dx) {
-    DeviceInfo* d;
-    if (check_xent(T, D, V) || T == 0 || device_info(&d)) return 0;
-    return sbl::xent_backward_workspace_bytes(T, D, V, need_dx, d->num_sms);
+    return check_xent(T, D, V) || T == 0 ? 0 : sbl::xent_backward_workspace_bytes(T, D, V, need_dx);
 }
 
 sbl_status sbl_linear_cross_entropy_backward(const float* dloss, const uint16_t* x_bf16, int64_t T, int64_t D,
@@ -488,11 +486,11 @@ sbl_status sbl_linear_cross_entropy_backward(const float* dloss, const uint16_t*
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (T == 0) return dw ? from_cuda(cudaMemsetAsync(dw, 0, static_cast<size_t>(V) * D * 2, st)) : SBL_OK;
     if (!xent_inputs_ok(x_bf16, w_bf16, target, dloss, lse)) return SBL_ERR_INVALID_ARG;
-    if (!workspace || !aligned(workspace, 256)) return SBL_ERR_WORKSPACE;
+    if (!workspace || !aligned(workspace, 256) ||
+        workspace_bytes < sbl::xent_backward_workspace_bytes(T, D, V, dx != nullptr))
+        return SBL_ERR_WORKSPACE;
     DeviceInfo* d;
     if (sbl_status s = device_info(&d)) return s;
-    if (workspace_bytes < sbl::xent_backward_workspace_bytes(T, D, V, dx != nullptr, d->num_sms))
-        return SBL_ERR_WORKSPACE;
     return from_cuda(sbl::launch_xent_backward(dloss, x_bf16, T, D, w_bf16, V,
                                                reinterpret_cast<const long long*>(target), ignore_index, lse, dx, dw,
                                                workspace, d->status, d->num_sms, st));

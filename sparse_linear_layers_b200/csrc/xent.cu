@@ -47,6 +47,9 @@ namespace {
 // one piece, D = 2048 left lse 1.5e-6 off (the tensor cores' rounding towards
 // zero), three times what a sum rounded to nearest leaves.
 constexpr int kLogitSegment = 16;
+// Up to 256 tokens, whose time is W's way from memory, segments of 4: over few
+// losses, some of them small, the sum's error shows (a token: 1e-6 of its loss).
+constexpr int kFewSegment = 4;
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -196,14 +199,14 @@ struct GradTile {
 struct SumF32 {
     struct Params {
         CUtensorMap out;
-        int add;
+        int add, rows;
     };
     static __device__ __forceinline__ void prefetch(const Params& p) { prefetch_tmap(&p.out); }
     const Params& p;
     __device__ __forceinline__ explicit SumF32(const Params& q) : p(q) {}
     __device__ __forceinline__ void begin(const GemmTile&) {}
     __device__ __forceinline__ void slice(GemmTile& t, int k, float (&v)[32]) {
-        put_f32(t, k, v, &p.out, 0, p.add != 0);
+        if (t.warp_row < p.rows) put_f32(t, k, v, &p.out, 0, p.add != 0);  // later rows are the next part's
     }
     __device__ __forceinline__ void end(const GemmTile&) {}
 };
@@ -340,27 +343,14 @@ long long piece_words(long long T, long long V) {
 constexpr int kPartsTokens = 128;
 bool g_parts(long long T) { return T <= kPartsTokens; }
 
-// dX has few tiles (T / 512 x D / 256) and a long reduction: it may be cut into
-// up to 8 parts, so that the last round of tiles keeps more pairs of SMs busy.
-// Each part has its own fp32 sums over the pieces, which xent_dx_kernel adds in
-// order; a cut has to save more of the product's time (at 1.3 PFLOP/s) than twice
-// what reading the sums costs (at 6 TB/s).  8192 x 128000 x 896: 8 parts save 209
-// us, their sums cost 39 us; 4096 x 32000 x 2048: 62 us and 45 us, not cut.
-long long dx_rows(long long T) { return (T + 511) / 512 * 512; }
-int dx_splits(long long T, long long D, long long V, int num_sms) {
-    const long long pairs = num_sms / 2, tiles = dx_rows(T) / 512 * ((D + gm::BN - 1) / gm::BN);
-    const double product = 2.0 * T * V * D / 1.3e15, sums = 4.0 * dx_rows(T) * D / 6e12;
-    int best = 1;
-    double least = 0.0;
-    for (int s = 1; s <= 8; ++s) {
-        const long long n = tiles * s, rounds = (n + pairs - 1) / pairs;
-        const double cost = product * static_cast<double>(rounds * pairs) / static_cast<double>(n) + 2.0 * s * sums;
-        if (s == 1 || cost < least) {
-            least = cost;
-            best = s;
-        }
-    }
-    return best;
+// dX has few tiles (T / 512 x D / 256) and a long reduction over the words, so it
+// may be cut into parts, each with its own fp32 sums over the pieces, which
+// xent_dx_kernel adds in order.
+long long dx_rows(long long T) { return (T + 31) / 32 * 32; }
+int dx_splits(long long T, long long D, long long V) {
+    const bool tall = !g_parts(T) && T > 256;
+    const long long rows = tall ? 512 : 256, tiles = (T + rows - 1) / rows * ((D + gm::BN - 1) / gm::BN);
+    return gemm_splits(tiles, (V + gm::BK - 1) / gm::BK, 4.0 * dx_rows(T) * D, tall || g_parts(T) ? 0.8 : 0.55, 64);
 }
 
 template <class Epi, bool A_MN, bool B_MN>
@@ -377,8 +367,8 @@ size_t xent_workspace_bytes(long long T, long long V) {
     return round256(static_cast<size_t>(parts(V)) * T * sizeof(float2)) + round256(static_cast<size_t>(T) * sizeof(float));
 }
 
-size_t xent_backward_workspace_bytes(long long T, long long D, long long V, int need_dx, int num_sms) {
-    return 256 + (need_dx ? round256(static_cast<size_t>(dx_splits(T, D, V, num_sms)) * dx_rows(T) * D * sizeof(float)) : 0) +
+size_t xent_backward_workspace_bytes(long long T, long long D, long long V, int need_dx) {
+    return 256 + (need_dx ? round256(static_cast<size_t>(dx_splits(T, D, V)) * dx_rows(T) * D * sizeof(float)) : 0) +
            round256(static_cast<size_t>(T) * piece_words(T, V) * (g_parts(T) ? 4 : 2));
 }
 
@@ -395,8 +385,9 @@ cudaError_t launch_xent(const uint16_t* x, long long T, long long D, const uint1
     const GemmShape shape{static_cast<int>(T), static_cast<int>(V), static_cast<int>(D), 0, 8, 1, 0};
     // one segment holds the whole sum: tall tiles need none
     const bool tall = D <= kLogitSegment * gm::BK && gemm_tall(T, V, 1, num_sms);
-    if (cudaError_t e = tall ? launch_gemm_f16<LsePart, 1, 2, false, false, false, 0>(a, b, p, shape, status, st)
-                             : launch_gemm_f16<LsePart, 1, 1, false, false, false, kLogitSegment>(a, b, p, shape, status, st))
+    if (cudaError_t e = T <= 256 ? launch_gemm_f16<LsePart, 1, 1, false, false, false, kFewSegment>(a, b, p, shape, status, st)
+                        : tall ? launch_gemm_f16<LsePart, 1, 2, false, false, false, 0>(a, b, p, shape, status, st)
+                               : launch_gemm_f16<LsePart, 1, 1, false, false, false, kLogitSegment>(a, b, p, shape, status, st))
         return e;
     return pdl_launch(xent_merge_kernel, dim3(static_cast<unsigned>((T + 7) / 8)), dim3(256), 0, st,
                       static_cast<const float2*>(part), static_cast<const float*>(tlogit), target, ignore,
@@ -406,7 +397,7 @@ cudaError_t launch_xent(const uint16_t* x, long long T, long long D, const uint1
 cudaError_t launch_xent_backward(const float* dloss, const uint16_t* x, long long T, long long D, const uint16_t* w,
                                  long long V, const long long* target, long long ignore, const float* lse, uint16_t* dx,
                                  uint16_t* dw, void* ws, unsigned* status, int num_sms, cudaStream_t st) {
-    const int splits = dx_splits(T, D, V, num_sms);
+    const int splits = dx_splits(T, D, V);
     const long long rows = dx_rows(T);
     uint8_t* at = static_cast<uint8_t*>(ws);
     float* cmax = reinterpret_cast<float*>(at);
@@ -457,6 +448,7 @@ cudaError_t launch_xent_backward(const float* dloss, const uint16_t* x, long lon
             CUtensorMap gk, wn;
             SumF32::Params sp;
             sp.add = v0 > 0;
+            sp.rows = Ti;
             if (!gemm_operand(&gk, false, false, g, T, g_cols, pitch) || !gemm_operand(&wn, false, true, wp, n, D, D) ||
                 !gemm_result_f32(&sp.out, dx32, splits * rows, D))
                 return cudaErrorInvalidValue;

@@ -116,7 +116,9 @@ NMS = [(2, 4), (3, 4), (6, 8), (4, 8)]
 # decode sizes (T <= 16; K of every chunk width and a ragged one), tile sizes with ragged rows, tokens
 # and k, K that TMA cannot address (K % 64 != 0), odd F (rows that TMA cannot store)
 SHAPES = [(1, 16, 1), (1, 64, 8), (1, 256, 130), (2, 144, 37), (5, 896, 200), (9, 128, 33), (16, 2048, 77), (13, 48, 515),
-          (17, 64, 128), (33, 80, 97), (100, 128, 129), (256, 256, 256), (257, 192, 131), (300, 272, 260), (520, 896, 300)]
+          (17, 64, 128), (33, 80, 97), (100, 128, 129), (256, 256, 256), (257, 192, 131), (300, 272, 260), (520, 896, 300),
+          # both gradients' reductions in parts
+          (3001, 64, 100)]
 
 
 @pytest.mark.parametrize("T,K,F", SHAPES)
