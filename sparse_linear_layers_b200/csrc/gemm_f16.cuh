@@ -578,11 +578,13 @@ inline int gemm_splits(long long tiles, long long KB, double part_bytes, double 
     return best;
 }
 
-// Whether 512-row tiles move fewer bytes than 256-row ones (48 KB against 32 KB
-// per k-block and CTA) over M rows and still give every pair of SMs one.
-inline bool gemm_tall(long long M, long long N, int splits, int num_sms) {
-    const long long tall = (M + 511) / 512, flat = (M + 255) / 256, cols = (N + gm::BN - 1) / gm::BN;
-    return 48 * tall < 32 * flat && tall * cols * splits >= num_sms / 2;
+// Whether 512-row tiles finish first: their rounds at 0.8 us per k-block against
+// those of 256-row tiles at 0.55 us (gemm_splits).  8192 x 16384 x 896: 64 tall tiles
+// 173 us, 128 flat ones 203 us.
+inline bool gemm_tall(long long M, long long N, int splits) {
+    const long long cols = (N + gm::BN - 1) / gm::BN * splits;
+    const long long tall = ((M + 511) / 512 * cols + 73) / 74, flat = ((M + 255) / 256 * cols + 73) / 74;
+    return 0.8 * static_cast<double>(tall) < 0.55 * static_cast<double>(flat);
 }
 
 }  // namespace sbl

@@ -84,7 +84,7 @@ size_t xent_workspace_bytes(long long T, long long V);
 size_t xent_backward_workspace_bytes(long long T, long long D, long long V, int need_dx);
 cudaError_t launch_xent(const uint16_t* x, long long T, long long D, const uint16_t* w, long long V,
                         const long long* target, long long ignore, float* loss, float* lse, void* ws, unsigned* status,
-                        int num_sms, cudaStream_t st);
+                        cudaStream_t st);
 cudaError_t launch_xent_backward(const float* dloss, const uint16_t* x, long long T, long long D, const uint16_t* w,
                                  long long V, const long long* target, long long ignore, const float* lse, uint16_t* dx,
                                  uint16_t* dw, void* ws, unsigned* status, int num_sms, cudaStream_t st);
@@ -469,7 +469,7 @@ sbl_status sbl_linear_cross_entropy(const uint16_t* x_bf16, int64_t T, int64_t D
     DeviceInfo* d;
     if (sbl_status s = device_info(&d)) return s;
     return from_cuda(sbl::launch_xent(x_bf16, T, D, w_bf16, V, reinterpret_cast<const long long*>(target), ignore_index,
-                                      loss, lse, workspace, d->status, d->num_sms, static_cast<cudaStream_t>(stream)));
+                                      loss, lse, workspace, d->status, static_cast<cudaStream_t>(stream)));
 }
 
 size_t sbl_linear_cross_entropy_backward_workspace_bytes(int64_t T, int64_t D, int64_t V, int need_dx) {

@@ -47,9 +47,9 @@ namespace {
 // one piece, D = 2048 left lse 1.5e-6 off (the tensor cores' rounding towards
 // zero), three times what a sum rounded to nearest leaves.
 constexpr int kLogitSegment = 16;
-// Up to 256 tokens, whose time is W's way from memory, segments of 4: over few
+// Up to 256 tokens, whose time is W's way from memory, segments of 2: over few
 // losses, some of them small, the sum's error shows (a token: 1e-6 of its loss).
-constexpr int kFewSegment = 4;
+constexpr int kFewSegment = 2;
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -355,8 +355,8 @@ int dx_splits(long long T, long long D, long long V) {
 
 template <class Epi, bool A_MN, bool B_MN>
 cudaError_t launch_either(const CUtensorMap& a, const CUtensorMap& b, const typename Epi::Params& p, const GemmShape& shape,
-                          unsigned* status, int num_sms, cudaStream_t st) {
-    return gemm_tall(shape.M, shape.N, shape.splits, num_sms)
+                          unsigned* status, cudaStream_t st) {
+    return gemm_tall(shape.M, shape.N, shape.splits)
                ? launch_gemm_f16<Epi, 1, 2, A_MN, B_MN, false, 0>(a, b, p, shape, status, st)
                : launch_gemm_f16<Epi, 1, 1, A_MN, B_MN, false, 0>(a, b, p, shape, status, st);
 }
@@ -374,7 +374,7 @@ size_t xent_backward_workspace_bytes(long long T, long long D, long long V, int 
 
 cudaError_t launch_xent(const uint16_t* x, long long T, long long D, const uint16_t* w, long long V,
                         const long long* target, long long ignore, float* loss, float* lse, void* ws, unsigned* status,
-                        int num_sms, cudaStream_t st) {
+                        cudaStream_t st) {
     float2* part = static_cast<float2*>(ws);
     float* tlogit = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) +
                                              round256(static_cast<size_t>(parts(V)) * T * sizeof(float2)));
@@ -384,7 +384,7 @@ cudaError_t launch_xent(const uint16_t* x, long long T, long long D, const uint1
     const LsePart::Params p{part, tlogit, target, static_cast<int>(T), static_cast<int>(V), parts(V)};
     const GemmShape shape{static_cast<int>(T), static_cast<int>(V), static_cast<int>(D), 0, 8, 1, 0};
     // one segment holds the whole sum: tall tiles need none
-    const bool tall = D <= kLogitSegment * gm::BK && gemm_tall(T, V, 1, num_sms);
+    const bool tall = D <= kLogitSegment * gm::BK && gemm_tall(T, V, 1);
     if (cudaError_t e = T <= 256 ? launch_gemm_f16<LsePart, 1, 1, false, false, false, kFewSegment>(a, b, p, shape, status, st)
                         : tall ? launch_gemm_f16<LsePart, 1, 2, false, false, false, 0>(a, b, p, shape, status, st)
                                : launch_gemm_f16<LsePart, 1, 1, false, false, false, kLogitSegment>(a, b, p, shape, status, st))
@@ -438,7 +438,7 @@ cudaError_t launch_xent_backward(const float* dloss, const uint16_t* x, long lon
             gp.n = ni;
             const GemmShape shape{Ti, ni, Di, 0, 8, 1, 0};
             if constexpr (PARTS) return launch_gemm_f16<GradTile<true>, 1, 1, false, false, false, 0>(xk, wk, gp, shape, status, st);
-            else return launch_either<GradTile<false>, false, false>(xk, wk, gp, shape, status, num_sms, st);
+            else return launch_either<GradTile<false>, false, false>(xk, wk, gp, shape, status, st);
         };
         e = parts ? logits(std::true_type{}) : logits(std::false_type{});
         if (e != cudaSuccess) return e;
@@ -454,7 +454,7 @@ cudaError_t launch_xent_backward(const float* dloss, const uint16_t* x, long lon
                 return cudaErrorInvalidValue;
             const GemmShape shape{Ti, Di, ni, low, d_panel, splits, static_cast<int>(rows)};
             e = parts ? launch_gemm_f16<SumF32, 2, 1, false, true, false, 0>(gk, wn, sp, shape, status, st)
-                      : launch_either<SumF32, false, true>(gk, wn, sp, shape, status, num_sms, st);
+                      : launch_either<SumF32, false, true>(gk, wn, sp, shape, status, st);
             if (e != cudaSuccess) return e;
         }
         if (dw) {
@@ -466,7 +466,7 @@ cudaError_t launch_xent_backward(const float* dloss, const uint16_t* x, long lon
                 return cudaErrorInvalidValue;
             const GemmShape shape{ni, Di, Ti, low, d_panel, 1, 0};
             e = parts ? launch_gemm_f16<ScaledBf16, 2, 1, true, true, false, 0>(gm_, xn, bp, shape, status, st)
-                      : launch_either<ScaledBf16, true, true>(gm_, xn, bp, shape, status, num_sms, st);
+                      : launch_either<ScaledBf16, true, true>(gm_, xn, bp, shape, status, st);
         }
     }
     if (e == cudaSuccess && dx) {
