@@ -99,7 +99,7 @@ def _ptr(t: Optional[torch.Tensor]):
 def _scratch(nbytes: int, workspace: Optional[torch.Tensor], device) -> torch.Tensor:
     """``workspace``, checked, or a new one of ``nbytes``."""
     if workspace is None:
-        return torch.empty((max(1, nbytes),), dtype=torch.uint8, device=device)
+        return torch.empty(max(1, nbytes), dtype=torch.uint8, device=device)
     _need_workspace(workspace, device)
     return workspace
 
@@ -239,8 +239,8 @@ def sbl_norm(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor]
             y = torch.empty_like(x)
         else:
             _need_cuda(y, "y", x.dtype, (T, K), x.device)
-        mean = weight.new_empty((T,)) if with_stats and kind == "layer" else None
-        rstd = weight.new_empty((T,)) if with_stats else None
+        rstd = torch.empty(T, dtype=torch.float32, device=x.device) if with_stats else None
+        mean = torch.empty_like(rstd) if with_stats and kind == "layer" else None
         check(lib.sbl_norm(x.data_ptr(), _DTYPES[x.dtype], T, K, _NORM_KINDS[kind], weight.data_ptr(), _ptr(bias),
                            float(eps), y.data_ptr(), _ptr(mean), _ptr(rstd), st), "sbl_norm")
     return (y, mean, rstd) if with_stats else y
@@ -589,7 +589,7 @@ def sbl_ffn_gated(x: torch.Tensor, gate: PreparedWeights, up: PreparedWeights, a
         if (out_dtype if h is None else h.dtype) not in _DTYPES:
             raise ValueError("h must be float32 or bfloat16")
         if h is None:
-            h = x.new_empty((T, F), dtype=out_dtype)
+            h = torch.empty(T, F, dtype=out_dtype, device=x.device)
         else:
             _need_cuda(h, "h", h.dtype, (T, F), x.device)
         need = sbl_ffn_gated_workspace_bytes(T, K, F)
@@ -618,9 +618,8 @@ def sbl_ffn_gated_backward(dh: torch.Tensor, x: torch.Tensor, gate: PreparedWeig
     if not (need_dx or need_dgate or need_dup):
         raise ValueError("ask for dX, dW_gate or dW_up")
     with _LaunchOn(dev, stream) as st:
-        dx = torch.empty((T, K), dtype=torch.float32, device=dev) if need_dx else None
-        dg = torch.empty((F, K), dtype=torch.float32, device=dev) if need_dgate else None
-        du = torch.empty((F, K), dtype=torch.float32, device=dev) if need_dup else None
+        new = lambda rows, wanted: torch.empty(rows, K, dtype=torch.float32, device=dev) if wanted else None
+        dx, dg, du = new(T, need_dx), new(F, need_dgate), new(F, need_dup)
         ws = _scratch(sbl_ffn_gated_backward_workspace_bytes(T, K, F, need_dx, need_dgate or need_dup), workspace, dev)
         check(lib.sbl_ffn_gated_backward(dh.data_ptr(), x.data_ptr(), T, K, gate.packed.data_ptr(),
                                          gate.row_scale.data_ptr(), up.packed.data_ptr(), up.row_scale.data_ptr(), F,
@@ -651,7 +650,7 @@ def sbl_linear_cross_entropy(x: torch.Tensor, W: torch.Tensor, target: torch.Ten
     [T]; tokens whose target is ``ignore_index`` have loss 0."""
     T, D, V = _need_xent(x, W, target)
     with _LaunchOn(x.device, stream) as st:
-        loss = x.new_empty((T,), dtype=torch.float32)
+        loss = torch.empty(T, dtype=torch.float32, device=x.device)
         lse = torch.empty_like(loss)
         ws = _scratch(sbl_linear_cross_entropy_workspace_bytes(T, V), workspace, x.device)
         check(lib.sbl_linear_cross_entropy(x.data_ptr(), T, D, W.data_ptr(), V, target.data_ptr(), ignore_index,

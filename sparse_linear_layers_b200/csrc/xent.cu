@@ -97,13 +97,13 @@ struct LsePart {
 #pragma unroll
         for (int i = 3; i < 31; i += 2) m4[(i >> 1) & 3] = max3(m4[(i >> 1) & 3], v[i], v[i + 1]);
         const float m = fmaxf(max3(m4[0], m4[1], m4[2]), fmaxf(m4[3], v[31]));
-        // exp(z - m) = 2^(z log2 e - m log2 e): the fused product is exact, and the
-        // second's rounding (2^-24 |m log2 e|) moves lse by less than its own last bit
-        const float2 l2 = both(kLog2e), less = both(-m * kLog2e);
+        // (z - m) log2 e, not z log2 e - m log2 e in one step: the maximum's term has to
+        // be exactly 1, or a likely word's small loss is the rounding of m log2 e
+        const float2 l2 = both(kLog2e), less = both(-m);
         float2 s2[2] = {make_float2(mx == -INFINITY ? 0.f : sum * exp2_fast((mx - m) * kLog2e), 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            const float2 e = fma2(make_float2(v[2 * i], v[2 * i + 1]), l2, less);
+            const float2 e = mul2(add2(make_float2(v[2 * i], v[2 * i + 1]), less), l2);
             s2[i & 1] = add2(s2[i & 1], make_float2(exp2_fast(e.x), exp2_fast(e.y)));
         }
         s2[0] = add2(s2[0], s2[1]);
@@ -266,19 +266,21 @@ __global__ void __launch_bounds__(256)
     for (int off = 16; off > 0; off >>= 1)
         join(__shfl_xor_sync(0xFFFFFFFFu, m, off), __shfl_xor_sync(0xFFFFFFFFu, sum, off));
     if (lane != 0) return;
-    const float lse = m + logf(sum);
+    const float log_sum = logf(sum);
     const long long y = target[t];
     float l = 0.f;
     if (y != ignore) {
         if (y >= 0 && y < V) {
-            l = lse - tlogit[t];
+            // not lse - z: for a likely word both are large and the loss is what their
+            // rounding would leave
+            l = (m - tlogit[t]) + log_sum;
         } else {
             raise_status(status, kStatusInvalid);
             l = NAN;
         }
     }
     loss[t] = l;
-    lse_out[t] = lse;
+    lse_out[t] = m + log_sum;
 }
 
 // c = max |dloss[t]| over the tokens that count (NaN if one is NaN).

@@ -184,6 +184,26 @@ def test_large_logits_do_not_overflow(sbl):
     _check("loss", got_loss, loss, 2 * e + L + 2 * U * loss.abs())
 
 
+def test_likely_words(sbl):
+    """Targets of probability close to 1: the loss is far smaller than lse and the
+    target's logit.  dloss/dz = p - onehot sums to 2 (1 - p_target) in magnitude, so
+    the logits' error e moves the loss by 2 e (1 - p); the exponentials' 2^-21
+    acts on the other words only, and at most 100 additions round at a sum near 1."""
+    g = torch.Generator().manual_seed(4)
+    T, D, V = 300, 256, 3000
+    w = torch.randn(V, D, generator=g) / 16
+    t = torch.randint(0, V, (T,), generator=g)
+    x = (torch.randn(T, D, generator=g) + torch.linspace(8, 30, T)[:, None] * w[t]).bfloat16()
+    w = w.bfloat16()
+    z, lse, loss, p, *_ = _refs(x, w, t, torch.ones(T))
+    assert loss.min() < 1e-6 and loss.max() > 1e-2
+    e, _, _ = _bounds(x, w, z, lse, loss)
+    rest = 1 - torch.exp(-loss)
+    for n in (T, 200):   # more and fewer than 256 tokens
+        got, _ = sbl.sbl_linear_cross_entropy(x[:n].cuda().contiguous(), w.cuda(), t[:n].cuda())
+        _check("loss", got, loss[:n], ((2 * e + 2.0 ** -21) * rest + 100 * U)[:n])
+
+
 def test_empty_all_ignored_and_bad_targets(sbl):
     w = torch.randn(100, 32, device="cuda").bfloat16()
     x = torch.empty((0, 32), dtype=torch.bfloat16, device="cuda")
