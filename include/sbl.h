@@ -386,7 +386,8 @@ sbl_status sbl_ffn_gated_backward(const float* dh, const uint16_t* x_bf16, int64
  *   workspace sbl_linear_cross_entropy_workspace_bytes(T, V) bytes, 256-byte
  *             aligned (8 bytes per token and 128 words).
  * D % 16 == 0; T, D, V up to 2^24 and T * V below 2^46, else SBL_ERR_UNSUPPORTED.  x and W finite
- * (also in ignored rows).  Asynchronous on `stream`.
+ * (NaN or Inf in the row of a token reaches that token's loss and lse alone; an
+ * ignored token's loss stays 0).  Asynchronous on `stream`.
  */
 size_t sbl_linear_cross_entropy_workspace_bytes(int64_t T, int64_t V);
 sbl_status sbl_linear_cross_entropy(const uint16_t* x_bf16, int64_t T, int64_t D, const uint16_t* w_bf16, int64_t V,
@@ -408,7 +409,8 @@ sbl_status sbl_linear_cross_entropy(const uint16_t* x_bf16, int64_t T, int64_t D
  * rounded to bf16 for the tensor cores (relative to max |dloss|, so a uniform
  * dloss is exact); sums are fp32, and dx and dw are rounded once.  The same
  * inputs give the same bits.  Limits and errors as the forward; a target
- * outside [0, V) that is not ignored has no gradient.
+ * outside [0, V) that is not ignored has no gradient.  dx of an ignored token is
+ * 0 whatever its x holds; dw, a product with x, needs ignored rows finite too.
  */
 size_t sbl_linear_cross_entropy_backward_workspace_bytes(int64_t T, int64_t D, int64_t V, int need_dx);
 sbl_status sbl_linear_cross_entropy_backward(const float* dloss, const uint16_t* x_bf16, int64_t T, int64_t D,

@@ -133,7 +133,8 @@ struct GradTile {
     const Params& p;
     float less, d;   // -lse log2 e; dloss / c
     long long tcol;
-    __device__ __forceinline__ explicit GradTile(const Params& q) : p(q), less(0.f), d(0.f), tcol(-1) {}
+    bool some_zero;  // a row of this warp has d = 0
+    __device__ __forceinline__ explicit GradTile(const Params& q) : p(q), less(0.f), d(0.f), tcol(-1), some_zero(false) {}
     __device__ __forceinline__ void begin(const GemmTile& t) {
         d = 0.f;
         tcol = -1;
@@ -144,7 +145,7 @@ struct GradTile {
             if (y != p.ignore && y >= 0 && y < p.V && c != 0.f) d = __fdiv_rn(__ldg(p.dloss + t.row), c);
             tcol = y - p.v0 - t.col0;
         }
-        if (d == 0.f) less = -INFINITY;  // exp becomes 0: the row writes zeros
+        some_zero = __any_sync(0xFFFFFFFFu, d == 0.f);
     }
     __device__ __forceinline__ void slice(GemmTile& t, int k, float (&v)[32]) {
         const float2 l2 = both(kLog2e), ls = both(less);
@@ -165,6 +166,11 @@ struct GradTile {
             const float2 g = mul2(make_float2(v[i], v[i + 1]), both(d));
             v[i] = g.x;
             v[i + 1] = g.y;
+        }
+        if (some_zero) {
+            // not by 0 * exp: an ignored token's logits may be NaN or overflow
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = d == 0.f ? 0.f : v[i];
         }
         if constexpr (PARTS) {
             // the products read whole tiles of both parts: zeros past the last word

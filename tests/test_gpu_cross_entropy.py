@@ -232,6 +232,26 @@ def test_empty_all_ignored_and_bad_targets(sbl):
         assert not dx[4].any() and torch.isfinite(dw).all()
 
 
+@pytest.mark.parametrize("T", [9, 300])
+def test_nonfinite_ignored_rows(sbl, T):
+    """NaN, Inf and overflowing logits in the rows of ignored tokens (padding that
+    nothing ever wrote) change nothing of the other tokens, and their own loss
+    and dx are 0."""
+    x, w, t = [v.cuda() for v in _inputs(T, 64, 700, seed=21)]
+    t[torch.tensor([1, 4, 6])] = -100
+    d = torch.full((T,), 0.5, device="cuda")
+    run = lambda xv: (lambda loss, lse: (loss, sbl.sbl_linear_cross_entropy_backward(d, xv, w, t, lse, need_dw=False)[0]))(
+        *sbl.sbl_linear_cross_entropy(xv, w, t))
+    loss, dx = run(x)
+    bad = x.clone()
+    bad[1] = float("nan")
+    bad[4, 3] = float("inf")
+    bad[6] = 3e38
+    got_loss, got_dx = run(bad)
+    assert torch.equal(got_loss, loss) and torch.equal(got_dx, dx)
+    assert not got_loss[[1, 4, 6]].any() and not got_dx[[1, 4, 6]].any()
+
+
 def test_other_stream_and_graph(sbl):
     c = lambda vs: [v.cuda() for v in vs]
     x, w, t = c(_inputs(300, 96, 3000, seed=11))
