@@ -24,12 +24,19 @@ Argument marshalling only: no arithmetic of these layers runs in PyTorch.
 """
 from __future__ import annotations
 
+import contextlib
 import math
 
 import torch
 from torch.autograd.function import once_differentiable
 
 from . import _lib, api
+
+
+def _on_device_of(x: torch.Tensor):
+    # The weight preparation, the linear layers and the status word belong to
+    # the current device, which need not be x's.
+    return torch.cuda.device(x.device) if x.is_cuda else contextlib.nullcontext()
 
 
 def _stop_on_nonfinite(where: str) -> None:
@@ -141,7 +148,7 @@ class SparseBitNormFunction(torch.autograd.Function):
 class SparseBitNorm(torch.nn.Module):
     """RMS norm (``kind="rms"``, the guide module's, with torch's epsilon) or layer
     norm (``"layer"``) over the last dimension: fp32 weight and optional bias,
-    fp32 or bf16 inputs (others are cast to fp32), output in the input's type."""
+    output in the input's type (types other than fp32 and bf16 go through fp32)."""
 
     def __init__(self, features: int, kind: str = "rms", bias: bool = False, eps: float = api.RMSNORM_EPS_F32,
                  device=None):
@@ -153,7 +160,8 @@ class SparseBitNorm(torch.nn.Module):
     def forward(self, x: torch.Tensor) -> torch.Tensor:
         x2 = x.reshape(-1, self.features)
         x2 = (x2 if x2.dtype in (torch.float32, torch.bfloat16) else x2.float()).contiguous()
-        return SparseBitNormFunction.apply(x2, self.weight, self.bias, self.kind, self.eps).reshape(x.shape)
+        y = SparseBitNormFunction.apply(x2, self.weight, self.bias, self.kind, self.eps)
+        return y.to(x.dtype).reshape(x.shape)
 
     def extra_repr(self) -> str:
         return f"{self.features}, kind={self.kind}, bias={self.bias is not None}, eps={self.eps}"
@@ -215,9 +223,10 @@ class SparseBitFeedForward(torch.nn.Module):
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
         x2 = x.reshape(-1, self.in_features).to(torch.bfloat16).contiguous()
-        h = SparseBitGatedFunction.apply(x2, self.gate, self.up, self.n, self.m, self.act, self.dw_ternary,
-                                         self.check_finite)
-        return self.down(h).reshape(x.shape)
+        with _on_device_of(x):
+            h = SparseBitGatedFunction.apply(x2, self.gate, self.up, self.n, self.m, self.act, self.dw_ternary,
+                                             self.check_finite)
+            return self.down(h).reshape(x.shape)
 
     def extra_repr(self) -> str:
         return (f"in_features={self.in_features}, hidden_features={self.hidden_features}, {self.n}:{self.m}, "

@@ -150,6 +150,18 @@ def test_frozen_parts_and_reductions(sbl):
         sbl.SparseBitFeedForward(64, 264)   # the down projection's rows are not whole blocks
 
 
+def test_norm_of_other_types(sbl):
+    """fp16 goes through fp32 and back: half a step of fp16 (2^-11) on top of the
+    fp32 result, which is far below it."""
+    norm = sbl.SparseBitNorm(64, kind="layer", bias=True, device="cuda")
+    x = torch.randn(5, 3, 64, device="cuda").half().requires_grad_()
+    y = norm(x)
+    y.sum().backward()
+    assert y.dtype == x.grad.dtype == torch.float16 and y.shape == x.shape
+    want = torch.nn.functional.layer_norm(x.detach().double(), (64,), eps=norm.eps)
+    assert ((y.double() - want).abs() <= 2.0 ** -11 * want.abs() + 2.0 ** -18).all()
+
+
 def test_feed_forward_stops_on_nonfinite_input(sbl):
     ffn = sbl.SparseBitFeedForward(64, 96, device="cuda")
     x = torch.randn(30, 64, device="cuda")

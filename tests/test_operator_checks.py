@@ -187,3 +187,29 @@ def test_ffn_gated_tensor_checks(rec):
     for f in bad:
         with pytest.raises(ValueError):
             f()
+
+
+def test_feed_forward_runs_on_the_device_of_its_input(monkeypatch):
+    """The module's calls are made with the input's device current."""
+    import contextlib
+
+    from sparse_linear_layers_b200 import train
+
+    entered = []
+
+    @contextlib.contextmanager
+    def device(d):
+        entered.append(d)
+        yield
+
+    class OnGpu:
+        is_cuda, device = True, torch.device("cuda", 1)
+
+    monkeypatch.setattr(torch.cuda, "device", device)
+    with train._on_device_of(OnGpu()):
+        assert entered == [torch.device("cuda", 1)]
+    with train._on_device_of(torch.zeros(1)):
+        assert len(entered) == 1
+    ffn = train.SparseBitFeedForward(64, 96)
+    with pytest.raises(ValueError):
+        ffn(torch.zeros(2, 64))     # not on a GPU
