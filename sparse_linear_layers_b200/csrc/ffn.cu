@@ -824,22 +824,23 @@ struct FfnDx {
         CUtensorMap out;
         const unsigned* row_max;
         const float* s_tok;
-        int T;
+        int T, row_mask;  // 127 when rows 128 .. 255 are the low parts' sums of the same tokens, else -1
     };
     static __device__ __forceinline__ void prefetch(const Params& p) { prefetch_tmap(&p.out); }
     const Params& p;
     float e, s;
     __device__ __forceinline__ explicit FfnDx(const Params& r) : p(r), e(0.f), s(0.f) {}
     __device__ __forceinline__ void begin(const GemmTile& t) {
-        if (t.row < p.T) {
-            e = pow2f(row_exponent(__ldg(p.row_max + t.row)));
-            s = __ldg(p.s_tok + t.row);
+        const int token = t.row & p.row_mask;
+        if (token < p.T) {
+            e = pow2f(row_exponent(__ldg(p.row_max + token)));
+            s = __ldg(p.s_tok + token);
         }
     }
     __device__ __forceinline__ void slice(GemmTile& t, int k, float (&v)[32]) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = (v[i] * e) * s;
-        if (t.warp_row < p.T) put_f32(t, k, v, &p.out, 0, false);  // later rows are the next part's
+        if ((t.warp_row & p.row_mask) < p.T) put_f32(t, k, v, &p.out, 0, false);  // later rows are the next part's
     }
     __device__ __forceinline__ void end(const GemmTile&) {}
 };
@@ -913,8 +914,12 @@ FfnSpace ffn_space(long long T, long long K, long long F) {
 }
 
 // Parts of the two gradients' reductions (over 2 Fp hidden units, over T).
+// Up to 128 tokens v's two parts lie in the two CTAs' rows of one A (GemmShape::stack)
+// instead of in two A of 256 rows: half the MMAs.
+bool dx_stacks(long long T) { return T <= gm::BM; }
 int dx_splits(long long T, long long K, long long Fp) {
-    return gemm_splits((T + 255) / 256 * ((K + gm::BN - 1) / gm::BN), 2 * Fp / gm::BK, 4.0 * T * K, 0.8, 32);
+    return gemm_splits((T + 255) / 256 * ((K + gm::BN - 1) / gm::BN), 2 * Fp / gm::BK, (dx_stacks(T) ? 8.0 : 4.0) * T * K,
+                       dx_stacks(T) ? 0.45 : 0.8, 32);
 }
 int dw_splits(long long T, long long K, long long Fp) {
     return gemm_splits((2 * Fp + 255) / 256 * ((K + gm::BN - 1) / gm::BN), (T + gm::BK - 1) / gm::BK, 8.0 * Fp * K, 0.8, 32);
@@ -938,10 +943,10 @@ FfnBwdSpace ffn_bwd_space(long long T, long long K, long long F, int need_dx, in
     s.xs = s.codes + (need_dx ? round256(static_cast<size_t>(2) * s.Fp * K * 2) : 0);
     s.sums = s.xs + (need_dw ? round256(static_cast<size_t>(T) * K * 2) : 0);
     // the parts of a split reduction; dX's have been added before dW's are written
-    s.dx_rows = (T + 31) / 32 * 32;
+    s.dx_rows = dx_stacks(T) ? 2 * gm::BM : (T + 31) / 32 * 32;
     s.dx_splits = need_dx ? dx_splits(T, K, s.Fp) : 1;
     s.dw_splits = need_dw ? dw_splits(T, K, s.Fp) : 1;
-    const size_t a = s.dx_splits > 1 ? static_cast<size_t>(s.dx_splits) * s.dx_rows * K * 4 : 0;
+    const size_t a = need_dx && (s.dx_splits > 1 || dx_stacks(T)) ? static_cast<size_t>(s.dx_splits) * s.dx_rows * K * 4 : 0;
     const size_t b = s.dw_splits > 1 ? static_cast<size_t>(s.dw_splits) * 2 * s.Fp * K * 4 : 0;
     s.end = s.sums + round256(a > b ? a : b);
     return s;
@@ -1172,18 +1177,22 @@ cudaError_t launch_ffn_backward(const float* dh, const uint16_t* x, long long T,
     if (dx) {
         CUtensorMap a, b;
         FfnDx::Params p;
-        const int splits = sp.dx_splits;
-        if (!gemm_operand(&a, true, false, parts, T, 4 * sp.Fp, 4 * sp.Fp) ||
+        const int splits = sp.dx_splits, a_box = gemm_a_box(T);
+        const bool stack = dx_stacks(T);
+        if (!gemm_operand(&a, true, false, parts, T, 4 * sp.Fp, 4 * sp.Fp, a_box) ||
             !gemm_operand(&b, true, true, codes, 2 * sp.Fp, K, K) ||
-            !gemm_result_f32(&p.out, splits > 1 ? sums : dx, splits > 1 ? splits * sp.dx_rows : T, K))
+            !gemm_result_f32(&p.out, splits > 1 || stack ? sums : dx, splits > 1 || stack ? splits * sp.dx_rows : T, K))
             return cudaErrorInvalidValue;
         p.row_max = row_max;
         p.s_tok = s_tok;
         p.T = Ti;
-        const GemmShape shape{Ti, Ki, 2 * Fp, 2 * Fp, k_panel, splits, static_cast<int>(sp.dx_rows)};
-        if (cudaError_t e = launch_gemm_f16<FfnDx, 2, 1, false, true, true, 4>(a, b, p, shape, status, st)) return e;
-        if (splits > 1)
-            if (cudaError_t e = join(splits, sp.dx_rows, 0, T, dx)) return e;
+        p.row_mask = stack ? gm::BM - 1 : -1;
+        const GemmShape shape{Ti, Ki, 2 * Fp, 2 * Fp, k_panel, splits, static_cast<int>(sp.dx_rows), a_box, stack ? 2 * Fp : 0};
+        if (cudaError_t e = stack ? launch_gemm_f16<FfnDx, 1, 1, false, true, true, 4>(a, b, p, shape, status, st)
+                                  : launch_gemm_f16<FfnDx, 2, 1, false, true, true, 4>(a, b, p, shape, status, st))
+            return e;
+        if (splits > 1 || stack)
+            if (cudaError_t e = stack ? join(2 * splits, gm::BM, 0, T, dx) : join(splits, sp.dx_rows, 0, T, dx)) return e;
     }
     if (need_dw) {
         CUtensorMap a, b;
@@ -1204,7 +1213,7 @@ cudaError_t launch_ffn_backward(const float* dh, const uint16_t* x, long long T,
         p.want_g = dwg != nullptr;
         p.want_u = dwu != nullptr;
         p.ternary = ternary;
-        const GemmShape shape{2 * Fp, Ki, Ti, 2 * Fp, k_panel, splits, 2 * Fp};
+        const GemmShape shape{2 * Fp, Ki, Ti, 2 * Fp, k_panel, splits, 2 * Fp, gm::BM, 0};
         if (cudaError_t e = launch_gemm_f16<FfnDw, 2, 1, true, true, true, 4>(a, b, p, shape, status, st)) return e;
         if (splits > 1 && dwg)
             if (cudaError_t e = join(splits, 2 * sp.Fp, 0, F, dwg)) return e;

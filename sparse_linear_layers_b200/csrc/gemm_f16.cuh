@@ -83,6 +83,9 @@ struct GemmShape {
     int panel;      // consecutive tiles walk across `panel` column tiles, then down M
     int splits;     // parts of the reduction, each a GEMM of its own into rows
     int split_rows; // split_rows further down (whole staging boxes: a multiple of 32)
+    int a_box;      // rows of a box of K-major A (gemm_a_box)
+    int stack;      // 0, or: the odd CTA's A rows are the even one's again, `stack` columns further on
+                    // (K-major A of at most 128 rows); their sums are rows 128 .. 255 of the result
 };
 
 struct GemmTile {
@@ -378,23 +381,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gm::threads(MH), 1)
             for (int tile = pair; tile < tiles && ok; tile += npairs) {
                 int m0, n0, split;
                 tile_at(tile, m0, n0, split);
-                const int arow = m0 + static_cast<int>(rank) * gm::BM, brow = n0 + static_cast<int>(rank) * gm::BM;
+                const int arow = m0 + (shape.stack ? 0 : static_cast<int>(rank) * gm::BM);
+                const int acol = rank ? shape.stack : 0, brow = n0 + static_cast<int>(rank) * gm::BM;
+                // boxes of A without a row are left out: what the tile holds there
+                // ends in rows that no epilogue stores
+                int boxes = 0;
+#pragma unroll
+                for (int j = 0; j < AT; ++j) {
+                    const int r = m0 + (MH == 2 ? 2 * gm::BM * j : 0);
+                    boxes += (r < shape.M) + (r + (shape.stack ? 0 : gm::BM) < shape.M);
+                }
+                const uint32_t bytes = static_cast<uint32_t>(boxes * (A_MN ? gm::TILE : shape.a_box * 128) + 2 * gm::TILE);
                 for (int kb = 0; kb < KB; ++kb, ++it) {
                     const int s = it % STAGES;
                     if (!mbar_wait(&sm->empty[s], ((it / STAGES) & 1) ^ 1, abort_flag)) { give_up(); ok = false; break; }
                     // the even CTA expects the bytes of both CTAs
-                    if (leader) mbar_arrive_expect_tx(&sm->full[s], 2 * (AT + 1) * gm::TILE);
+                    if (leader) mbar_arrive_expect_tx(&sm->full[s], bytes);
                     const uint32_t full = map_to_cta(smem_u32(&sm->full[s]), 0);
                     const int k0 = (split * KB + kb) * gm::BK;
 #pragma unroll
                     for (int j = 0; j < AT; ++j) {
                         const uint32_t dst = smem_u32(sm->a[s][j]);
                         const int part = MH == 2 ? 0 : j * shape.a_part, r = arow + (MH == 2 ? 2 * gm::BM * j : 0);
+                        if (r >= shape.M) continue;
                         if (A_MN) {
                             tma_load_2d_pair(dst, &tmap_a, part + r, k0, full);
                             tma_load_2d_pair(dst + gm::TILE / 2, &tmap_a, part + r + 64, k0, full);
                         } else {
-                            tma_load_2d_pair(dst, &tmap_a, part + k0, r, full);
+                            tma_load_2d_pair(dst, &tmap_a, acol + part + k0, r, full);
                         }
                     }
                     const uint32_t dst = smem_u32(sm->b[s]);
@@ -514,13 +528,17 @@ inline bool gemm_result_bf16(CUtensorMap* map, void* base, long long rows, long 
 }
 
 // An operand of the GEMM: a 2-byte row-major matrix [rows, cols].  K-major
-// operands are read in boxes of 64 k x 128 rows, MN-major ones in boxes of
+// operands are read in boxes of 64 k x box_rows rows, MN-major ones in boxes of
 // 64 columns x 64 k.
 inline bool gemm_operand(CUtensorMap* map, bool fp16, bool mn_major, const void* base, long long rows, long long cols,
-                         long long pitch_elems) {
+                         long long pitch_elems, int box_rows = gm::BM) {
     return gemm_map(map, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, rows, cols,
-                    pitch_elems * 2, 64, mn_major ? 64 : gm::BM);
+                    pitch_elems * 2, 64, mn_major ? 64 : box_rows);
 }
+
+// Rows of a box of K-major A with M rows: whole swizzle atoms, no more than
+// there are rows (1 row x 1440 against 15710 columns: 21 us with boxes of 128, 19 so).
+inline int gemm_a_box(long long M) { return M < gm::BM ? static_cast<int>((M + 7) / 8 * 8) : gm::BM; }
 
 template <class Epi, int NA, int MH, bool A_MN, bool B_MN, bool FP16, int SEGMENT>
 cudaError_t launch_gemm_f16(const CUtensorMap& a, const CUtensorMap& b, const typename Epi::Params& p,
@@ -560,7 +578,8 @@ cudaError_t launch_gemm_f16(const CUtensorMap& a, const CUtensorMap& b, const ty
 // Parts that a reduction of KB k-blocks is best cut into, when each part's fp32
 // result (part_bytes) is written and read back: `tiles` tiles take rounds of 74
 // pairs of SMs, a k-block of a tile about us_per_block (what L2 feeds a pair:
-// 0.55 us for 256 rows and one A, 0.8 us for 512 rows or two A), the sum over
+// 0.55 us for 256 rows and one A, 0.45 if half of them are past the end, 0.8 for 512
+// rows or two A), the sum over
 // the parts 3 us and its bytes at 6 TB/s.  1 token, 2 tiles of 619 k-blocks: 37 parts
 // (one part took 200 us); 1001 tokens, 16 tiles of 88: 4 parts (59 us -> 25 us).
 inline int gemm_splits(long long tiles, long long KB, double part_bytes, double us_per_block, int most) {

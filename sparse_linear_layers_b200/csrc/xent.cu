@@ -205,14 +205,14 @@ struct GradTile {
 struct SumF32 {
     struct Params {
         CUtensorMap out;
-        int add, rows;
+        int add, rows, row_mask;  // row_mask: 127 when rows 128 .. 255 are the second part's sums, else -1
     };
     static __device__ __forceinline__ void prefetch(const Params& p) { prefetch_tmap(&p.out); }
     const Params& p;
     __device__ __forceinline__ explicit SumF32(const Params& q) : p(q) {}
     __device__ __forceinline__ void begin(const GemmTile&) {}
     __device__ __forceinline__ void slice(GemmTile& t, int k, float (&v)[32]) {
-        if (t.warp_row < p.rows) put_f32(t, k, v, &p.out, 0, p.add != 0);  // later rows are the next part's
+        if ((t.warp_row & p.row_mask) < p.rows) put_f32(t, k, v, &p.out, 0, p.add != 0);  // later rows are the next part's
     }
     __device__ __forceinline__ void end(const GemmTile&) {}
 };
@@ -236,16 +236,19 @@ struct ScaledBf16 {
     __device__ __forceinline__ void end(const GemmTile&) {}
 };
 
-// Joins the P parts of a row in one warp, in a fixed order.
+// Joins the P parts of a row, in a fixed order: WARPS warps per row.
+template <int WARPS>
 __global__ void __launch_bounds__(256)
     xent_merge_kernel(const float2* __restrict__ part, const float* __restrict__ tlogit,
                       const long long* __restrict__ target, long long ignore, int T, int V, int P,
                       float* __restrict__ loss, float* __restrict__ lse_out, unsigned* status) {
+    constexpr int STEP = 32 * WARPS;
+    __shared__ float2 joined[WARPS];
     asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int lane = threadIdx.x & 31;
-    const long long t = blockIdx.x * 8ll + (threadIdx.x >> 5);
-    if (t >= T) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long t = blockIdx.x * static_cast<long long>(8 / WARPS) + warp / WARPS;
+    if (t >= T) return;  // WARPS = 8: the whole block
     const float2* const row = part + static_cast<size_t>(t) * P;
     // every part has a column, so its sum has a term 1 (or is NaN); the empty
     // start of a lane past the last part has the sum 0
@@ -255,22 +258,29 @@ __global__ void __launch_bounds__(256)
         sum = (sum == 0.f ? 0.f : sum * exp2_fast((m - n) * kLog2e)) + (qs == 0.f ? 0.f : qs * exp2_fast((qm - n) * kLog2e));
         m = n;
     };
-    int p = lane;
-    for (; p + 96 < P; p += 128) {  // four loads in flight
-        const float2 a = __ldg(row + p), b = __ldg(row + p + 32), c = __ldg(row + p + 64), d = __ldg(row + p + 96);
+    int p = warp % WARPS * 32 + lane;
+    for (; p + 3 * STEP < P; p += 4 * STEP) {  // four loads in flight
+        const float2 a = __ldg(row + p), b = __ldg(row + p + STEP), c = __ldg(row + p + 2 * STEP), d = __ldg(row + p + 3 * STEP);
         const float n = fmaxf(fmaxf(m, fmaxf(a.x, b.x)), fmaxf(c.x, d.x));
         const float s0 = a.y * exp2_fast((a.x - n) * kLog2e) + b.y * exp2_fast((b.x - n) * kLog2e);
         const float s1 = c.y * exp2_fast((c.x - n) * kLog2e) + d.y * exp2_fast((d.x - n) * kLog2e);
         sum = (sum == 0.f ? 0.f : sum * exp2_fast((m - n) * kLog2e)) + (s0 + s1);
         m = n;
     }
-    for (; p < P; p += 32) {
+    for (; p < P; p += STEP) {
         const float2 q = __ldg(row + p);
         join(q.x, q.y);
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1)
         join(__shfl_xor_sync(0xFFFFFFFFu, m, off), __shfl_xor_sync(0xFFFFFFFFu, sum, off));
+    if constexpr (WARPS > 1) {
+        if (lane == 0) joined[warp] = make_float2(m, sum);
+        __syncthreads();
+        if (warp != 0) return;
+#pragma unroll
+        for (int w = 1; w < WARPS; ++w) join(joined[w].x, joined[w].y);
+    }
     if (lane != 0) return;
     const float log_sum = logf(sum);
     const long long y = target[t];
@@ -308,24 +318,43 @@ __global__ void __launch_bounds__(1024) xent_cmax_kernel(const float* __restrict
     }
 }
 
-// dX = c * (the parts' fp32 sums, added in order), in bf16; 8 elements per thread.
+// dX = c * (the parts' fp32 sums, added in a fixed order), in bf16; 8 elements per
+// thread and slice of the parts.  Eight slices for many parts, which come from few
+// rows: one thread adding 64 parts of them took 12 us.
+template <int SLICES>
 __global__ void __launch_bounds__(256) xent_dx_kernel(const float* __restrict__ sums, const float* __restrict__ cmax,
-                                                      long long n8, int splits, long long split8,
+                                                      long long n8, int parts, long long part8,
                                                       uint16_t* __restrict__ dx) {
+    constexpr int COLS = 256 / SLICES;
+    __shared__ float4 slice_sum[SLICES > 1 ? SLICES : 1][2][COLS];
     asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const float c = *cmax;
-    for (long long i = blockIdx.x * 256ll + threadIdx.x; i < n8; i += gridDim.x * 256ll) {
-        const float4* p = reinterpret_cast<const float4*>(sums) + 2 * i;
-        float4 a = p[0], b = p[1];
-        for (int s = 1; s < splits; ++s) {
-            p += 2 * split8;
-            const float4 u = p[0], v = p[1];
-            a.x += u.x; a.y += u.y; a.z += u.z; a.w += u.w;
-            b.x += v.x; b.y += v.y; b.z += v.z; b.w += v.w;
+    const int col = threadIdx.x % COLS, slice = threadIdx.x / COLS;
+    float4 a, b;
+    auto add = [&](const float4& u, const float4& v) {
+        a.x += u.x; a.y += u.y; a.z += u.z; a.w += u.w;
+        b.x += v.x; b.y += v.y; b.z += v.z; b.w += v.w;
+    };
+    for (long long base = static_cast<long long>(blockIdx.x) * COLS; base < n8; base += static_cast<long long>(gridDim.x) * COLS) {
+        const long long i = base + col;
+        const float4* const p = reinterpret_cast<const float4*>(sums) + 2 * i;
+        a = b = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i < n8)
+#pragma unroll 4
+            for (int s = slice; s < parts; s += SLICES) add(p[2 * s * part8], p[2 * s * part8 + 1]);
+        if constexpr (SLICES > 1) {
+            slice_sum[slice][0][col] = a;
+            slice_sum[slice][1][col] = b;
+            __syncthreads();
+            if (slice == 0)
+#pragma unroll
+                for (int s = 1; s < SLICES; ++s) add(slice_sum[s][0][col], slice_sum[s][1][col]);
+            __syncthreads();
         }
-        reinterpret_cast<uint4*>(dx)[i] = make_uint4(pack_bf16(a.x * c, a.y * c), pack_bf16(a.z * c, a.w * c),
-                                                     pack_bf16(b.x * c, b.y * c), pack_bf16(b.z * c, b.w * c));
+        if (slice == 0 && i < n8)
+            reinterpret_cast<uint4*>(dx)[i] = make_uint4(pack_bf16(a.x * c, a.y * c), pack_bf16(a.z * c, a.w * c),
+                                                         pack_bf16(b.x * c, b.y * c), pack_bf16(b.z * c, b.w * c));
     }
 }
 
@@ -354,11 +383,14 @@ bool g_parts(long long T) { return T <= kPartsTokens; }
 // dX has few tiles (T / 512 x D / 256) and a long reduction over the words, so it
 // may be cut into parts, each with its own fp32 sums over the pieces, which
 // xent_dx_kernel adds in order.
-long long dx_rows(long long T) { return (T + 31) / 32 * 32; }
+// With G in two parts they lie in the two CTAs' rows of one A (GemmShape::stack),
+// each with sums of its own, instead of in two A of 256 rows: half the MMAs.
+long long dx_rows(long long T) { return g_parts(T) ? 2 * gm::BM : (T + 31) / 32 * 32; }
 int dx_splits(long long T, long long D, long long V) {
-    const bool tall = !g_parts(T) && T > 256;
+    const bool tall = T > 256;
     const long long rows = tall ? 512 : 256, tiles = (T + rows - 1) / rows * ((D + gm::BN - 1) / gm::BN);
-    return gemm_splits(tiles, (V + gm::BK - 1) / gm::BK, 4.0 * dx_rows(T) * D, tall || g_parts(T) ? 0.8 : 0.55, 64);
+    return gemm_splits(tiles, (V + gm::BK - 1) / gm::BK, (g_parts(T) ? 8.0 : 4.0) * T * D,
+                       tall ? 0.8 : g_parts(T) ? 0.45 : 0.55, 64);
 }
 
 template <class Epi, bool A_MN, bool B_MN>
@@ -387,19 +419,23 @@ cudaError_t launch_xent(const uint16_t* x, long long T, long long D, const uint1
     float* tlogit = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) +
                                              round256(static_cast<size_t>(parts(V)) * T * sizeof(float2)));
     CUtensorMap a, b;
-    if (!gemm_operand(&a, false, false, x, T, D, D) || !gemm_operand(&b, false, false, w, V, D, D))
+    if (!gemm_operand(&a, false, false, x, T, D, D, gemm_a_box(T)) || !gemm_operand(&b, false, false, w, V, D, D))
         return cudaErrorInvalidValue;
     const LsePart::Params p{part, tlogit, target, static_cast<int>(T), static_cast<int>(V), parts(V)};
-    const GemmShape shape{static_cast<int>(T), static_cast<int>(V), static_cast<int>(D), 0, 8, 1, 0};
+    const GemmShape shape{static_cast<int>(T), static_cast<int>(V), static_cast<int>(D), 0, 8, 1, 0, gemm_a_box(T), 0};
     // one segment holds the whole sum: tall tiles need none
     const bool tall = D <= kLogitSegment * gm::BK && gemm_tall(T, V, 1);
     if (cudaError_t e = T <= 256 ? launch_gemm_f16<LsePart, 1, 1, false, false, false, kFewSegment>(a, b, p, shape, status, st)
                         : tall ? launch_gemm_f16<LsePart, 1, 2, false, false, false, 0>(a, b, p, shape, status, st)
                                : launch_gemm_f16<LsePart, 1, 1, false, false, false, kLogitSegment>(a, b, p, shape, status, st))
         return e;
-    return pdl_launch(xent_merge_kernel, dim3(static_cast<unsigned>((T + 7) / 8)), dim3(256), 0, st,
-                      static_cast<const float2*>(part), static_cast<const float*>(tlogit), target, ignore,
-                      static_cast<int>(T), static_cast<int>(V), parts(V), loss, lse, status);
+    // a block per row while that leaves SMs idle otherwise
+    auto merge = [&](auto kern, int rows_per_block) {
+        return pdl_launch(kern, dim3(static_cast<unsigned>((T + rows_per_block - 1) / rows_per_block)), dim3(256), 0, st,
+                          static_cast<const float2*>(part), static_cast<const float*>(tlogit), target, ignore,
+                          static_cast<int>(T), static_cast<int>(V), parts(V), loss, lse, status);
+    };
+    return T <= 1024 ? merge(xent_merge_kernel<8>, 1) : merge(xent_merge_kernel<1>, 8);
 }
 
 cudaError_t launch_xent_backward(const float* dloss, const uint16_t* x, long long T, long long D, const uint16_t* w,
@@ -427,7 +463,7 @@ cudaError_t launch_xent_backward(const float* dloss, const uint16_t* x, long lon
         const int ni = static_cast<int>(n);
         const uint16_t* wp = w + v0 * D;
         CUtensorMap xk, wk;
-        if (!gemm_operand(&xk, false, false, x, T, D, D) || !gemm_operand(&wk, false, false, wp, n, D, D))
+        if (!gemm_operand(&xk, false, false, x, T, D, D, gemm_a_box(T)) || !gemm_operand(&wk, false, false, wp, n, D, D))
             return cudaErrorInvalidValue;
         auto logits = [&](auto parts_tag) -> cudaError_t {
             constexpr bool PARTS = decltype(parts_tag)::value;
@@ -444,7 +480,7 @@ cudaError_t launch_xent_backward(const float* dloss, const uint16_t* x, long lon
             gp.T = Ti;
             gp.V = static_cast<int>(V);
             gp.n = ni;
-            const GemmShape shape{Ti, ni, Di, 0, 8, 1, 0};
+            const GemmShape shape{Ti, ni, Di, 0, 8, 1, 0, gemm_a_box(T), 0};
             if constexpr (PARTS) return launch_gemm_f16<GradTile<true>, 1, 1, false, false, false, 0>(xk, wk, gp, shape, status, st);
             else return launch_either<GradTile<false>, false, false>(xk, wk, gp, shape, status, st);
         };
@@ -457,11 +493,12 @@ cudaError_t launch_xent_backward(const float* dloss, const uint16_t* x, long lon
             SumF32::Params sp;
             sp.add = v0 > 0;
             sp.rows = Ti;
-            if (!gemm_operand(&gk, false, false, g, T, g_cols, pitch) || !gemm_operand(&wn, false, true, wp, n, D, D) ||
+            sp.row_mask = parts ? gm::BM - 1 : -1;
+            if (!gemm_operand(&gk, false, false, g, T, g_cols, pitch, gemm_a_box(T)) || !gemm_operand(&wn, false, true, wp, n, D, D) ||
                 !gemm_result_f32(&sp.out, dx32, splits * rows, D))
                 return cudaErrorInvalidValue;
-            const GemmShape shape{Ti, Di, ni, low, d_panel, splits, static_cast<int>(rows)};
-            e = parts ? launch_gemm_f16<SumF32, 2, 1, false, true, false, 0>(gk, wn, sp, shape, status, st)
+            const GemmShape shape{Ti, Di, ni, 0, d_panel, splits, static_cast<int>(rows), gemm_a_box(T), parts ? low : 0};
+            e = parts ? launch_gemm_f16<SumF32, 1, 1, false, true, false, 0>(gk, wn, sp, shape, status, st)
                       : launch_either<SumF32, false, true>(gk, wn, sp, shape, status, st);
             if (e != cudaSuccess) return e;
         }
@@ -472,15 +509,20 @@ cudaError_t launch_xent_backward(const float* dloss, const uint16_t* x, long lon
             if (!gemm_operand(&gm_, false, true, g, T, g_cols, pitch) || !gemm_operand(&xn, false, true, x, T, D, D) ||
                 !gemm_result_bf16(&bp.out, dw + v0 * D, n, D, D))
                 return cudaErrorInvalidValue;
-            const GemmShape shape{ni, Di, Ti, low, d_panel, 1, 0};
+            const GemmShape shape{ni, Di, Ti, low, d_panel, 1, 0, gm::BM, 0};
             e = parts ? launch_gemm_f16<ScaledBf16, 2, 1, true, true, false, 0>(gm_, xn, bp, shape, status, st)
                       : launch_either<ScaledBf16, true, true>(gm_, xn, bp, shape, status, st);
         }
     }
     if (e == cudaSuccess && dx) {
-        const long long n8 = T * D / 8, blocks = (n8 + 255) / 256, most = 8ll * num_sms;
-        e = pdl_launch(xent_dx_kernel, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), dim3(256), 0, st,
-                       static_cast<const float*>(dx32), static_cast<const float*>(cmax), n8, splits, rows * D / 8, dx);
+        const int sums = parts ? 2 * splits : splits;
+        const long long n8 = T * D / 8, part8 = (parts ? gm::BM : rows) * D / 8, most = 8ll * num_sms;
+        auto sum_up = [&](auto kern, int cols) {
+            const long long blocks = (n8 + cols - 1) / cols;
+            return pdl_launch(kern, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), dim3(256), 0, st,
+                              static_cast<const float*>(dx32), static_cast<const float*>(cmax), n8, sums, part8, dx);
+        };
+        e = sums > 8 ? sum_up(xent_dx_kernel<8>, 32) : sum_up(xent_dx_kernel<1>, 256);
     }
     return e;
 }
