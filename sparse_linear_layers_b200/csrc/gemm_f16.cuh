@@ -16,11 +16,13 @@
 // MH = 2: tiles of 512 x 256, both buffers one tile's (its upper and lower 256
 // rows), so B is loaded once for twice the rows.  What feeds the MMAs bounds
 // this GEMM: L2 delivers about 9 TB/s to the SMs whatever the kernel (measured on
-// four of them), 7.8 KB per MFLOP of a 256 x 256 tile and 5.9 KB of a 512 x 256
+// four of them), 60 bytes/ns to one SM, also when 15 pairs run alone; 7.8 KB per MFLOP of a 256 x 256 tile and 5.9 KB of a 512 x 256
 // one.  The MMAs of the next tile wait until the epilogue has read a half, while
 // the loads run on for four stages; sixteen epilogue warps read both halves at
 // once to keep that wait short.  (Letting the upper half's MMAs run ahead
 // through those stages made the whole 3% slower: their stages come back later.)
+//
+// BN_ = 64 or 128: narrow tiles for a B of few rows (K-major, one A), eight stages.
 //
 // SEGMENT > 0: the tensor cores round every fp32 accumulation towards zero, an
 // error that grows with the number of MMAs summed into one accumulator (a
@@ -45,34 +47,36 @@ namespace sbl {
 
 namespace gm {
 constexpr int BM = 128;             // rows per CTA (pair: 256)
-constexpr int BN = 256;             // columns per pair tile
+constexpr int BN = 256;             // columns per pair tile, unless the kernel's BN_ says fewer
 constexpr int BK = 64;              // reduction elements per stage (128 bytes)
 constexpr int TILE = BM * BK * 2;   // one operand tile of one CTA: 16 KB
 constexpr int EPI_WARPS = 8;        // per accumulator half of a tall tile
 constexpr int threads(int mh) { return (EPI_WARPS * mh + 2) * 32; }
 constexpr int BOX = 32 * 64;        // a staging box: 32 rows x 64 bytes; 2 / MH per epilogue warp
 constexpr int BOXES = 16;
-constexpr int stages(int tiles) { return tiles == 1 ? 6 : 4; }  // by A tiles of a stage
+constexpr int b_tile(int bn) { return bn / 2 * BK * 2; }  // B tile of one CTA
+constexpr int stages(int tiles, int bn = BN) { return bn < BN ? 8 : tiles == 1 ? 6 : 4; }  // by A tiles of a stage
 }  // namespace gm
 
-template <int AT>
+template <int AT, int BN_ = gm::BN>
 struct GemmSmem {
-    uint8_t a[gm::stages(AT)][AT][gm::TILE];  // 1024-byte aligned tiles
-    uint8_t b[gm::stages(AT)][gm::TILE];
+    uint8_t a[gm::stages(AT, BN_)][AT][gm::TILE];  // 1024-byte aligned tiles
+    uint8_t b[gm::stages(AT, BN_)][gm::b_tile(BN_)];
     uint8_t box[gm::BOXES][gm::BOX];
-    uint64_t full[gm::stages(AT)];            // used in the even CTA
-    uint64_t empty[gm::stages(AT)];
+    uint64_t full[gm::stages(AT, BN_)];            // used in the even CTA
+    uint64_t empty[gm::stages(AT, BN_)];
     uint64_t tmem_full[2];
     uint64_t tmem_empty[2];                   // used in the even CTA
     uint64_t mma_done;
     uint32_t tmem_base;
     int abort_flag;
 };
-template <int AT>
+template <int AT, int BN_ = gm::BN>
 constexpr size_t gemm_smem_bytes() {
-    return sizeof(GemmSmem<AT>) + 1024;
+    return sizeof(GemmSmem<AT, BN_>) + 1024;
 }
-static_assert(gemm_smem_bytes<1>() <= 232448 && gemm_smem_bytes<2>() <= 232448, "GEMM stages do not fit");
+static_assert(gemm_smem_bytes<1>() <= 232448 && gemm_smem_bytes<2>() <= 232448 && gemm_smem_bytes<1, 128>() <= 232448,
+              "GEMM stages do not fit");
 
 // The sizes of one launch.  Rows of A beyond M, of B beyond N and k beyond K
 // are zero-filled by TMA.  a_part: columns between the A_j, which lie side by
@@ -203,24 +207,26 @@ __device__ __forceinline__ void put_f32(GemmTile& t, int k, const float (&v)[32]
 // Epi: a struct with
 //   struct Params (a kernel argument, may hold tensor maps), static prefetch(const Params&),
 //   Epi(const Params&), begin(const GemmTile&), slice(GemmTile&, int k, float (&v)[32])
-//   for columns col0 + 32 k .. + 31 of the thread's row (k = 0..3 in order), end(const GemmTile&).
-template <class Epi, int NA, int MH, bool A_MN, bool B_MN, bool FP16, int SEGMENT>
+//   for columns col0 + 32 k .. + 31 of the thread's row (k = 0 .. BN_ / 64 - 1 in order), end(const GemmTile&).
+template <class Epi, int NA, int MH, bool A_MN, bool B_MN, bool FP16, int SEGMENT, int BN_ = gm::BN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gm::threads(MH), 1)
     gemm_f16_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
                     const __grid_constant__ typename Epi::Params params, const GemmShape shape, unsigned* status) {
     static_assert(MH == 1 || (NA == 1 && SEGMENT == 0), "a tall tile has one A and one sum per row");
     constexpr int AT = NA * MH;  // A tiles of a stage
-    constexpr int STAGES = gm::stages(AT);
+    static_assert(BN_ == gm::BN || (AT == 1 && !B_MN && (BN_ == 64 || BN_ == 128)), "narrow tiles: K-major B, one A");
+    constexpr int SLICES = BN_ / 64;  // 32-column slices of a warp's half of the columns
+    constexpr int STAGES = gm::stages(AT, BN_);
     constexpr int ROWS = 2 * gm::BM * MH;  // rows of a tile
     constexpr int EPI = gm::EPI_WARPS * MH, WARP_TMA = EPI, WARP_MMA = EPI + 1;
     extern __shared__ uint8_t smem_raw[];
-    auto* sm = reinterpret_cast<GemmSmem<AT>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    auto* sm = reinterpret_cast<GemmSmem<AT, BN_>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     volatile int* abort_flag = &sm->abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const bool leader = rank == 0;
     const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
-    const int MT = (shape.M + ROWS - 1) / ROWS, NT = (shape.N + gm::BN - 1) / gm::BN;
+    const int MT = (shape.M + ROWS - 1) / ROWS, NT = (shape.N + BN_ - 1) / BN_;
     const int tiles = MT * NT * shape.splits;
     const int KB_ALL = (shape.K + gm::BK - 1) / gm::BK;
     const int KB = (KB_ALL + shape.splits - 1) / shape.splits;  // k-blocks of a part; those past the end read zeros
@@ -246,7 +252,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gm::threads(MH), 1)
     }
     if (warp == WARP_MMA) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm->tmem_base)),
-                     "r"(2 * gm::BN)
+                     "r"(2 * BN_)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
@@ -271,7 +277,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gm::threads(MH), 1)
         const int rem = tile - first * MT;
         const int width = NT - first < shape.panel ? NT - first : shape.panel;
         m0 = rem / width * ROWS;
-        n0 = (first + rem % width) * gm::BN;
+        n0 = (first + rem % width) * BN_;
     };
 
     if (warp < EPI) {
@@ -297,35 +303,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gm::threads(MH), 1)
         for (int tile = pair; tile < tiles && ok; tile += npairs) {
             int split;
             tile_at(tile, t.m0, t.n0, split);
-            t.col0 = t.n0 + half * (gm::BN / 2);
+            t.col0 = t.n0 + half * (BN_ / 2);
             if (SEGMENT > 0) {
                 t.warp_row = t.m0 + static_cast<int>(rank) * gm::BM + qd * 32;
                 t.row = t.warp_row + lane;
                 t.out_row = t.warp_row + split * shape.split_rows;
                 epi.begin(t);
-                float acc[4][32];
+                float acc[SLICES][32];
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
+                for (int k = 0; k < SLICES; ++k)
 #pragma unroll
                     for (int i = 0; i < 32; ++i) acc[k][i] = 0.f;
                 for (int kb = 0; kb < KB; kb += SEGMENT > 0 ? SEGMENT : 1, ++seg) {
                     const int b = seg & 1;
                     if (!warp_wait(&sm->tmem_full[b], (seg >> 1) & 1, abort_flag)) { give_up(); ok = false; break; }
                     tc_fence_after();
-                    const uint32_t tbase = tmem_base + lane_addr + b * gm::BN + half * (gm::BN / 2);
+                    const uint32_t tbase = tmem_base + lane_addr + b * BN_ + half * (BN_ / 2);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
+                    for (int k = 0; k < SLICES; ++k) {
                         uint32_t r[32];
                         tmem_ld32_nowait(tbase + 32 * k, r);
                         tmem_wait_into(r);
-                        if (k == 3) release(b);
+                        if (k == SLICES - 1) release(b);
 #pragma unroll
                         for (int i = 0; i < 32; ++i) acc[k][i] += __uint_as_float(r[i]);
                     }
                 }
                 if (!ok) break;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) epi.slice(t, k, acc[k]);
+                for (int k = 0; k < SLICES; ++k) epi.slice(t, k, acc[k]);
                 epi.end(t);
             } else {
                 // MH = 2: this warp's half of the tile is in buffer j
@@ -338,15 +344,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gm::threads(MH), 1)
                 epi.begin(t);
                 if (!warp_wait(&sm->tmem_full[b], phase, abort_flag)) { give_up(); break; }
                 tc_fence_after();
-                const uint32_t tbase = tmem_base + lane_addr + b * gm::BN + half * (gm::BN / 2);
+                const uint32_t tbase = tmem_base + lane_addr + b * BN_ + half * (BN_ / 2);
                 if constexpr (MH == 2) {
                     // sixteen warps hide each other's loads
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
+                    for (int k = 0; k < SLICES; ++k) {
                         uint32_t r[32];
                         tmem_ld32_nowait(tbase + 32 * k, r);
                         tmem_wait_into(r);
-                        if (k == 3) release(b);
+                        if (k == SLICES - 1) release(b);
                         float v[32];
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
@@ -357,16 +363,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gm::threads(MH), 1)
                     tmem_ld32_nowait(tbase, ra);
                     tmem_wait_into(ra);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
+                    for (int k = 0; k < SLICES; ++k) {
                         uint32_t(&cur)[32] = k & 1 ? rb : ra;
                         uint32_t(&nxt)[32] = k & 1 ? ra : rb;
-                        if (k < 3) tmem_ld32_nowait(tbase + 32 * (k + 1), nxt);
+                        if (k < SLICES - 1) tmem_ld32_nowait(tbase + 32 * (k + 1), nxt);
                         else release(b);
                         float v[32];
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(cur[i]);
                         epi.slice(t, k, v);
-                        if (k < 3) tmem_wait_into(nxt);
+                        if (k < SLICES - 1) tmem_wait_into(nxt);
                     }
                 }
                 epi.end(t);
@@ -382,7 +388,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gm::threads(MH), 1)
                 int m0, n0, split;
                 tile_at(tile, m0, n0, split);
                 const int arow = m0 + (shape.stack ? 0 : static_cast<int>(rank) * gm::BM);
-                const int acol = rank ? shape.stack : 0, brow = n0 + static_cast<int>(rank) * gm::BM;
+                const int acol = rank ? shape.stack : 0, brow = n0 + static_cast<int>(rank) * (BN_ / 2);
                 // boxes of A without a row are left out: what the tile holds there
                 // ends in rows that no epilogue stores
                 int boxes = 0;
@@ -391,7 +397,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gm::threads(MH), 1)
                     const int r = m0 + (MH == 2 ? 2 * gm::BM * j : 0);
                     boxes += (r < shape.M) + (r + (shape.stack ? 0 : gm::BM) < shape.M);
                 }
-                const uint32_t bytes = static_cast<uint32_t>(boxes * (A_MN ? gm::TILE : shape.a_box * 128) + 2 * gm::TILE);
+                const uint32_t bytes = static_cast<uint32_t>(boxes * (A_MN ? gm::TILE : shape.a_box * 128) + 2 * gm::b_tile(BN_));
                 for (int kb = 0; kb < KB; ++kb, ++it) {
                     const int s = it % STAGES;
                     if (!mbar_wait(&sm->empty[s], ((it / STAGES) & 1) ^ 1, abort_flag)) { give_up(); ok = false; break; }
@@ -434,7 +440,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gm::threads(MH), 1)
         if (lane == 0) {
             if (leader) {
                 const uint32_t idesc = (1u << 4) | (FP16 ? 0u : (1u << 7) | (1u << 10)) | (A_MN ? 1u << 15 : 0u) |
-                                       (B_MN ? 1u << 16 : 0u) | (static_cast<uint32_t>(gm::BN >> 3) << 17) |
+                                       (B_MN ? 1u << 16 : 0u) | (static_cast<uint32_t>(BN_ >> 3) << 17) |
                                        (static_cast<uint32_t>((2 * gm::BM) >> 4) << 24);
                 uint32_t it = 0, seg = 0;
                 bool ok = true;
@@ -466,13 +472,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gm::threads(MH), 1)
                         tc_fence_after();
                         if constexpr (MH == 2) {
                             // upper half, then lower half; the lower buffer comes back later
-                            issue(it, 0, tmem_base + (seg & 1) * gm::BN, first);
+                            issue(it, 0, tmem_base + (seg & 1) * BN_, first);
                             if (last) tc_commit_pair_both(&sm->tmem_full[seg & 1]);
                             if (first && !take(seg + 1)) { give_up(); ok = false; break; }
-                            issue(it, 1, tmem_base + ((seg + 1) & 1) * gm::BN, first);
+                            issue(it, 1, tmem_base + ((seg + 1) & 1) * BN_, first);
                         } else {
 #pragma unroll
-                            for (int j = 0; j < NA; ++j) issue(it, j, tmem_base + (seg & 1) * gm::BN, first && j == 0);
+                            for (int j = 0; j < NA; ++j) issue(it, j, tmem_base + (seg & 1) * BN_, first && j == 0);
                         }
                         tc_commit_pair_both(&sm->empty[it % STAGES]);
                         if (last) {
@@ -494,7 +500,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gm::threads(MH), 1)
     cluster_sync();  // neither CTA leaves while the other may still touch its shared memory
     if (warp == WARP_MMA) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(2 * gm::BN)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(2 * BN_)
                      : "memory");
     }
 }
@@ -540,11 +546,11 @@ inline bool gemm_operand(CUtensorMap* map, bool fp16, bool mn_major, const void*
 // there are rows (1 row x 1440 against 15710 columns: 21 us with boxes of 128, 19 so).
 inline int gemm_a_box(long long M) { return M < gm::BM ? static_cast<int>((M + 7) / 8 * 8) : gm::BM; }
 
-template <class Epi, int NA, int MH, bool A_MN, bool B_MN, bool FP16, int SEGMENT>
+template <class Epi, int NA, int MH, bool A_MN, bool B_MN, bool FP16, int SEGMENT, int BN_ = gm::BN>
 cudaError_t launch_gemm_f16(const CUtensorMap& a, const CUtensorMap& b, const typename Epi::Params& p,
                             const GemmShape& shape, unsigned* status, cudaStream_t stream) {
-    auto kern = gemm_f16_kernel<Epi, NA, MH, A_MN, B_MN, FP16, SEGMENT>;
-    constexpr size_t smem = gemm_smem_bytes<NA * MH>();
+    auto kern = gemm_f16_kernel<Epi, NA, MH, A_MN, B_MN, FP16, SEGMENT, BN_>;
+    constexpr size_t smem = gemm_smem_bytes<NA * MH, BN_>();
     constexpr int rows = 2 * gm::BM * MH;
     static int clusters[64] = {};  // pairs of this kernel that fit on each device at once
     int dev = 0;
@@ -563,7 +569,7 @@ cudaError_t launch_gemm_f16(const CUtensorMap& a, const CUtensorMap& b, const ty
         if (n <= 0) return cudaErrorNotSupported;
         clusters[dev] = n;
     }
-    const long long tiles = static_cast<long long>((shape.M + rows - 1) / rows) * ((shape.N + gm::BN - 1) / gm::BN) *
+    const long long tiles = static_cast<long long>((shape.M + rows - 1) / rows) * ((shape.N + BN_ - 1) / BN_) *
                             shape.splits;
     if (tiles <= 0 || tiles > (1ll << 30)) return cudaErrorInvalidValue;
     cfg.gridDim = dim3(2 * static_cast<unsigned>(tiles < clusters[dev] ? tiles : clusters[dev]));

@@ -12,7 +12,8 @@
 //   forward   z tiles of 256 x 256 whose epilogue keeps, per row and 128
 //             columns, the maximum and the sum of exponentials below it, and
 //             the target's logit; xent_merge_kernel joins the V / 128 parts of
-//             a row.  Memory: x and W once, 8 bytes per row and 128 columns.
+//             a row.  Memory: x and W once, 8 bytes per row and 128 columns (32
+//             for few tokens, whose tiles are turned: LseWords).
 //   backward  per piece of the vocabulary: the z tiles again, their epilogue
 //             writing G in bf16; dX += G . W[piece]; dW[piece] = G^T . x.  G of
 //             one piece is all that exists of the [T, V] matrix.
@@ -23,7 +24,7 @@
 // the largest terms out of it, c = max_t |dloss[t]| is taken out of G and
 // multiplied back into the fp32 results: under a mean or sum reduction G's
 // entry at an unlikely target is then -1 exactly.  A few tokens, whose errors do
-// not average out, take two bf16 parts (kPartsTokens).
+// not average out, take two bf16 parts (kFewTokens).
 //
 // Bound by what feeds the tensor cores (gemm_f16.cuh) and, over longer runs, by
 // the power limit: 2 T V D operations forward, 6 T V D backward (a third of them
@@ -33,8 +34,6 @@
 // spend about three instructions per logit on pairs of values; an index into
 // a row's registers anywhere in them would put the row into local memory.
 #include <cuda.h>
-
-#include <type_traits>
 
 #include "gemm_f16.cuh"
 #include "sbl_common.cuh"
@@ -116,34 +115,40 @@ struct LsePart {
 };
 
 // Backward epilogue of the logits: G / c in bf16, columns counted from the
-// piece's first word v0.  PARTS: as two bf16 values, the second what the first
-// rounds off.
-template <bool PARTS>
+// piece's first word v0.
+struct GradInputs {
+    const float* lse;
+    const float* dloss;
+    const float* cmax;
+    const long long* target;
+    long long ignore, v0;
+    int T, V, n;  // n: words of the piece
+};
+// -lse log2 e and dloss / c of a token; d stays 0 for one without a gradient.
+__device__ __forceinline__ void token_factors(const GradInputs& q, int token, long long y, float& less, float& d) {
+    const float c = *q.cmax;
+    less = -__ldg(q.lse + token) * kLog2e;
+    if (y != q.ignore && y >= 0 && y < q.V && c != 0.f) d = __fdiv_rn(__ldg(q.dloss + token), c);
+}
+
 struct GradTile {
     struct Params {
-        CUtensorMap g, g_low;
-        const float* lse;
-        const float* dloss;
-        const float* cmax;
-        const long long* target;
-        long long ignore, v0;
-        int T, V, n;  // n: words of the piece
+        CUtensorMap g;
+        GradInputs q;
     };
     static __device__ __forceinline__ void prefetch(const Params& p) { prefetch_tmap(&p.g); }
     const Params& p;
-    float less, d;   // -lse log2 e; dloss / c
+    float less, d;
     long long tcol;
     bool some_zero;  // a row of this warp has d = 0
-    __device__ __forceinline__ explicit GradTile(const Params& q) : p(q), less(0.f), d(0.f), tcol(-1), some_zero(false) {}
+    __device__ __forceinline__ explicit GradTile(const Params& r) : p(r), less(0.f), d(0.f), tcol(-1), some_zero(false) {}
     __device__ __forceinline__ void begin(const GemmTile& t) {
         d = 0.f;
         tcol = -1;
-        if (t.row < p.T) {
-            const long long y = __ldg(p.target + t.row);
-            const float c = *p.cmax;
-            less = -__ldg(p.lse + t.row) * kLog2e;
-            if (y != p.ignore && y >= 0 && y < p.V && c != 0.f) d = __fdiv_rn(__ldg(p.dloss + t.row), c);
-            tcol = y - p.v0 - t.col0;
+        if (t.row < p.q.T) {
+            const long long y = __ldg(p.q.target + t.row);
+            token_factors(p.q, t.row, y, less, d);
+            tcol = y - p.q.v0 - t.col0;
         }
         some_zero = __any_sync(0xFFFFFFFFu, d == 0.f);
     }
@@ -172,31 +177,132 @@ struct GradTile {
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = d == 0.f ? 0.f : v[i];
         }
-        if constexpr (PARTS) {
-            // the products read whole tiles of both parts: zeros past the last word
-            const int valid = p.n - (t.col0 + 32 * k);
-            if (valid < 32) {
+        put_bf16(t, k, v, &p.g);
+    }
+    __device__ __forceinline__ void end(const GemmTile&) {}
+};
+
+// ---------------------------------------------------------------- a few tokens
+// Up to kFewTokens the logits' tiles are turned: 256 words x 64 or 128 tokens
+// instead of 256 tokens, most of them past the end, x 256 words.  A thread then
+// holds one word's logits of 32 tokens, and a warp's 32 words are a part of the row.
+// 64 x 128000 x 896: 53 us forward, 66% of the copy bandwidth (70 us not turned), 49 us
+// for G (54); one token x 15710 x 1440: 15.5 us (19), of which 5 are the launch.
+constexpr int kFewTokens = 128;
+
+// Reduces 32 values over the 32 lanes; lane l gets value l's result (norm.cu's
+// warp_sums: each step halves the values a lane carries).
+template <class Op>
+__device__ __forceinline__ float reduce_to_lanes(float (&v)[32], Op op) {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    if (i >= valid) v[i] = 0.f;
-            }
-            uint4 w[4];
-            to_bf16(v, w);
-            put_64(t, t.col0 + 32 * k, 0, w, &p.g);
+    for (int n = 32, off = 16; n > 1; n >>= 1, off >>= 1) {
+        const bool up = (lane & off) != 0;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const uint32_t h[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    v[8 * c + 2 * j] -= __uint_as_float(h[j] << 16);
-                    v[8 * c + 2 * j + 1] -= __uint_as_float(h[j] & 0xFFFF0000u);
-                }
-            }
-            to_bf16(v, w);
-            put_64(t, t.col0 + 32 * k, 0, w, &p.g_low);
-        } else {
-            put_bf16(t, k, v, &p.g);
+        for (int i = 0; i < n / 2; ++i) {
+            const float send = up ? v[i] : v[i + n / 2], keep = up ? v[i + n / 2] : v[i];
+            v[i] = op(keep, __shfl_xor_sync(0xFFFFFFFFu, send, off));
         }
+    }
+    return v[0];
+}
+
+// The lane (0..31) whose word is the target of each lane's token, or -1.
+__device__ __forceinline__ int target_lane(long long y, long long first_word) {
+    const long long d = y - first_word;
+    return d >= 0 && d < 32 ? static_cast<int>(d) : -1;
+}
+
+// Forward: part[t][p] = (max, sum of exp(z - max)) over words 32 p .. + 31.
+struct LseWords {
+    using Params = LsePart::Params;
+    static __device__ __forceinline__ void prefetch(const Params&) {}
+    const Params& p;
+    __device__ __forceinline__ explicit LseWords(const Params& q) : p(q) {}
+    __device__ __forceinline__ void begin(const GemmTile&) {}
+    __device__ __forceinline__ void slice(GemmTile& t, int k, float (&v)[32]) {
+        const int c0 = t.col0 + 32 * k, token = c0 + t.lane;
+        if (c0 >= p.T || t.warp_row >= p.V) return;
+        if (t.row >= p.V) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = -INFINITY;
+        }
+        const int at = token < p.T ? target_lane(__ldg(p.target + token), t.warp_row) : -1;
+        if (__any_sync(0xFFFFFFFFu, at >= 0)) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (__shfl_sync(0xFFFFFFFFu, at, i) == t.lane) p.tlogit[c0 + i] = v[i];
+        }
+        float w[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) w[i] = v[i];
+        const float m = reduce_to_lanes(w, [](float a, float b) { return fmaxf(a, b); });
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = exp2_fast((v[i] - __shfl_sync(0xFFFFFFFFu, m, i)) * kLog2e);
+        const float sum = reduce_to_lanes(v, [](float a, float b) { return a + b; });
+        if (token < p.T) p.part[static_cast<size_t>(token) * p.P + (t.warp_row >> 5)] = make_float2(m, sum);
+    }
+    __device__ __forceinline__ void end(const GemmTile&) {}
+};
+
+// Backward: G / c as two bf16 values, the second what the first rounds off,
+// written along the words like GradTile's.
+struct GradWords {
+    struct Params {
+        CUtensorMap g, g_low;
+        GradInputs q;
+    };
+    static __device__ __forceinline__ void prefetch(const Params& p) {
+        prefetch_tmap(&p.g);
+        prefetch_tmap(&p.g_low);
+    }
+    const Params& p;
+    __device__ __forceinline__ explicit GradWords(const Params& r) : p(r) {}
+    __device__ __forceinline__ void begin(const GemmTile&) {}
+    // 32 tokens x 32 words from tokens' pairs in registers (thread: one word)
+    // through a box (64B swizzle) to column warp_row, row c0 of the map.
+    __device__ __forceinline__ void put(GemmTile& t, int c0, const uint32_t (&h)[16], const CUtensorMap* map) {
+        uint8_t* const box = t.box + (t.stores & 1) * gm::BOX;  // two boxes: MH = 1
+        ++t.stores;
+        if (t.lane == 0) bulk_wait_read<1>();
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            const uint32_t a = smem_u32(box + i * 64 + (((t.lane >> 3) ^ ((i >> 1) & 3)) << 4) + (t.lane & 7) * 2);
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(a), "h"(static_cast<uint16_t>(h[i >> 1] >> (16 * (i & 1)))) : "memory");
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (t.lane == 0) tma_store_2d(map, smem_u32(box), t.warp_row, c0);
+    }
+    __device__ __forceinline__ void slice(GemmTile& t, int k, float (&v)[32]) {
+        const GradInputs& q = p.q;
+        const int c0 = t.col0 + 32 * k, token = c0 + t.lane;
+        if (c0 >= q.T) return;
+        float less = 0.f, d = 0.f;
+        int at = -1;
+        if (token < q.T) {
+            const long long y = __ldg(q.target + token);
+            token_factors(q, token, y, less, d);
+            at = target_lane(y, q.v0 + t.warp_row);
+        }
+        const bool hot = __any_sync(0xFFFFFFFFu, at >= 0), inside = t.row < q.n;
+        uint32_t h[16];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            v[i] = exp2_fast(fmaf(v[i], kLog2e, __shfl_sync(0xFFFFFFFFu, less, i)));
+            if (hot) v[i] -= __shfl_sync(0xFFFFFFFFu, at, i) == t.lane ? 1.0f : 0.0f;
+            const float di = __shfl_sync(0xFFFFFFFFu, d, i);
+            // words past the last, which the products read, and ignored tokens (see GradTile): zeros
+            v[i] = inside && di != 0.f ? v[i] * di : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) h[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+        put(t, c0, h, &p.g);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            h[i] = pack_bf16(v[2 * i] - __uint_as_float(h[i] << 16), v[2 * i + 1] - __uint_as_float(h[i] & 0xFFFF0000u));
+        put(t, c0, h, &p.g_low);
     }
     __device__ __forceinline__ void end(const GemmTile&) {}
 };
@@ -359,7 +465,7 @@ __global__ void __launch_bounds__(256) xent_dx_kernel(const float* __restrict__ 
 }
 
 size_t round256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
-int parts(long long V) { return static_cast<int>((V + 127) / 128); }
+int parts(long long T, long long V) { return static_cast<int>(T <= kFewTokens ? (V + 31) / 32 : (V + 127) / 128); }
 
 // Words per piece of the backward: at most 2^28 entries of G (512 MB).  Smaller
 // pieces stay in L2 but cost more launches and more passes over dX's sums
@@ -372,13 +478,12 @@ long long piece_words(long long T, long long V) {
     return w < all ? w : all;
 }
 
-// Up to this many tokens G goes as two bf16 parts: the rounding of a token's
+// Up to kFewTokens G goes as two bf16 parts: the rounding of a token's
 // one large entry, its target's, moves a whole row of dX and dW together, and
 // over a few tokens such errors do not average out (1 to 8 tokens: up to 1.75
 // times the error that rounding the results alone leaves).  These sizes are bound by
 // reading W and writing dW, which hides the second part's MMAs.
-constexpr int kPartsTokens = 128;
-bool g_parts(long long T) { return T <= kPartsTokens; }
+bool g_parts(long long T) { return T <= kFewTokens; }
 
 // dX has few tiles (T / 512 x D / 256) and a long reduction over the words, so it
 // may be cut into parts, each with its own fp32 sums over the pieces, which
@@ -404,7 +509,7 @@ cudaError_t launch_either(const CUtensorMap& a, const CUtensorMap& b, const type
 }  // namespace
 
 size_t xent_workspace_bytes(long long T, long long V) {
-    return round256(static_cast<size_t>(parts(V)) * T * sizeof(float2)) + round256(static_cast<size_t>(T) * sizeof(float));
+    return round256(static_cast<size_t>(parts(T, V)) * T * sizeof(float2)) + round256(static_cast<size_t>(T) * sizeof(float));
 }
 
 size_t xent_backward_workspace_bytes(long long T, long long D, long long V, int need_dx) {
@@ -417,23 +522,34 @@ cudaError_t launch_xent(const uint16_t* x, long long T, long long D, const uint1
                         cudaStream_t st) {
     float2* part = static_cast<float2*>(ws);
     float* tlogit = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) +
-                                             round256(static_cast<size_t>(parts(V)) * T * sizeof(float2)));
+                                             round256(static_cast<size_t>(parts(T, V)) * T * sizeof(float2)));
+    const int Ti = static_cast<int>(T), Vi = static_cast<int>(V), Di = static_cast<int>(D);
+    const LsePart::Params p{part, tlogit, target, Ti, Vi, parts(T, V)};
     CUtensorMap a, b;
-    if (!gemm_operand(&a, false, false, x, T, D, D, gemm_a_box(T)) || !gemm_operand(&b, false, false, w, V, D, D))
-        return cudaErrorInvalidValue;
-    const LsePart::Params p{part, tlogit, target, static_cast<int>(T), static_cast<int>(V), parts(V)};
-    const GemmShape shape{static_cast<int>(T), static_cast<int>(V), static_cast<int>(D), 0, 8, 1, 0, gemm_a_box(T), 0};
-    // one segment holds the whole sum: tall tiles need none
-    const bool tall = D <= kLogitSegment * gm::BK && gemm_tall(T, V, 1);
-    if (cudaError_t e = T <= 256 ? launch_gemm_f16<LsePart, 1, 1, false, false, false, kFewSegment>(a, b, p, shape, status, st)
-                        : tall ? launch_gemm_f16<LsePart, 1, 2, false, false, false, 0>(a, b, p, shape, status, st)
-                               : launch_gemm_f16<LsePart, 1, 1, false, false, false, kLogitSegment>(a, b, p, shape, status, st))
-        return e;
+    cudaError_t e;
+    if (T <= kFewTokens) {
+        const int box = T <= 64 ? 32 : 64;
+        if (!gemm_operand(&a, false, false, w, V, D, D, gemm_a_box(V)) || !gemm_operand(&b, false, false, x, T, D, D, box))
+            return cudaErrorInvalidValue;
+        const GemmShape shape{Vi, Ti, Di, 0, 1, 1, 0, gemm_a_box(V), 0};
+        e = T <= 64 ? launch_gemm_f16<LseWords, 1, 1, false, false, false, kFewSegment, 64>(a, b, p, shape, status, st)
+                    : launch_gemm_f16<LseWords, 1, 1, false, false, false, kFewSegment, 128>(a, b, p, shape, status, st);
+    } else {
+        if (!gemm_operand(&a, false, false, x, T, D, D) || !gemm_operand(&b, false, false, w, V, D, D))
+            return cudaErrorInvalidValue;
+        const GemmShape shape{Ti, Vi, Di, 0, 8, 1, 0, gm::BM, 0};
+        // one segment holds the whole sum: tall tiles need none
+        const bool tall = D <= kLogitSegment * gm::BK && gemm_tall(T, V, 1);
+        e = T <= 256 ? launch_gemm_f16<LsePart, 1, 1, false, false, false, kFewSegment>(a, b, p, shape, status, st)
+            : tall   ? launch_gemm_f16<LsePart, 1, 2, false, false, false, 0>(a, b, p, shape, status, st)
+                     : launch_gemm_f16<LsePart, 1, 1, false, false, false, kLogitSegment>(a, b, p, shape, status, st);
+    }
+    if (e != cudaSuccess) return e;
     // a block per row while that leaves SMs idle otherwise
     auto merge = [&](auto kern, int rows_per_block) {
         return pdl_launch(kern, dim3(static_cast<unsigned>((T + rows_per_block - 1) / rows_per_block)), dim3(256), 0, st,
                           static_cast<const float2*>(part), static_cast<const float*>(tlogit), target, ignore,
-                          static_cast<int>(T), static_cast<int>(V), parts(V), loss, lse, status);
+                          static_cast<int>(T), static_cast<int>(V), parts(T, V), loss, lse, status);
     };
     return T <= 1024 ? merge(xent_merge_kernel<8>, 1) : merge(xent_merge_kernel<1>, 8);
 }
@@ -462,29 +578,27 @@ cudaError_t launch_xent_backward(const float* dloss, const uint16_t* x, long lon
         const long long n = V - v0 < piece ? V - v0 : piece;
         const int ni = static_cast<int>(n);
         const uint16_t* wp = w + v0 * D;
+        const GradInputs in{lse, dloss, cmax, target, ignore, v0, Ti, static_cast<int>(V), ni};
         CUtensorMap xk, wk;
-        if (!gemm_operand(&xk, false, false, x, T, D, D, gemm_a_box(T)) || !gemm_operand(&wk, false, false, wp, n, D, D))
-            return cudaErrorInvalidValue;
-        auto logits = [&](auto parts_tag) -> cudaError_t {
-            constexpr bool PARTS = decltype(parts_tag)::value;
-            typename GradTile<PARTS>::Params gp;
-            if (!gemm_result_bf16(&gp.g, g, T, PARTS ? piece : n, pitch) ||
-                !gemm_result_bf16(&gp.g_low, g + (PARTS ? piece : 0), T, PARTS ? piece : n, pitch))
+        if (parts) {
+            const int box = T <= 64 ? 32 : 64;
+            GradWords::Params p;
+            p.q = in;
+            if (!gemm_operand(&wk, false, false, wp, n, D, D, gemm_a_box(n)) || !gemm_operand(&xk, false, false, x, T, D, D, box) ||
+                !gemm_result_bf16(&p.g, g, T, piece, pitch) || !gemm_result_bf16(&p.g_low, g + piece, T, piece, pitch))
                 return cudaErrorInvalidValue;
-            gp.lse = lse;
-            gp.dloss = dloss;
-            gp.cmax = cmax;
-            gp.target = target;
-            gp.ignore = ignore;
-            gp.v0 = v0;
-            gp.T = Ti;
-            gp.V = static_cast<int>(V);
-            gp.n = ni;
-            const GemmShape shape{Ti, ni, Di, 0, 8, 1, 0, gemm_a_box(T), 0};
-            if constexpr (PARTS) return launch_gemm_f16<GradTile<true>, 1, 1, false, false, false, 0>(xk, wk, gp, shape, status, st);
-            else return launch_either<GradTile<false>, false, false>(xk, wk, gp, shape, status, st);
-        };
-        e = parts ? logits(std::true_type{}) : logits(std::false_type{});
+            const GemmShape shape{ni, Ti, Di, 0, 1, 1, 0, gemm_a_box(n), 0};
+            e = T <= 64 ? launch_gemm_f16<GradWords, 1, 1, false, false, false, 0, 64>(wk, xk, p, shape, status, st)
+                        : launch_gemm_f16<GradWords, 1, 1, false, false, false, 0, 128>(wk, xk, p, shape, status, st);
+        } else {
+            GradTile::Params p;
+            p.q = in;
+            if (!gemm_operand(&xk, false, false, x, T, D, D) || !gemm_operand(&wk, false, false, wp, n, D, D) ||
+                !gemm_result_bf16(&p.g, g, T, n, pitch))
+                return cudaErrorInvalidValue;
+            const GemmShape shape{Ti, ni, Di, 0, 8, 1, 0, gm::BM, 0};
+            e = launch_either<GradTile, false, false>(xk, wk, p, shape, status, st);
+        }
         if (e != cudaSuccess) return e;
         const long long g_cols = parts ? piece + n : n;
         const int low = static_cast<int>(piece);  // columns from a part to the next
