@@ -119,16 +119,20 @@ struct LsePart {
 struct GradInputs {
     const float* lse;
     const float* dloss;
-    const float* cmax;
+    float* cmax;
     const long long* target;
     long long ignore, v0;
     int T, V, n;  // n: words of the piece
 };
 // -lse log2 e and dloss / c of a token; d stays 0 for one without a gradient.
-__device__ __forceinline__ void token_factors(const GradInputs& q, int token, long long y, float& less, float& d) {
-    const float c = *q.cmax;
+__device__ __forceinline__ void token_factors(const GradInputs& q, float c, int token, long long y, float& less, float& d) {
     less = -__ldg(q.lse + token) * kLog2e;
     if (y != q.ignore && y >= 0 && y < q.V && c != 0.f) d = __fdiv_rn(__ldg(q.dloss + token), c);
+}
+
+// |dloss| of a token that counts; magnitudes order like their bits, NaN above all.
+__device__ __forceinline__ unsigned weight_bits(const float* dloss, const long long* target, long long ignore, int t) {
+    return target[t] != ignore ? __float_as_uint(dloss[t]) & 0x7FFFFFFFu : 0u;
 }
 
 struct GradTile {
@@ -147,7 +151,7 @@ struct GradTile {
         tcol = -1;
         if (t.row < p.q.T) {
             const long long y = __ldg(p.q.target + t.row);
-            token_factors(p.q, t.row, y, less, d);
+            token_factors(p.q, *p.q.cmax, t.row, y, less, d);
             tcol = y - p.q.v0 - t.col0;
         }
         some_zero = __any_sync(0xFFFFFFFFu, d == 0.f);
@@ -257,7 +261,14 @@ struct GradWords {
         prefetch_tmap(&p.g_low);
     }
     const Params& p;
-    __device__ __forceinline__ explicit GradWords(const Params& r) : p(r) {}
+    float c;
+    // c of a few tokens by each warp itself (a kernel less); kept for the products
+    __device__ __forceinline__ explicit GradWords(const Params& r) : p(r) {
+        unsigned m = 0;
+        for (int t = threadIdx.x & 31; t < p.q.T; t += 32) m = max(m, weight_bits(p.q.dloss, p.q.target, p.q.ignore, t));
+        c = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, m));
+        if (blockIdx.x == 0 && threadIdx.x == 0) *p.q.cmax = c;
+    }
     __device__ __forceinline__ void begin(const GemmTile&) {}
     // 32 tokens x 32 words from tokens' pairs in registers (thread: one word)
     // through a box (64B swizzle) to column warp_row, row c0 of the map.
@@ -283,7 +294,7 @@ struct GradWords {
         int at = -1;
         if (token < q.T) {
             const long long y = __ldg(q.target + token);
-            token_factors(q, token, y, less, d);
+            token_factors(q, c, token, y, less, d);
             at = target_lane(y, q.v0 + t.warp_row);
         }
         const bool hot = __any_sync(0xFFFFFFFFu, at >= 0), inside = t.row < q.n;
@@ -412,9 +423,8 @@ __global__ void __launch_bounds__(1024) xent_cmax_kernel(const float* __restrict
     __shared__ unsigned s[32];
     asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    unsigned m = 0;  // magnitudes order like their bits
-    for (int t = threadIdx.x; t < T; t += 1024)
-        if (target[t] != ignore) m = max(m, __float_as_uint(dloss[t]) & 0x7FFFFFFFu);
+    unsigned m = 0;
+    for (int t = threadIdx.x; t < T; t += 1024) m = max(m, weight_bits(dloss, target, ignore, t));
     m = __reduce_max_sync(0xFFFFFFFFu, m);
     if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = m;
     __syncthreads();
@@ -571,7 +581,8 @@ cudaError_t launch_xent_backward(const float* dloss, const uint16_t* x, long lon
     const long long piece = piece_words(T, V);
     const bool parts = g_parts(T);
     const long long pitch = parts ? 2 * piece : piece;
-    cudaError_t e = pdl_launch(xent_cmax_kernel, dim3(1), dim3(1024), 0, st, dloss, target, ignore, static_cast<int>(T), cmax);
+    cudaError_t e = cudaSuccess;
+    if (!parts) e = pdl_launch(xent_cmax_kernel, dim3(1), dim3(1024), 0, st, dloss, target, ignore, static_cast<int>(T), cmax);
     const int Ti = static_cast<int>(T), Di = static_cast<int>(D);
     const int d_panel = (Di + gm::BN - 1) / gm::BN;
     for (long long v0 = 0; v0 < V && e == cudaSuccess; v0 += piece) {
