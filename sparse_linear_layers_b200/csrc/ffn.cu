@@ -917,19 +917,20 @@ FfnSpace ffn_space(long long T, long long K, long long F) {
 // Up to 128 tokens v's two parts lie in the two CTAs' rows of one A (GemmShape::stack)
 // instead of in two A of 256 rows: half the MMAs.
 bool dx_stacks(long long T) { return T <= gm::BM; }
-int dx_splits(long long T, long long K, long long Fp) {
-    return gemm_splits((T + 255) / 256 * ((K + gm::BN - 1) / gm::BN), 2 * Fp / gm::BK, (dx_stacks(T) ? 8.0 : 4.0) * T * K,
-                       dx_stacks(T) ? 0.45 : 0.8, 32);
-}
-int dw_splits(long long T, long long K, long long Fp) {
-    return gemm_splits((2 * Fp + 255) / 256 * ((K + gm::BN - 1) / gm::BN), (T + gm::BK - 1) / gm::BK, 8.0 * Fp * K, 0.8, 32);
+// (The plan is of both gradients also when one is wanted: the same bits.)
+GemmPlan grad_plan(long long T, long long K, long long Fp) {
+    const long long cols = (K + gm::BN - 1) / gm::BN;
+    const GemmWork dx{(T + 255) / 256 * cols, 2 * Fp / gm::BK, dx_stacks(T) ? 0.45 : 0.8, 3.0,
+                      (dx_stacks(T) ? 8.0 : 4.0) * T * K, 32};
+    const GemmWork dw{(2 * Fp + 255) / 256 * cols, (T + gm::BK - 1) / gm::BK, 0.8, 3.0, 8.0 * Fp * K, 32};
+    return gemm_plan(dx, dw);
 }
 
 struct FfnBwdSpace {
     FfnSpace fwd;
-    size_t maxima, v, parts, codes, xs, sums, end;
+    size_t maxima, v, parts, codes, xs, dx_sums, dw_sums, end;
     long long Fp, nmax16, dx_rows;
-    int dx_splits, dw_splits;
+    GemmPlan plan;  // of dX and dW
 };
 FfnBwdSpace ffn_bwd_space(long long T, long long K, long long F, int need_dx, int need_dw) {
     FfnBwdSpace s;
@@ -941,14 +942,12 @@ FfnBwdSpace ffn_bwd_space(long long T, long long K, long long F, int need_dx, in
     s.parts = s.v + round256(static_cast<size_t>(T) * 2 * s.Fp * 4);
     s.codes = s.parts + round256(static_cast<size_t>(T) * 4 * s.Fp * 2);
     s.xs = s.codes + (need_dx ? round256(static_cast<size_t>(2) * s.Fp * K * 2) : 0);
-    s.sums = s.xs + (need_dw ? round256(static_cast<size_t>(T) * K * 2) : 0);
-    // the parts of a split reduction; dX's have been added before dW's are written
+    s.dx_sums = s.xs + (need_dw ? round256(static_cast<size_t>(T) * K * 2) : 0);
     s.dx_rows = dx_stacks(T) ? 2 * gm::BM : (T + 31) / 32 * 32;
-    s.dx_splits = need_dx ? dx_splits(T, K, s.Fp) : 1;
-    s.dw_splits = need_dw ? dw_splits(T, K, s.Fp) : 1;
-    const size_t a = need_dx && (s.dx_splits > 1 || dx_stacks(T)) ? static_cast<size_t>(s.dx_splits) * s.dx_rows * K * 4 : 0;
-    const size_t b = s.dw_splits > 1 ? static_cast<size_t>(s.dw_splits) * 2 * s.Fp * K * 4 : 0;
-    s.end = s.sums + round256(a > b ? a : b);
+    s.plan = grad_plan(T, K, s.Fp);
+    const bool dx_parts = need_dx && (s.plan.splits1 > 1 || dx_stacks(T)), dw_parts = need_dw && s.plan.splits2 > 1;
+    s.dw_sums = s.dx_sums + (dx_parts ? round256(static_cast<size_t>(s.plan.splits1) * s.dx_rows * K * 4) : 0);
+    s.end = s.dw_sums + (dw_parts ? round256(static_cast<size_t>(s.plan.splits2) * 2 * s.Fp * K * 4) : 0);
     return s;
 }
 
@@ -1167,60 +1166,71 @@ cudaError_t launch_ffn_backward(const float* dh, const uint16_t* x, long long T,
         return e;
 
     const int k_panel = (Ki + gm::BN - 1) / gm::BN;
-    float* const sums = reinterpret_cast<float*>(base + sp.sums);
-    // adds the parts of `rows` rows that start at row0 of each
-    auto join = [&](int splits, long long split_rows, long long row0, long long rows, float* out) {
-        return pdl_launch(ffn_sum_kernel, dim3(blocks_for(rows * K / 4, 8)), dim3(256), 0, st,
-                          reinterpret_cast<const float4*>(sums + row0 * K), splits, split_rows * K / 4, rows * K / 4,
-                          reinterpret_cast<float4*>(out));
-    };
+    float* const dx_sums = reinterpret_cast<float*>(base + sp.dx_sums);
+    float* const dw_sums = reinterpret_cast<float*>(base + sp.dw_sums);
+    using DxJob = GemmJob<FfnDx, 2, false, true>;
+    using DxStacked = GemmJob<FfnDx, 1, false, true>;
+    using DwJob = GemmJob<FfnDw, 2, true, true>;
+    const bool stack = dx_stacks(T);
+    const int dx_splits = sp.plan.splits1, dw_splits = sp.plan.splits2;
+    GemmArgs<DxJob> gx;
+    GemmArgs<DwJob> gw;
+    memset(&gx, 0, sizeof(gx));
+    memset(&gw, 0, sizeof(gw));
     if (dx) {
-        CUtensorMap a, b;
-        FfnDx::Params p;
-        const int splits = sp.dx_splits, a_box = gemm_a_box(T);
-        const bool stack = dx_stacks(T);
-        if (!gemm_operand(&a, true, false, parts, T, 4 * sp.Fp, 4 * sp.Fp, a_box) ||
-            !gemm_operand(&b, true, true, codes, 2 * sp.Fp, K, K) ||
-            !gemm_result_f32(&p.out, splits > 1 || stack ? sums : dx, splits > 1 || stack ? splits * sp.dx_rows : T, K))
+        const int a_box = gemm_a_box(T);
+        const bool parts_first = dx_splits > 1 || stack;
+        if (!gemm_operand(&gx.a, true, false, parts, T, 4 * sp.Fp, 4 * sp.Fp, a_box) ||
+            !gemm_operand(&gx.b, true, true, codes, 2 * sp.Fp, K, K) ||
+            !gemm_result_f32(&gx.p.out, parts_first ? dx_sums : dx, parts_first ? dx_splits * sp.dx_rows : T, K))
             return cudaErrorInvalidValue;
-        p.row_max = row_max;
-        p.s_tok = s_tok;
-        p.T = Ti;
-        p.row_mask = stack ? gm::BM - 1 : -1;
-        const GemmShape shape{Ti, Ki, 2 * Fp, 2 * Fp, k_panel, splits, static_cast<int>(sp.dx_rows), a_box, stack ? 2 * Fp : 0};
-        if (cudaError_t e = stack ? launch_gemm_f16<FfnDx, 1, 1, false, true, true, 4>(a, b, p, shape, status, st)
-                                  : launch_gemm_f16<FfnDx, 2, 1, false, true, true, 4>(a, b, p, shape, status, st))
-            return e;
-        if (splits > 1 || stack)
-            if (cudaError_t e = stack ? join(2 * splits, gm::BM, 0, T, dx) : join(splits, sp.dx_rows, 0, T, dx)) return e;
+        gx.p.row_max = row_max;
+        gx.p.s_tok = s_tok;
+        gx.p.T = Ti;
+        gx.p.row_mask = stack ? gm::BM - 1 : -1;
+        gx.shape = GemmShape{Ti, Ki, 2 * Fp, 2 * Fp, k_panel, dx_splits, static_cast<int>(sp.dx_rows), a_box, 0, stack ? 2 * Fp : 0};
     }
     if (need_dw) {
-        CUtensorMap a, b;
-        FfnDw::Params p;
-        memset(&p, 0, sizeof(p));
-        const int splits = sp.dw_splits;
-        if (!gemm_operand(&a, true, true, parts, T, 4 * sp.Fp, 4 * sp.Fp) || !gemm_operand(&b, true, true, xs, T, K, K))
+        FfnDw::Params& p = gw.p;
+        if (!gemm_operand(&gw.a, true, true, parts, T, 4 * sp.Fp, 4 * sp.Fp) || !gemm_operand(&gw.b, true, true, xs, T, K, K))
             return cudaErrorInvalidValue;
-        if (splits > 1 ? !gemm_result_f32(&p.out_g, sums, splits * 2 * sp.Fp, K) || !gemm_result_f32(&p.out_u, sums, splits * 2 * sp.Fp, K)
-                       : (dwg && !gemm_result_f32(&p.out_g, dwg, F, K)) || (dwu && !gemm_result_f32(&p.out_u, dwu, F, K)))
+        if (dw_splits > 1 ? !gemm_result_f32(&p.out_g, dw_sums, dw_splits * 2 * sp.Fp, K) ||
+                                !gemm_result_f32(&p.out_u, dw_sums, dw_splits * 2 * sp.Fp, K)
+                          : (dwg && !gemm_result_f32(&p.out_g, dwg, F, K)) || (dwu && !gemm_result_f32(&p.out_u, dwu, F, K)))
             return cudaErrorInvalidValue;
         p.all_max = all_max;
         p.scale_g = scale_g;
         p.scale_u = scale_u;
         p.F = Fi;
         p.Fp = Fp;
-        p.up_row = splits > 1 ? 0 : Fp;
+        p.up_row = dw_splits > 1 ? 0 : Fp;
         p.want_g = dwg != nullptr;
         p.want_u = dwu != nullptr;
         p.ternary = ternary;
-        const GemmShape shape{2 * Fp, Ki, Ti, 2 * Fp, k_panel, splits, 2 * Fp, gm::BM, 0};
-        if (cudaError_t e = launch_gemm_f16<FfnDw, 2, 1, true, true, true, 4>(a, b, p, shape, status, st)) return e;
-        if (splits > 1 && dwg)
-            if (cudaError_t e = join(splits, 2 * sp.Fp, 0, F, dwg)) return e;
-        if (splits > 1 && dwu)
-            if (cudaError_t e = join(splits, 2 * sp.Fp, sp.Fp, F, dwu)) return e;
+        gw.shape = GemmShape{2 * Fp, Ki, Ti, 2 * Fp, k_panel, dw_splits, 2 * Fp, gm::BM, sp.plan.lead, 0};
     }
-    return cudaSuccess;
+    const GemmArgs<DxStacked> gs{gx.a, gx.b, gx.p, gx.shape};
+    const GemmArgs<GemmNoJob> none{};
+    cudaError_t e;
+    if (dx && need_dw)
+        e = stack ? launch_gemm_jobs<DxStacked, DwJob, 1, true, 4>(gs, gw, status, st)
+                  : launch_gemm_jobs<DxJob, DwJob, 1, true, 4>(gx, gw, status, st);
+    else if (dx)
+        e = stack ? launch_gemm_jobs<DxStacked, GemmNoJob, 1, true, 4>(gs, none, status, st)
+                  : launch_gemm_jobs<DxJob, GemmNoJob, 1, true, 4>(gx, none, status, st);
+    else
+        e = launch_gemm_jobs<DwJob, GemmNoJob, 1, true, 4>(gw, none, status, st);
+    // adds `splits` parts of `rows` rows, split_rows apart
+    auto join = [&](const float* sums, int splits, long long split_rows, long long rows, float* out) {
+        return pdl_launch(ffn_sum_kernel, dim3(blocks_for(rows * K / 4, 8)), dim3(256), 0, st,
+                          reinterpret_cast<const float4*>(sums), splits, split_rows * K / 4, rows * K / 4,
+                          reinterpret_cast<float4*>(out));
+    };
+    if (e == cudaSuccess && dx && (dx_splits > 1 || stack))
+        e = stack ? join(dx_sums, 2 * dx_splits, gm::BM, T, dx) : join(dx_sums, dx_splits, sp.dx_rows, T, dx);
+    if (e == cudaSuccess && dw_splits > 1 && dwg) e = join(dw_sums, dw_splits, 2 * sp.Fp, F, dwg);
+    if (e == cudaSuccess && dw_splits > 1 && dwu) e = join(dw_sums + sp.Fp * K, dw_splits, 2 * sp.Fp, F, dwu);
+    return e;
 }
 
 }  // namespace sbl

@@ -40,6 +40,8 @@
 
 #include <cuda.h>
 
+#include <type_traits>
+
 #include "sbl_common.cuh"
 #include "tc_util.cuh"
 
@@ -88,6 +90,7 @@ struct GemmShape {
     int splits;     // parts of the reduction, each a GEMM of its own into rows
     int split_rows; // split_rows further down (whole staging boxes: a multiple of 32)
     int a_box;      // rows of a box of K-major A (gemm_a_box)
+    int lead;       // of a second product: tiles that a pair takes first if it has one less of the first
     int stack;      // 0, or: the odd CTA's A rows are the even one's again, `stack` columns further on
                     // (K-major A of at most 128 rows); their sums are rows 128 .. 255 of the result
 };
@@ -208,13 +211,39 @@ __device__ __forceinline__ void put_f32(GemmTile& t, int k, const float (&v)[32]
 //   struct Params (a kernel argument, may hold tensor maps), static prefetch(const Params&),
 //   Epi(const Params&), begin(const GemmTile&), slice(GemmTile&, int k, float (&v)[32])
 //   for columns col0 + 32 k .. + 31 of the thread's row (k = 0 .. BN_ / 64 - 1 in order), end(const GemmTile&).
-template <class Epi, int NA, int MH, bool A_MN, bool B_MN, bool FP16, int SEGMENT, int BN_ = gm::BN>
+// A product of a launch.
+template <class Epi_, int NA_, bool A_MN_, bool B_MN_>
+struct GemmJob {
+    using Epi = Epi_;
+    static constexpr int NA = NA_;
+    static constexpr bool A_MN = A_MN_, B_MN = B_MN_;
+};
+struct GemmNoEpi {
+    struct Params {};
+    __device__ __forceinline__ explicit GemmNoEpi(const Params&) {}
+};
+using GemmNoJob = GemmJob<GemmNoEpi, 1, false, false>;
+template <class Job>
+struct GemmArgs {
+    CUtensorMap a, b;
+    typename Job::Epi::Params p;
+    GemmShape shape;
+};
+template <>
+struct GemmArgs<GemmNoJob> {
+    GemmNoEpi::Params p;
+};
+
+// J2: a second product that does not depend on the first, in the same launch;
+// its tiles follow the first's on each pair (GemmShape::lead).
+template <class J1, class J2, int MH, bool FP16, int SEGMENT, int BN_ = gm::BN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gm::threads(MH), 1)
-    gemm_f16_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
-                    const __grid_constant__ typename Epi::Params params, const GemmShape shape, unsigned* status) {
+    gemm_f16_kernel(const __grid_constant__ GemmArgs<J1> g1, const __grid_constant__ GemmArgs<J2> g2, unsigned* status) {
+    constexpr bool TWO = !std::is_same_v<J2, GemmNoJob>;
+    constexpr int NA = J1::NA > J2::NA ? J1::NA : J2::NA;
     static_assert(MH == 1 || (NA == 1 && SEGMENT == 0), "a tall tile has one A and one sum per row");
     constexpr int AT = NA * MH;  // A tiles of a stage
-    static_assert(BN_ == gm::BN || (AT == 1 && !B_MN && (BN_ == 64 || BN_ == 128)), "narrow tiles: K-major B, one A");
+    static_assert(BN_ == gm::BN || (AT == 1 && !TWO && !J1::B_MN && (BN_ == 64 || BN_ == 128)), "narrow tiles: K-major B, one A");
     constexpr int SLICES = BN_ / 64;  // 32-column slices of a warp's half of the columns
     constexpr int STAGES = gm::stages(AT, BN_);
     constexpr int ROWS = 2 * gm::BM * MH;  // rows of a tile
@@ -226,16 +255,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gm::threads(MH), 1)
     const uint32_t rank = cluster_ctarank();
     const bool leader = rank == 0;
     const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
-    const int MT = (shape.M + ROWS - 1) / ROWS, NT = (shape.N + BN_ - 1) / BN_;
-    const int tiles = MT * NT * shape.splits;
-    const int KB_ALL = (shape.K + gm::BK - 1) / gm::BK;
-    const int KB = (KB_ALL + shape.splits - 1) / shape.splits;  // k-blocks of a part; those past the end read zeros
+    auto args = [&](auto second) -> const auto& {
+        if constexpr (second.value) return g2;
+        else return g1;
+    };
+    auto tiles_of = [](const GemmShape& shape) {
+        return (shape.M + ROWS - 1) / ROWS * ((shape.N + BN_ - 1) / BN_) * shape.splits;
+    };
+    auto blocks_of = [](const GemmShape& shape) {  // k-blocks of a part; those past the end read zeros
+        return ((shape.K + gm::BK - 1) / gm::BK + shape.splits - 1) / shape.splits;
+    };
+    // f(which product, tile) for this pair's tiles, until it returns false
+    auto for_tiles = [&](auto&& f) {
+        const int n1 = tiles_of(g1.shape);
+        for (int t = pair; t < n1; t += npairs)
+            if (!f(std::false_type{}, t)) return;
+        if constexpr (TWO) {
+            // pairs with a tile less of the first product begin with `lead` of the second
+            const int n2 = tiles_of(g2.shape), extra = n1 % npairs, idle = npairs - extra;
+            const int order = pair >= extra ? pair - extra : idle + pair, lead = extra ? g2.shape.lead : 0;
+            if (pair >= extra)
+                for (int i = 0, t = order; i < lead && t < n2; ++i, t += idle)
+                    if (!f(std::true_type{}, t)) return;
+            for (int t = idle * lead + order; t < n2; t += npairs)
+                if (!f(std::true_type{}, t)) return;
+        }
+    };
 
     asm volatile("griddepcontrol.launch_dependents;");
     if (threadIdx.x == 32) {
-        prefetch_tmap(&tmap_a);
-        prefetch_tmap(&tmap_b);
-        Epi::prefetch(params);
+        prefetch_tmap(&g1.a);
+        prefetch_tmap(&g1.b);
+        J1::Epi::prefetch(g1.p);
+        if constexpr (TWO) {
+            prefetch_tmap(&g2.a);
+            prefetch_tmap(&g2.b);
+            J2::Epi::prefetch(g2.p);
+        }
     }
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -270,7 +326,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gm::threads(MH), 1)
     };
     // tiles go panel by panel of column tiles, row by row of a panel: the
     // panel's B tiles stay in L2 while A streams past them once per panel
-    auto tile_at = [&](int tile, int& m0, int& n0, int& split) {
+    auto tile_at = [](const GemmShape& shape, int tile, int& m0, int& n0, int& split) {
+        const int MT = (shape.M + ROWS - 1) / ROWS, NT = (shape.N + BN_ - 1) / BN_;
         split = shape.splits > 1 ? tile / (MT * NT) : 0;
         tile -= split * MT * NT;
         const int first = tile / (MT * shape.panel) * shape.panel;
@@ -284,7 +341,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gm::threads(MH), 1)
         // ------------------------------------------------------------ epilogue
         const int qd = warp & 3, half = (warp >> 2) & 1;
         const uint32_t lane_addr = static_cast<uint32_t>(qd * 32) << 16;
-        Epi epi(params);
         GemmTile t;
         t.lane = lane;
         t.boxes = 2 / MH;
@@ -299,10 +355,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gm::threads(MH), 1)
                 else mbar_arrive_cluster(map_to_cta(smem_u32(&sm->tmem_empty[b]), 0));
             }
         };
-        bool ok = true;
-        for (int tile = pair; tile < tiles && ok; tile += npairs) {
+        auto store_tile = [&](auto second, int tile, auto& epi) {
+            const GemmShape& shape = args(second).shape;
+            const int KB = blocks_of(shape);
             int split;
-            tile_at(tile, t.m0, t.n0, split);
+            tile_at(shape, tile, t.m0, t.n0, split);
             t.col0 = t.n0 + half * (BN_ / 2);
             if (SEGMENT > 0) {
                 t.warp_row = t.m0 + static_cast<int>(rank) * gm::BM + qd * 32;
@@ -316,7 +373,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gm::threads(MH), 1)
                     for (int i = 0; i < 32; ++i) acc[k][i] = 0.f;
                 for (int kb = 0; kb < KB; kb += SEGMENT > 0 ? SEGMENT : 1, ++seg) {
                     const int b = seg & 1;
-                    if (!warp_wait(&sm->tmem_full[b], (seg >> 1) & 1, abort_flag)) { give_up(); ok = false; break; }
+                    if (!warp_wait(&sm->tmem_full[b], (seg >> 1) & 1, abort_flag)) { give_up(); return false; }
                     tc_fence_after();
                     const uint32_t tbase = tmem_base + lane_addr + b * BN_ + half * (BN_ / 2);
 #pragma unroll
@@ -329,7 +386,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gm::threads(MH), 1)
                         for (int i = 0; i < 32; ++i) acc[k][i] += __uint_as_float(r[i]);
                     }
                 }
-                if (!ok) break;
 #pragma unroll
                 for (int k = 0; k < SLICES; ++k) epi.slice(t, k, acc[k]);
                 epi.end(t);
@@ -342,7 +398,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gm::threads(MH), 1)
                 t.row = t.warp_row + lane;
                 t.out_row = t.warp_row + split * shape.split_rows;
                 epi.begin(t);
-                if (!warp_wait(&sm->tmem_full[b], phase, abort_flag)) { give_up(); break; }
+                if (!warp_wait(&sm->tmem_full[b], phase, abort_flag)) { give_up(); return false; }
                 tc_fence_after();
                 const uint32_t tbase = tmem_base + lane_addr + b * BN_ + half * (BN_ / 2);
                 if constexpr (MH == 2) {
@@ -377,55 +433,70 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gm::threads(MH), 1)
                 }
                 epi.end(t);
             }
+            return true;
+        };
+        if constexpr (TWO) {  // made for each tile: both at once cost registers
+            for_tiles([&](auto second, int tile) {
+                typename std::conditional_t<second.value, J2, J1>::Epi epi(args(second).p);
+                return store_tile(second, tile, epi);
+            });
+        } else {
+            typename J1::Epi epi(g1.p);
+            for_tiles([&](auto second, int tile) { return store_tile(second, tile, epi); });
         }
         if (lane == 0) bulk_wait_all();
     } else if (warp == WARP_TMA) {
         // ------------------------------------------------------------ TMA producer
         if (lane == 0) {
             uint32_t it = 0;
-            bool ok = true;
-            for (int tile = pair; tile < tiles && ok; tile += npairs) {
+            for_tiles([&](auto second, int tile) {
+                using Job = std::conditional_t<second.value, J2, J1>;
+                constexpr int JT = Job::NA * MH;
+                const auto& g = args(second);
+                const GemmShape& shape = g.shape;
+                const int KB = blocks_of(shape);
                 int m0, n0, split;
-                tile_at(tile, m0, n0, split);
+                tile_at(shape, tile, m0, n0, split);
                 const int arow = m0 + (shape.stack ? 0 : static_cast<int>(rank) * gm::BM);
                 const int acol = rank ? shape.stack : 0, brow = n0 + static_cast<int>(rank) * (BN_ / 2);
                 // boxes of A without a row are left out: what the tile holds there
                 // ends in rows that no epilogue stores
                 int boxes = 0;
 #pragma unroll
-                for (int j = 0; j < AT; ++j) {
+                for (int j = 0; j < JT; ++j) {
                     const int r = m0 + (MH == 2 ? 2 * gm::BM * j : 0);
                     boxes += (r < shape.M) + (r + (shape.stack ? 0 : gm::BM) < shape.M);
                 }
-                const uint32_t bytes = static_cast<uint32_t>(boxes * (A_MN ? gm::TILE : shape.a_box * 128) + 2 * gm::b_tile(BN_));
+                const uint32_t bytes = static_cast<uint32_t>(boxes * (Job::A_MN ? gm::TILE : shape.a_box * 128) + 2 * gm::b_tile(BN_));
                 for (int kb = 0; kb < KB; ++kb, ++it) {
                     const int s = it % STAGES;
-                    if (!mbar_wait(&sm->empty[s], ((it / STAGES) & 1) ^ 1, abort_flag)) { give_up(); ok = false; break; }
+                    if (!mbar_wait(&sm->empty[s], ((it / STAGES) & 1) ^ 1, abort_flag)) { give_up(); return false; }
                     // the even CTA expects the bytes of both CTAs
                     if (leader) mbar_arrive_expect_tx(&sm->full[s], bytes);
                     const uint32_t full = map_to_cta(smem_u32(&sm->full[s]), 0);
                     const int k0 = (split * KB + kb) * gm::BK;
 #pragma unroll
-                    for (int j = 0; j < AT; ++j) {
+                    for (int j = 0; j < JT; ++j) {
                         const uint32_t dst = smem_u32(sm->a[s][j]);
                         const int part = MH == 2 ? 0 : j * shape.a_part, r = arow + (MH == 2 ? 2 * gm::BM * j : 0);
                         if (r >= shape.M) continue;
-                        if (A_MN) {
-                            tma_load_2d_pair(dst, &tmap_a, part + r, k0, full);
-                            tma_load_2d_pair(dst + gm::TILE / 2, &tmap_a, part + r + 64, k0, full);
+                        if (Job::A_MN) {
+                            tma_load_2d_pair(dst, &g.a, part + r, k0, full);
+                            tma_load_2d_pair(dst + gm::TILE / 2, &g.a, part + r + 64, k0, full);
                         } else {
-                            tma_load_2d_pair(dst, &tmap_a, acol + part + k0, r, full);
+                            tma_load_2d_pair(dst, &g.a, acol + part + k0, r, full);
                         }
                     }
                     const uint32_t dst = smem_u32(sm->b[s]);
-                    if (B_MN) {
-                        tma_load_2d_pair(dst, &tmap_b, brow, k0, full);
-                        tma_load_2d_pair(dst + gm::TILE / 2, &tmap_b, brow + 64, k0, full);
+                    if (Job::B_MN) {
+                        tma_load_2d_pair(dst, &g.b, brow, k0, full);
+                        tma_load_2d_pair(dst + gm::TILE / 2, &g.b, brow + 64, k0, full);
                     } else {
-                        tma_load_2d_pair(dst, &tmap_b, k0, brow, full);
+                        tma_load_2d_pair(dst, &g.b, k0, brow, full);
                     }
                 }
-            }
+                return true;
+            });
             // let the issued loads land before either CTA can exit (the even
             // CTA's barriers count both CTAs' loads)
             if (leader) {
@@ -439,46 +510,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gm::threads(MH), 1)
         // ------------------------------------------------------------ MMA issuer (even CTA)
         if (lane == 0) {
             if (leader) {
-                const uint32_t idesc = (1u << 4) | (FP16 ? 0u : (1u << 7) | (1u << 10)) | (A_MN ? 1u << 15 : 0u) |
-                                       (B_MN ? 1u << 16 : 0u) | (static_cast<uint32_t>(BN_ >> 3) << 17) |
-                                       (static_cast<uint32_t>((2 * gm::BM) >> 4) << 24);
                 uint32_t it = 0, seg = 0;
-                bool ok = true;
                 // buffer of the seg-th accumulation, once the epilogue has read what it held
                 auto take = [&](uint32_t sg) {
                     if (!mbar_wait(&sm->tmem_empty[sg & 1], ((sg >> 1) & 1) ^ 1, abort_flag)) return false;
                     tc_fence_after();
                     return true;
                 };
-                // the MMAs of one k-block (stage of iteration i) on A tile j
-                auto issue = [&](uint32_t i, int j, uint32_t d, bool fresh) {
-                    const uint32_t a0 = smem_u32(sm->a[i % STAGES][j]), b0 = smem_u32(sm->b[i % STAGES]);
-#pragma unroll
-                    for (int kk = 0; kk < gm::BK / 16; ++kk)
-                        tc_mma_pair_f16(d, A_MN ? sw128_mn_desc(a0 + kk * 2048) : sw128_desc(a0 + kk * 32),
-                                        B_MN ? sw128_mn_desc(b0 + kk * 2048) : sw128_desc(b0 + kk * 32), idesc,
-                                        !(fresh && kk == 0));
-                };
                 auto loaded = [&](uint32_t i) { return mbar_wait(&sm->full[i % STAGES], (i / STAGES) & 1, abort_flag); };
-                for (int tile = pair; tile < tiles && ok; tile += npairs) {
+                for_tiles([&](auto second, int) {
+                    using Job = std::conditional_t<second.value, J2, J1>;
+                    constexpr uint32_t idesc = (1u << 4) | (FP16 ? 0u : (1u << 7) | (1u << 10)) | (Job::A_MN ? 1u << 15 : 0u) |
+                                               (Job::B_MN ? 1u << 16 : 0u) | (static_cast<uint32_t>(BN_ >> 3) << 17) |
+                                               (static_cast<uint32_t>((2 * gm::BM) >> 4) << 24);
+                    const int KB = blocks_of(args(second).shape);
+                    // the MMAs of one k-block (stage of iteration i) on A tile j
+                    auto issue = [&](uint32_t i, int j, uint32_t d, bool fresh) {
+                        const uint32_t a0 = smem_u32(sm->a[i % STAGES][j]), b0 = smem_u32(sm->b[i % STAGES]);
+#pragma unroll
+                        for (int kk = 0; kk < gm::BK / 16; ++kk)
+                            tc_mma_pair_f16(d, Job::A_MN ? sw128_mn_desc(a0 + kk * 2048) : sw128_desc(a0 + kk * 32),
+                                            Job::B_MN ? sw128_mn_desc(b0 + kk * 2048) : sw128_desc(b0 + kk * 32), idesc,
+                                            !(fresh && kk == 0));
+                    };
                     for (int kb = 0; kb < KB; ++kb, ++it) {
                         bool first = kb == 0, last = kb == KB - 1;
                         if constexpr (SEGMENT > 0) {
                             first = kb % SEGMENT == 0;
                             last = last || kb % SEGMENT == SEGMENT - 1;
                         }
-                        if (first && !take(seg)) { give_up(); ok = false; break; }
-                        if (!loaded(it)) { give_up(); ok = false; break; }
+                        if (first && !take(seg)) { give_up(); return false; }
+                        if (!loaded(it)) { give_up(); return false; }
                         tc_fence_after();
                         if constexpr (MH == 2) {
                             // upper half, then lower half; the lower buffer comes back later
                             issue(it, 0, tmem_base + (seg & 1) * BN_, first);
                             if (last) tc_commit_pair_both(&sm->tmem_full[seg & 1]);
-                            if (first && !take(seg + 1)) { give_up(); ok = false; break; }
+                            if (first && !take(seg + 1)) { give_up(); return false; }
                             issue(it, 1, tmem_base + ((seg + 1) & 1) * BN_, first);
                         } else {
 #pragma unroll
-                            for (int j = 0; j < NA; ++j) issue(it, j, tmem_base + (seg & 1) * BN_, first && j == 0);
+                            for (int j = 0; j < Job::NA; ++j) issue(it, j, tmem_base + (seg & 1) * BN_, first && j == 0);
                         }
                         tc_commit_pair_both(&sm->empty[it % STAGES]);
                         if (last) {
@@ -486,7 +558,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gm::threads(MH), 1)
                             seg += MH;
                         }
                     }
-                }
+                    return true;
+                });
                 // every MMA must be complete before either CTA frees tensor memory
                 tc_commit_pair_both(&sm->mma_done);
             }
@@ -546,11 +619,10 @@ inline bool gemm_operand(CUtensorMap* map, bool fp16, bool mn_major, const void*
 // there are rows (1 row x 1440 against 15710 columns: 21 us with boxes of 128, 19 so).
 inline int gemm_a_box(long long M) { return M < gm::BM ? static_cast<int>((M + 7) / 8 * 8) : gm::BM; }
 
-template <class Epi, int NA, int MH, bool A_MN, bool B_MN, bool FP16, int SEGMENT, int BN_ = gm::BN>
-cudaError_t launch_gemm_f16(const CUtensorMap& a, const CUtensorMap& b, const typename Epi::Params& p,
-                            const GemmShape& shape, unsigned* status, cudaStream_t stream) {
-    auto kern = gemm_f16_kernel<Epi, NA, MH, A_MN, B_MN, FP16, SEGMENT, BN_>;
-    constexpr size_t smem = gemm_smem_bytes<NA * MH, BN_>();
+template <class J1, class J2, int MH, bool FP16, int SEGMENT, int BN_ = gm::BN>
+cudaError_t launch_gemm_jobs(const GemmArgs<J1>& g1, const GemmArgs<J2>& g2, unsigned* status, cudaStream_t stream) {
+    auto kern = gemm_f16_kernel<J1, J2, MH, FP16, SEGMENT, BN_>;
+    constexpr size_t smem = gemm_smem_bytes<(J1::NA > J2::NA ? J1::NA : J2::NA) * MH, BN_>();
     constexpr int rows = 2 * gm::BM * MH;
     static int clusters[64] = {};  // pairs of this kernel that fit on each device at once
     int dev = 0;
@@ -569,8 +641,11 @@ cudaError_t launch_gemm_f16(const CUtensorMap& a, const CUtensorMap& b, const ty
         if (n <= 0) return cudaErrorNotSupported;
         clusters[dev] = n;
     }
-    const long long tiles = static_cast<long long>((shape.M + rows - 1) / rows) * ((shape.N + BN_ - 1) / BN_) *
-                            shape.splits;
+    auto count = [&](const GemmShape& shape) {
+        return static_cast<long long>((shape.M + rows - 1) / rows) * ((shape.N + BN_ - 1) / BN_) * shape.splits;
+    };
+    long long tiles = count(g1.shape);
+    if constexpr (!std::is_same_v<J2, GemmNoJob>) tiles += count(g2.shape);
     if (tiles <= 0 || tiles > (1ll << 30)) return cudaErrorInvalidValue;
     cfg.gridDim = dim3(2 * static_cast<unsigned>(tiles < clusters[dev] ? tiles : clusters[dev]));
     cudaLaunchAttribute attr[1];
@@ -578,7 +653,16 @@ cudaError_t launch_gemm_f16(const CUtensorMap& a, const CUtensorMap& b, const ty
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, a, b, p, shape, status);
+    return cudaLaunchKernelEx(&cfg, kern, g1, g2, status);
+}
+
+// One product.
+template <class Epi, int NA, int MH, bool A_MN, bool B_MN, bool FP16, int SEGMENT, int BN_ = gm::BN>
+cudaError_t launch_gemm_f16(const CUtensorMap& a, const CUtensorMap& b, const typename Epi::Params& p,
+                            const GemmShape& shape, unsigned* status, cudaStream_t stream) {
+    using Job = GemmJob<Epi, NA, A_MN, B_MN>;
+    return launch_gemm_jobs<Job, GemmNoJob, MH, FP16, SEGMENT, BN_>(GemmArgs<Job>{a, b, p, shape}, GemmArgs<GemmNoJob>{}, status,
+                                                                   stream);
 }
 
 // Parts that a reduction of KB k-blocks is best cut into, when each part's fp32
@@ -598,6 +682,44 @@ inline int gemm_splits(long long tiles, long long KB, double part_bytes, double 
         if (s == 1 || cost < least) {
             least = cost;
             best = s;
+        }
+    }
+    return best;
+}
+
+// The same for two products in one launch (the first's tiles the longer ones).
+// us_tile: the least that a tile takes, its epilogue's time.
+struct GemmWork {
+    long long tiles, KB;
+    double us_per_block, us_tile, part_bytes;
+    int most;  // parts at most
+};
+struct GemmPlan {
+    int splits1, splits2, lead;
+    double us;
+};
+inline GemmPlan gemm_plan(const GemmWork& w1, const GemmWork& w2) {
+    static constexpr int kParts[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64};
+    auto tile_us = [](const GemmWork& w, int s) {
+        const double us = static_cast<double>((w.KB + s - 1) / s) * w.us_per_block;
+        return us > w.us_tile ? us : w.us_tile;
+    };
+    auto sum_us = [](const GemmWork& w, int s) { return s > 1 ? 3.0 + s * 2.0 * w.part_bytes / 6e6 : 0.0; };
+    GemmPlan best{1, 1, 0, 0.0};
+    for (int s1 : kParts) {
+        if (s1 > 1 && (s1 > w1.most || s1 > w1.KB)) break;
+        const double l1 = tile_us(w1, s1);
+        const long long n1 = w1.tiles * s1, each = n1 / 74, extra = n1 % 74, idle = 74 - extra;
+        for (int s2 : kParts) {
+            if (s2 > 1 && (s2 > w2.most || s2 > w2.KB || w2.tiles * s2 > 148)) break;
+            const double l2 = tile_us(w2, s2);
+            const long long n2 = w2.tiles * s2;
+            const int lead = extra ? static_cast<int>(l1 / l2 + 0.5) : 0;
+            const long long early = n2 < idle * lead ? n2 : idle * lead, rest = n2 - early, full = rest / 74, tail = rest % 74;
+            const double a = each * l1 + static_cast<double>((early + idle - 1) / idle + full + (tail > 0)) * l2;
+            const double b = extra ? (each + 1) * l1 + static_cast<double>(full + (tail > idle)) * l2 : 0.0;
+            const double us = (a > b ? a : b) + sum_us(w1, s1) + sum_us(w2, s2);
+            if ((s1 == 1 && s2 == 1) || us < best.us) best = GemmPlan{s1, s2, lead, us};
         }
     }
     return best;

@@ -541,13 +541,13 @@ cudaError_t launch_xent(const uint16_t* x, long long T, long long D, const uint1
         const int box = T <= 64 ? 32 : 64;
         if (!gemm_operand(&a, false, false, w, V, D, D, gemm_a_box(V)) || !gemm_operand(&b, false, false, x, T, D, D, box))
             return cudaErrorInvalidValue;
-        const GemmShape shape{Vi, Ti, Di, 0, 1, 1, 0, gemm_a_box(V), 0};
+        const GemmShape shape{Vi, Ti, Di, 0, 1, 1, 0, gemm_a_box(V), 0, 0};
         e = T <= 64 ? launch_gemm_f16<LseWords, 1, 1, false, false, false, kFewSegment, 64>(a, b, p, shape, status, st)
                     : launch_gemm_f16<LseWords, 1, 1, false, false, false, kFewSegment, 128>(a, b, p, shape, status, st);
     } else {
         if (!gemm_operand(&a, false, false, x, T, D, D) || !gemm_operand(&b, false, false, w, V, D, D))
             return cudaErrorInvalidValue;
-        const GemmShape shape{Ti, Vi, Di, 0, 8, 1, 0, gm::BM, 0};
+        const GemmShape shape{Ti, Vi, Di, 0, 8, 1, 0, gm::BM, 0, 0};
         // one segment holds the whole sum: tall tiles need none
         const bool tall = D <= kLogitSegment * gm::BK && gemm_tall(T, V, 1);
         e = T <= 256 ? launch_gemm_f16<LsePart, 1, 1, false, false, false, kFewSegment>(a, b, p, shape, status, st)
@@ -598,7 +598,7 @@ cudaError_t launch_xent_backward(const float* dloss, const uint16_t* x, long lon
             if (!gemm_operand(&wk, false, false, wp, n, D, D, gemm_a_box(n)) || !gemm_operand(&xk, false, false, x, T, D, D, box) ||
                 !gemm_result_bf16(&p.g, g, T, piece, pitch) || !gemm_result_bf16(&p.g_low, g + piece, T, piece, pitch))
                 return cudaErrorInvalidValue;
-            const GemmShape shape{ni, Ti, Di, 0, 1, 1, 0, gemm_a_box(n), 0};
+            const GemmShape shape{ni, Ti, Di, 0, 1, 1, 0, gemm_a_box(n), 0, 0};
             e = T <= 64 ? launch_gemm_f16<GradWords, 1, 1, false, false, false, 0, 64>(wk, xk, p, shape, status, st)
                         : launch_gemm_f16<GradWords, 1, 1, false, false, false, 0, 128>(wk, xk, p, shape, status, st);
         } else {
@@ -607,7 +607,7 @@ cudaError_t launch_xent_backward(const float* dloss, const uint16_t* x, long lon
             if (!gemm_operand(&xk, false, false, x, T, D, D) || !gemm_operand(&wk, false, false, wp, n, D, D) ||
                 !gemm_result_bf16(&p.g, g, T, n, pitch))
                 return cudaErrorInvalidValue;
-            const GemmShape shape{Ti, ni, Di, 0, 8, 1, 0, gm::BM, 0};
+            const GemmShape shape{Ti, ni, Di, 0, 8, 1, 0, gm::BM, 0, 0};
             e = launch_either<GradTile, false, false>(xk, wk, p, shape, status, st);
         }
         if (e != cudaSuccess) return e;
@@ -622,7 +622,7 @@ cudaError_t launch_xent_backward(const float* dloss, const uint16_t* x, long lon
             if (!gemm_operand(&gk, false, false, g, T, g_cols, pitch, gemm_a_box(T)) || !gemm_operand(&wn, false, true, wp, n, D, D) ||
                 !gemm_result_f32(&sp.out, dx32, splits * rows, D))
                 return cudaErrorInvalidValue;
-            const GemmShape shape{Ti, Di, ni, 0, d_panel, splits, static_cast<int>(rows), gemm_a_box(T), parts ? low : 0};
+            const GemmShape shape{Ti, Di, ni, 0, d_panel, splits, static_cast<int>(rows), gemm_a_box(T), 0, parts ? low : 0};
             e = parts ? launch_gemm_f16<SumF32, 1, 1, false, true, false, 0>(gk, wn, sp, shape, status, st)
                       : launch_either<SumF32, false, true>(gk, wn, sp, shape, status, st);
             if (e != cudaSuccess) return e;
@@ -634,7 +634,7 @@ cudaError_t launch_xent_backward(const float* dloss, const uint16_t* x, long lon
             if (!gemm_operand(&gm_, false, true, g, T, g_cols, pitch) || !gemm_operand(&xn, false, true, x, T, D, D) ||
                 !gemm_result_bf16(&bp.out, dw + v0 * D, n, D, D))
                 return cudaErrorInvalidValue;
-            const GemmShape shape{ni, Di, Ti, low, d_panel, 1, 0, gm::BM, 0};
+            const GemmShape shape{ni, Di, Ti, low, d_panel, 1, 0, gm::BM, 0, 0};
             e = parts ? launch_gemm_f16<ScaledBf16, 2, 1, true, true, false, 0>(gm_, xn, bp, shape, status, st)
                       : launch_either<ScaledBf16, true, true>(gm_, xn, bp, shape, status, st);
         }
