@@ -920,9 +920,9 @@ bool dx_stacks(long long T) { return T <= gm::BM; }
 // (The plan is of both gradients also when one is wanted: the same bits.)
 GemmPlan grad_plan(long long T, long long K, long long Fp) {
     const long long cols = (K + gm::BN - 1) / gm::BN;
-    const GemmWork dx{(T + 255) / 256 * cols, 2 * Fp / gm::BK, dx_stacks(T) ? 0.45 : 0.8, 3.0,
+    const GemmWork dx{(T + 255) / 256 * cols, 2 * Fp / gm::BK, dx_stacks(T) ? 0.45 : 0.8, 1.0,
                       (dx_stacks(T) ? 8.0 : 4.0) * T * K, 32};
-    const GemmWork dw{(2 * Fp + 255) / 256 * cols, (T + gm::BK - 1) / gm::BK, 0.8, 3.0, 8.0 * Fp * K, 32};
+    const GemmWork dw{(2 * Fp + 255) / 256 * cols, (T + gm::BK - 1) / gm::BK, 0.8, 1.0, 8.0 * Fp * K, 32};
     return gemm_plan(dx, dw);
 }
 

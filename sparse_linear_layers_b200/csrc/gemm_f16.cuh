@@ -234,6 +234,12 @@ struct GemmArgs<GemmNoJob> {
     GemmNoEpi::Params p;
 };
 
+template <bool SECOND, class A, class B>
+__device__ __forceinline__ const std::conditional_t<SECOND, B, A>& gemm_pick(const A& a, const B& b) {
+    if constexpr (SECOND) return b;
+    else return a;
+}
+
 // J2: a second product that does not depend on the first, in the same launch;
 // its tiles follow the first's on each pair (GemmShape::lead).
 template <class J1, class J2, int MH, bool FP16, int SEGMENT, int BN_ = gm::BN>
@@ -255,10 +261,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gm::threads(MH), 1)
     const uint32_t rank = cluster_ctarank();
     const bool leader = rank == 0;
     const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
-    auto args = [&](auto second) -> const auto& {
-        if constexpr (second.value) return g2;
-        else return g1;
-    };
     auto tiles_of = [](const GemmShape& shape) {
         return (shape.M + ROWS - 1) / ROWS * ((shape.N + BN_ - 1) / BN_) * shape.splits;
     };
@@ -356,7 +358,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gm::threads(MH), 1)
             }
         };
         auto store_tile = [&](auto second, int tile, auto& epi) {
-            const GemmShape& shape = args(second).shape;
+            const GemmShape& shape = gemm_pick<second.value>(g1, g2).shape;
             const int KB = blocks_of(shape);
             int split;
             tile_at(shape, tile, t.m0, t.n0, split);
@@ -437,7 +439,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gm::threads(MH), 1)
         };
         if constexpr (TWO) {  // made for each tile: both at once cost registers
             for_tiles([&](auto second, int tile) {
-                typename std::conditional_t<second.value, J2, J1>::Epi epi(args(second).p);
+                typename std::conditional_t<second.value, J2, J1>::Epi epi(gemm_pick<second.value>(g1, g2).p);
                 return store_tile(second, tile, epi);
             });
         } else {
@@ -452,7 +454,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gm::threads(MH), 1)
             for_tiles([&](auto second, int tile) {
                 using Job = std::conditional_t<second.value, J2, J1>;
                 constexpr int JT = Job::NA * MH;
-                const auto& g = args(second);
+                const auto& g = gemm_pick<second.value>(g1, g2);
                 const GemmShape& shape = g.shape;
                 const int KB = blocks_of(shape);
                 int m0, n0, split;
@@ -523,7 +525,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gm::threads(MH), 1)
                     constexpr uint32_t idesc = (1u << 4) | (FP16 ? 0u : (1u << 7) | (1u << 10)) | (Job::A_MN ? 1u << 15 : 0u) |
                                                (Job::B_MN ? 1u << 16 : 0u) | (static_cast<uint32_t>(BN_ >> 3) << 17) |
                                                (static_cast<uint32_t>((2 * gm::BM) >> 4) << 24);
-                    const int KB = blocks_of(args(second).shape);
+                    const int KB = blocks_of(gemm_pick<second.value>(g1, g2).shape);
                     // the MMAs of one k-block (stage of iteration i) on A tile j
                     auto issue = [&](uint32_t i, int j, uint32_t d, bool fresh) {
                         const uint32_t a0 = smem_u32(sm->a[i % STAGES][j]), b0 = smem_u32(sm->b[i % STAGES]);
@@ -665,30 +667,13 @@ cudaError_t launch_gemm_f16(const CUtensorMap& a, const CUtensorMap& b, const ty
                                                                    stream);
 }
 
-// Parts that a reduction of KB k-blocks is best cut into, when each part's fp32
-// result (part_bytes) is written and read back: `tiles` tiles take rounds of 74
-// pairs of SMs, a k-block of a tile about us_per_block (what L2 feeds a pair:
-// 0.55 us for 256 rows and one A, 0.45 if half of them are past the end, 0.8 for 512
-// rows or two A), the sum over
-// the parts 3 us and its bytes at 6 TB/s.  1 token, 2 tiles of 619 k-blocks: 37 parts
-// (one part took 200 us); 1001 tokens, 16 tiles of 88: 4 parts (59 us -> 25 us).
-inline int gemm_splits(long long tiles, long long KB, double part_bytes, double us_per_block, int most) {
-    int best = 1;
-    double least = 0.0;
-    for (int s = 1; s <= most && s <= KB; ++s) {
-        const double rounds = static_cast<double>((tiles * s + 73) / 74);
-        const double cost = rounds * static_cast<double>((KB + s - 1) / s) * us_per_block +
-                            (s > 1 ? 3.0 + s * 2.0 * part_bytes / 6e6 : 0.0);
-        if (s == 1 || cost < least) {
-            least = cost;
-            best = s;
-        }
-    }
-    return best;
-}
-
-// The same for two products in one launch (the first's tiles the longer ones).
-// us_tile: the least that a tile takes, its epilogue's time.
+// What the parts that two products' reductions are cut into cost, when each
+// part's fp32 result (part_bytes) is written and read back: the tiles of both in
+// one launch (the first's the longer ones) take rounds of 74 pairs of SMs, a
+// k-block of a tile about us_per_block (what L2 feeds a pair: 0.55 us for 256 rows
+// and one A, 0.45 to 0.52 if half of them are past the end, 0.8 for 512 rows or two A), each
+// tile us_tile more (1 us; 2.5 for 512 rows, whose epilogue no MMAs hide), the sum
+// over the parts 3 us and its bytes at 6 TB/s.  Alone, 1 token, 2 tiles of 619 k-blocks: 200 us in one part, 37 in 37.
 struct GemmWork {
     long long tiles, KB;
     double us_per_block, us_tile, part_bytes;
@@ -699,11 +684,8 @@ struct GemmPlan {
     double us;
 };
 inline GemmPlan gemm_plan(const GemmWork& w1, const GemmWork& w2) {
-    static constexpr int kParts[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64};
-    auto tile_us = [](const GemmWork& w, int s) {
-        const double us = static_cast<double>((w.KB + s - 1) / s) * w.us_per_block;
-        return us > w.us_tile ? us : w.us_tile;
-    };
+    static constexpr int kParts[] = {1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 12, 14, 16, 18, 20, 24, 28, 32, 37, 48, 64};
+    auto tile_us = [](const GemmWork& w, int s) { return static_cast<double>((w.KB + s - 1) / s) * w.us_per_block + w.us_tile; };
     auto sum_us = [](const GemmWork& w, int s) { return s > 1 ? 3.0 + s * 2.0 * w.part_bytes / 6e6 : 0.0; };
     GemmPlan best{1, 1, 0, 0.0};
     for (int s1 : kParts) {
@@ -726,7 +708,7 @@ inline GemmPlan gemm_plan(const GemmWork& w1, const GemmWork& w2) {
 }
 
 // Whether 512-row tiles finish first: their rounds at 0.8 us per k-block against
-// those of 256-row tiles at 0.55 us (gemm_splits).  8192 x 16384 x 896: 64 tall tiles
+// those of 256-row tiles at 0.55 us (gemm_plan).  8192 x 16384 x 896: 64 tall tiles
 // 173 us, 128 flat ones 203 us.
 inline bool gemm_tall(long long M, long long N, int splits) {
     const long long cols = (N + gm::BN - 1) / gm::BN * splits;

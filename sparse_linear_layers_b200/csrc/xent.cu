@@ -35,6 +35,8 @@
 // a row's registers anywhere in them would put the row into local memory.
 #include <cuda.h>
 
+#include <cstring>
+
 #include "gemm_f16.cuh"
 #include "sbl_common.cuh"
 
@@ -447,7 +449,7 @@ __global__ void __launch_bounds__(256) xent_dx_kernel(const float* __restrict__ 
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const float c = *cmax;
     const int col = threadIdx.x % COLS, slice = threadIdx.x / COLS;
-    float4 a, b;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
     auto add = [&](const float4& u, const float4& v) {
         a.x += u.x; a.y += u.y; a.z += u.z; a.w += u.w;
         b.x += v.x; b.y += v.y; b.z += v.z; b.w += v.w;
@@ -495,25 +497,46 @@ long long piece_words(long long T, long long V) {
 // reading W and writing dW, which hides the second part's MMAs.
 bool g_parts(long long T) { return T <= kFewTokens; }
 
-// dX has few tiles (T / 512 x D / 256) and a long reduction over the words, so it
-// may be cut into parts, each with its own fp32 sums over the pieces, which
-// xent_dx_kernel adds in order.
 // With G in two parts they lie in the two CTAs' rows of one A (GemmShape::stack),
 // each with sums of its own, instead of in two A of 256 rows: half the MMAs.
 long long dx_rows(long long T) { return g_parts(T) ? 2 * gm::BM : (T + 31) / 32 * 32; }
-int dx_splits(long long T, long long D, long long V) {
-    const bool tall = T > 256;
-    const long long rows = tall ? 512 : 256, tiles = (T + rows - 1) / rows * ((D + gm::BN - 1) / gm::BN);
-    return gemm_splits(tiles, (V + gm::BK - 1) / gm::BK, (g_parts(T) ? 8.0 : 4.0) * T * D,
-                       tall ? 0.8 : g_parts(T) ? 0.45 : 0.55, 64);
-}
 
-template <class Epi, bool A_MN, bool B_MN>
-cudaError_t launch_either(const CUtensorMap& a, const CUtensorMap& b, const typename Epi::Params& p, const GemmShape& shape,
-                          unsigned* status, cudaStream_t st) {
-    return gemm_tall(shape.M, shape.N, shape.splits)
-               ? launch_gemm_f16<Epi, 1, 2, A_MN, B_MN, false, 0>(a, b, p, shape, status, st)
-               : launch_gemm_f16<Epi, 1, 1, A_MN, B_MN, false, 0>(a, b, p, shape, status, st);
+// dX has few tiles (T / 512 x D / 256) and a long reduction over the words, so it
+// may be cut into parts, each with its own fp32 sums over the pieces, which
+// xent_dx_kernel adds in order.  dX and dW of a piece run as one launch where one
+// height of tiles suits both (8192 x 128000 x 896: loss and gradients 6.43 ms
+// together, 6.73 apart; 4112 x 2066 x 2944, tall dX tiles and flat dW ones: both
+// products 99 us apart, 121 together).  (The plan is
+// of both also when one is wanted: the same bits.)
+struct GradPlan {
+    int splits, lead;
+    bool together, tall_x, tall_w;
+};
+GradPlan grad_plan(long long T, long long D, long long V) {
+    const long long words = piece_words(T, V) < V ? piece_words(T, V) : V, cols = (D + gm::BN - 1) / gm::BN;
+    const double bytes = (g_parts(T) ? 8.0 : 4.0) * T * D;
+    const GemmWork none{0, 1, 0.0, 0.0, 0.0, 1};
+    auto x = [&](bool tall) {
+        return GemmWork{(T + (tall ? 511 : 255)) / (tall ? 512 : 256) * cols, (words + gm::BK - 1) / gm::BK,
+                        tall ? 0.8 : g_parts(T) ? 0.52 : 0.55, tall ? 2.5 : 1.0, bytes, 64};
+    };
+    auto w = [&](bool tall) {
+        return GemmWork{(words + (tall ? 511 : 255)) / (tall ? 512 : 256) * cols, (T + gm::BK - 1) / gm::BK,
+                        tall || g_parts(T) ? 0.8 : 0.55, tall ? 2.5 : 1.0, 0.0, 1};
+    };
+    GemmPlan best = gemm_plan(x(false), w(false));
+    GradPlan plan{best.splits1, best.lead, true, false, false};
+    if (g_parts(T)) return plan;
+    const GemmPlan tall = gemm_plan(x(true), w(true));
+    if (tall.us < best.us) {
+        best = tall;
+        plan = GradPlan{best.splits1, best.lead, true, true, true};
+    }
+    const GemmPlan xs[2] = {gemm_plan(x(false), none), gemm_plan(x(true), none)};
+    const GemmPlan ws[2] = {gemm_plan(w(false), none), gemm_plan(w(true), none)};
+    const bool tx = xs[1].us < xs[0].us, tw = ws[1].us < ws[0].us;
+    if (xs[tx].us + ws[tw].us + 3.0 < best.us) plan = GradPlan{xs[tx].splits1, 0, false, tx, tw};
+    return plan;
 }
 
 }  // namespace
@@ -523,7 +546,7 @@ size_t xent_workspace_bytes(long long T, long long V) {
 }
 
 size_t xent_backward_workspace_bytes(long long T, long long D, long long V, int need_dx) {
-    return 256 + (need_dx ? round256(static_cast<size_t>(dx_splits(T, D, V)) * dx_rows(T) * D * sizeof(float)) : 0) +
+    return 256 + (need_dx ? round256(static_cast<size_t>(grad_plan(T, D, V).splits) * dx_rows(T) * D * sizeof(float)) : 0) +
            round256(static_cast<size_t>(T) * piece_words(T, V) * (g_parts(T) ? 4 : 2));
 }
 
@@ -567,7 +590,8 @@ cudaError_t launch_xent(const uint16_t* x, long long T, long long D, const uint1
 cudaError_t launch_xent_backward(const float* dloss, const uint16_t* x, long long T, long long D, const uint16_t* w,
                                  long long V, const long long* target, long long ignore, const float* lse, uint16_t* dx,
                                  uint16_t* dw, void* ws, unsigned* status, int num_sms, cudaStream_t st) {
-    const int splits = dx_splits(T, D, V);
+    const GradPlan plan = grad_plan(T, D, V);
+    const int splits = plan.splits;
     const long long rows = dx_rows(T);
     uint8_t* at = static_cast<uint8_t*>(ws);
     float* cmax = reinterpret_cast<float*>(at);
@@ -608,36 +632,50 @@ cudaError_t launch_xent_backward(const float* dloss, const uint16_t* x, long lon
                 !gemm_result_bf16(&p.g, g, T, n, pitch))
                 return cudaErrorInvalidValue;
             const GemmShape shape{Ti, ni, Di, 0, 8, 1, 0, gm::BM, 0, 0};
-            e = launch_either<GradTile, false, false>(xk, wk, p, shape, status, st);
+            e = gemm_tall(T, n, 1) ? launch_gemm_f16<GradTile, 1, 2, false, false, false, 0>(xk, wk, p, shape, status, st)
+                                   : launch_gemm_f16<GradTile, 1, 1, false, false, false, 0>(xk, wk, p, shape, status, st);
         }
         if (e != cudaSuccess) return e;
         const long long g_cols = parts ? piece + n : n;
         const int low = static_cast<int>(piece);  // columns from a part to the next
+        using DxJob = GemmJob<SumF32, 1, false, true>;
+        using DwJob = GemmJob<ScaledBf16, 1, true, true>;
+        using DwParts = GemmJob<ScaledBf16, 2, true, true>;
+        GemmArgs<DxJob> gx;
+        GemmArgs<DwJob> gw;
+        memset(&gx, 0, sizeof(gx));
+        memset(&gw, 0, sizeof(gw));
         if (dx) {
-            CUtensorMap gk, wn;
-            SumF32::Params sp;
-            sp.add = v0 > 0;
-            sp.rows = Ti;
-            sp.row_mask = parts ? gm::BM - 1 : -1;
-            if (!gemm_operand(&gk, false, false, g, T, g_cols, pitch, gemm_a_box(T)) || !gemm_operand(&wn, false, true, wp, n, D, D) ||
-                !gemm_result_f32(&sp.out, dx32, splits * rows, D))
+            gx.p.add = v0 > 0;
+            gx.p.rows = Ti;
+            gx.p.row_mask = parts ? gm::BM - 1 : -1;
+            if (!gemm_operand(&gx.a, false, false, g, T, g_cols, pitch, gemm_a_box(T)) ||
+                !gemm_operand(&gx.b, false, true, wp, n, D, D) || !gemm_result_f32(&gx.p.out, dx32, splits * rows, D))
                 return cudaErrorInvalidValue;
-            const GemmShape shape{Ti, Di, ni, 0, d_panel, splits, static_cast<int>(rows), gemm_a_box(T), 0, parts ? low : 0};
-            e = parts ? launch_gemm_f16<SumF32, 1, 1, false, true, false, 0>(gk, wn, sp, shape, status, st)
-                      : launch_either<SumF32, false, true>(gk, wn, sp, shape, status, st);
-            if (e != cudaSuccess) return e;
+            gx.shape = GemmShape{Ti, Di, ni, 0, d_panel, splits, static_cast<int>(rows), gemm_a_box(T), 0, parts ? low : 0};
         }
         if (dw) {
-            CUtensorMap gm_, xn;
-            ScaledBf16::Params bp;
-            bp.cmax = cmax;
-            if (!gemm_operand(&gm_, false, true, g, T, g_cols, pitch) || !gemm_operand(&xn, false, true, x, T, D, D) ||
-                !gemm_result_bf16(&bp.out, dw + v0 * D, n, D, D))
+            gw.p.cmax = cmax;
+            if (!gemm_operand(&gw.a, false, true, g, T, g_cols, pitch) || !gemm_operand(&gw.b, false, true, x, T, D, D) ||
+                !gemm_result_bf16(&gw.p.out, dw + v0 * D, n, D, D))
                 return cudaErrorInvalidValue;
-            const GemmShape shape{ni, Di, Ti, low, d_panel, 1, 0, gm::BM, 0, 0};
-            e = parts ? launch_gemm_f16<ScaledBf16, 2, 1, true, true, false, 0>(gm_, xn, bp, shape, status, st)
-                      : launch_either<ScaledBf16, true, true>(gm_, xn, bp, shape, status, st);
+            gw.shape = GemmShape{ni, Di, Ti, low, d_panel, 1, 0, gm::BM, plan.lead, 0};
         }
+        const GemmArgs<DwParts> gp{gw.a, gw.b, gw.p, gw.shape};
+        const GemmArgs<GemmNoJob> none{};
+        if (dx && dw && plan.together) {
+            e = parts         ? launch_gemm_jobs<DxJob, DwParts, 1, false, 0>(gx, gp, status, st)
+                : plan.tall_x ? launch_gemm_jobs<DxJob, DwJob, 2, false, 0>(gx, gw, status, st)
+                              : launch_gemm_jobs<DxJob, DwJob, 1, false, 0>(gx, gw, status, st);
+            continue;
+        }
+        if (dx)
+            e = plan.tall_x ? launch_gemm_jobs<DxJob, GemmNoJob, 2, false, 0>(gx, none, status, st)
+                            : launch_gemm_jobs<DxJob, GemmNoJob, 1, false, 0>(gx, none, status, st);
+        if (dw && e == cudaSuccess)
+            e = parts         ? launch_gemm_jobs<DwParts, GemmNoJob, 1, false, 0>(gp, none, status, st)
+                : plan.tall_w ? launch_gemm_jobs<DwJob, GemmNoJob, 2, false, 0>(gw, none, status, st)
+                              : launch_gemm_jobs<DwJob, GemmNoJob, 1, false, 0>(gw, none, status, st);
     }
     if (e == cudaSuccess && dx) {
         const int sums = parts ? 2 * splits : splits;
