@@ -919,12 +919,25 @@ FfnSpace ffn_space(long long T, long long K, long long F) {
 // instead of in two A of 256 rows: half the MMAs.
 bool dx_stacks(long long T) { return T <= gm::BM; }
 // (The plan is of both gradients also when one is wanted: the same bits.)
-GemmPlan grad_plan(long long T, long long K, long long Fp) {
+GemmPlan make_grad_plan(long long T, long long K, long long Fp) {
     const long long cols = (K + gm::BN - 1) / gm::BN;
     const GemmWork dx{(T + 255) / 256 * cols, 2 * Fp / gm::BK, dx_stacks(T) ? 0.45 : 0.8, 1.0,
                       (dx_stacks(T) ? 8.0 : 4.0) * T * K, 32};
     const GemmWork dw{(2 * Fp + 255) / 256 * cols, (T + gm::BK - 1) / gm::BK, 0.8, 1.0, 8.0 * Fp * K, 32};
     return gemm_plan(dx, dw);
+}
+// Asked for three times a call (workspace, its check, the launch) at 1 to 2 us: the
+// thread's last sizes are remembered.
+GemmPlan grad_plan(long long T, long long K, long long Fp) {
+    thread_local long long sizes[3] = {};
+    thread_local GemmPlan plan = {};
+    if (sizes[0] != T || sizes[1] != K || sizes[2] != Fp) {
+        plan = make_grad_plan(T, K, Fp);
+        sizes[0] = T;
+        sizes[1] = K;
+        sizes[2] = Fp;
+    }
+    return plan;
 }
 
 struct FfnBwdSpace {

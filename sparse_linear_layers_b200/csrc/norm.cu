@@ -864,11 +864,13 @@ cudaError_t bwd(const void* dy, const void* x, const float* w, const float* mean
     cudaError_t e = cudaSuccess;
     StreamChoice c;
     if (stream_choice(T, K, sizeof(E), num_sms, c)) {
-        auto kern = c.nc == 1   ? (c.r == 2 ? norm_bwd_stream_kernel<Row, LAYER, 1, 2> : norm_bwd_stream_kernel<Row, LAYER, 1, 1>)
-                    : c.nc == 2 ? (c.r == 2 ? norm_bwd_stream_kernel<Row, LAYER, 2, 2> : norm_bwd_stream_kernel<Row, LAYER, 2, 1>)
-                                : (c.r == 2 ? norm_bwd_stream_kernel<Row, LAYER, 4, 2> : norm_bwd_stream_kernel<Row, LAYER, 4, 1>);
-        static bool allowed[6][64] = {};
-        e = allow_ring(kern, allowed[(c.nc == 4 ? 4 : 2 * c.nc - 2) + c.r - 1]);
+        // rows of up to 512 columns always fit two at a time
+        auto kern = c.nc == 1   ? norm_bwd_stream_kernel<Row, LAYER, 1, 2>
+                    : c.nc == 2 ? norm_bwd_stream_kernel<Row, LAYER, 2, 2>
+                    : c.r == 2  ? norm_bwd_stream_kernel<Row, LAYER, 4, 2>
+                                : norm_bwd_stream_kernel<Row, LAYER, 4, 1>;
+        static bool allowed[4][64] = {};
+        e = allow_ring(kern, allowed[c.nc < 4 ? c.nc - 1 : 1 + c.r]);
         if (e == cudaSuccess)
             e = pdl_launch(kern, dim3(P), dim3((c.plan.wpr * c.plan.groups + 1) * 32), c.smem, st, dyp, xp, w, mean, rstd, T, Ki,
                            c.plan, dxp, part_or_null, status);

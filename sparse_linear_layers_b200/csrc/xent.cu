@@ -513,7 +513,7 @@ struct GradPlan {
     int splits, lead;
     bool together, tall_x, tall_w;
 };
-GradPlan grad_plan(long long T, long long D, long long V) {
+GradPlan make_grad_plan(long long T, long long D, long long V) {
     const long long words = piece_words(T, V) < V ? piece_words(T, V) : V, cols = (D + gm::BN - 1) / gm::BN;
     const double bytes = (g_parts(T) ? 8.0 : 4.0) * T * D;
     const GemmWork none{0, 1, 0.0, 0.0, 0.0, 1};
@@ -537,6 +537,19 @@ GradPlan grad_plan(long long T, long long D, long long V) {
     const GemmPlan ws[2] = {gemm_plan(w(false), none), gemm_plan(w(true), none)};
     const bool tx = xs[1].us < xs[0].us, tw = ws[1].us < ws[0].us;
     if (xs[tx].us + ws[tw].us + 3.0 < best.us) plan = GradPlan{xs[tx].splits1, 0, false, tx, tw};
+    return plan;
+}
+// Asked for three times a call (workspace, its check, the launch) at 2 us: the
+// thread's last sizes are remembered.
+GradPlan grad_plan(long long T, long long D, long long V) {
+    thread_local long long sizes[3] = {};
+    thread_local GradPlan plan = {};
+    if (sizes[0] != T || sizes[1] != D || sizes[2] != V) {
+        plan = make_grad_plan(T, D, V);
+        sizes[0] = T;
+        sizes[1] = D;
+        sizes[2] = V;
+    }
     return plan;
 }
 

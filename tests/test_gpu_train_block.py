@@ -216,6 +216,46 @@ def test_step_in_a_graph(sbl):
     assert sbl.sbl_device_status() == 0
 
 
+def test_modules_in_a_graph(sbl):
+    """Forward and backward of the modules captured as a training loop captures them:
+    warmed up on a side stream, no eager graph of the same parameters alive."""
+    torch.manual_seed(9)
+    T, D, F, V = 150, 128, 160, 900
+    norm = sbl.SparseBitNorm(D, kind="layer", bias=True, device="cuda")
+    ffn = sbl.SparseBitFeedForward(D, F, 3, 4, device="cuda", check_finite=False)
+    head = sbl.LinearCrossEntropy(D, V, reduction="sum", device="cuda")
+    params = [*norm.parameters(), *ffn.parameters(), *head.parameters()]
+
+    def step(x, t):
+        for p in params:
+            p.grad = None
+        loss = head(x + ffn(norm(x)), t)
+        loss.backward()
+        return loss.detach()
+
+    new = lambda: (torch.randn(T, D, device="cuda"), torch.randint(0, V, (T,), device="cuda"))
+    x, t = new()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            step(x, t)
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        loss = step(x, t)
+    grads = [p.grad for p in params]
+    x2, t2 = new()
+    x.copy_(x2)
+    t.copy_(t2)
+    g.replay()
+    torch.cuda.synchronize()
+    got = [loss.clone(), *(v.clone() for v in grads)]
+    want = step(x2, t2)
+    for a, b in zip(got, [want, *(p.grad for p in params)]):
+        assert torch.equal(a, b)
+
+
 def test_first_use_inside_a_capture():
     """A process whose very first calls of the operators are captured."""
     import os
