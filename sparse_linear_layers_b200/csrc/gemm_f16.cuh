@@ -16,8 +16,8 @@
 // MH = 2: tiles of 512 x 256, both buffers one tile's (its upper and lower 256
 // rows), so B is loaded once for twice the rows.  What feeds the MMAs bounds
 // this GEMM: L2 delivers about 9 TB/s to the SMs whatever the kernel (measured on
-// four of them), 60 bytes/ns to one SM, also when 15 pairs run alone; 7.8 KB per MFLOP of a 256 x 256 tile and 5.9 KB of a 512 x 256
-// one.  The MMAs of the next tile wait until the epilogue has read a half, while
+// four of them), 60 bytes/ns to one SM, also when 15 pairs run alone; a 256 x 256
+// tile takes 7.8 KB per MFLOP and a 512 x 256 one 5.9 KB.  The MMAs of the next tile wait until the epilogue has read a half, while
 // the loads run on for four stages; sixteen epilogue warps read both halves at
 // once to keep that wait short.  (Letting the upper half's MMAs run ahead
 // through those stages made the whole 3% slower: their stages come back later.)
@@ -34,8 +34,9 @@
 //
 // Warps: 8 MH epilogue (warp w: TMEM lanes 32 (w % 4) .. + 31, columns
 // 128 (w / 4 % 2) .. + 127 of buffer w / 8), one TMA producer, one for TMEM
-// allocation and, in the even CTA, MMA issue.  Every wait is bounded; a CTA that gives up records a
-// timeout, lets its loads land and its MMAs finish (bounded) and exits.
+// allocation and, in the even CTA, MMA issue.  Every wait is bounded; a CTA that
+// gives up records a timeout, lets its loads land and its MMAs finish (bounded) and
+// exits.
 #pragma once
 
 #include <cuda.h>
@@ -211,6 +212,7 @@ __device__ __forceinline__ void put_f32(GemmTile& t, int k, const float (&v)[32]
 //   struct Params (a kernel argument, may hold tensor maps), static prefetch(const Params&),
 //   Epi(const Params&), begin(const GemmTile&), slice(GemmTile&, int k, float (&v)[32])
 //   for columns col0 + 32 k .. + 31 of the thread's row (k = 0 .. BN_ / 64 - 1 in order), end(const GemmTile&).
+
 // A product of a launch.
 template <class Epi_, int NA_, bool A_MN_, bool B_MN_>
 struct GemmJob {
