@@ -359,8 +359,10 @@ sbl_status sbl_ffn_gated(const uint16_t* x_bf16, int64_t T, int64_t K, const uin
  * Tensor-core sums of fp16 parts, fp32 accumulation: with v = (dg | du) * scale /
  * s_tok, each output is within (n / 128 + 80) * 2^-24 * sum |terms| of the sum
  * over these fp32 v (n the reduction length, 2 F or T), plus 2^-38 of the
- * largest |v| of each token times what it multiplies.  The same inputs give the same bits.  Other arguments, limits
- * and errors as the forward.
+ * largest |v| of each token times what it multiplies.  (The terms of dW of tokens whose
+ * largest |v| is below 2^-32 of all tokens' largest are summed on CUDA cores, in
+ * fp32, which takes longer where there are many.)  The same inputs give the same bits.
+ * Other arguments, limits and errors as the forward.
  */
 size_t sbl_ffn_gated_backward_workspace_bytes(int64_t T, int64_t K, int64_t F, int need_dx, int need_dw);
 sbl_status sbl_ffn_gated_backward(const float* dh, const uint16_t* x_bf16, int64_t T, int64_t K,

@@ -31,8 +31,11 @@
 // ffn_operands_kernel splits v, scaled by a power of two 2^-er[t] that brings
 // the token's largest value to [2^14, 2^15), into two fp16 parts (11 + 11
 // significant bits; what they drop is at most 2^-22 of v plus 2^-39 of the
-// token's largest |v|), writes the codes as fp16, and x_q * 2^(er[t] - max er + 8) as fp16
-// (exact down to 2^-32 of the largest token).  Two products of those in one launch (gemm_f16.cuh,
+// token's largest |v|), writes the codes as fp16, and x_q * 2^(er[t] - max er + 8) as fp16,
+// exact down to er = max er - 32.  Tokens below that (their largest |v| under 2^-32 of
+// all tokens' largest) would lose bits of x_q, then all of it, and with it the
+// gradient of a hidden unit that only they reach: they are left out of dW's product and
+// counted, and ffn_far_kernel adds their terms in fp32.  Two products of those in one launch (gemm_f16.cuh,
 // fp16 operands, both parts summed, segments of 4 k-blocks promoted to
 // round-to-nearest sums) give dX and dW: at 4096 x 2048 -> 7168 0.57 ms, the tensor
 // pipe 95% busy (0.60 as two launches).  Two parts instead of three bf16 ones
@@ -717,11 +720,15 @@ __global__ void __launch_bounds__(256)
 // ---------------------------------------------------------------- backward operands
 // er: the power of two that a token's v is divided by.  Its largest |v|, with
 // exponent e, lands in [2^14, 2^15) (a token below 2^-112 keeps what 2^126 gives it).
+// An infinite v counts as 2^128: it stays infinite, and its token above all others.
 __device__ __forceinline__ int row_exponent(unsigned bits) {
-    if (bits >= 0x7F800000u) return 0;  // NaN or Inf: passed on unscaled
     const int e = static_cast<int>(bits >> 23) - 127;
     return max(e - 14, -126);
 }
+// Power of two that x_q of a token takes in dW's product.
+__device__ __forceinline__ int token_shift(unsigned bits, int top) { return row_exponent(bits) - top + 8; }
+// Whether fp16 holds x_q times that: multiples of 2^-24.
+__device__ __forceinline__ bool token_far(unsigned bits, int top) { return bits != 0u && token_shift(bits, top) < -24; }
 __device__ __forceinline__ float pow2f(int e) { return __uint_as_float(static_cast<unsigned>(e + 127) << 23); }
 
 struct FfnOperands {
@@ -734,6 +741,7 @@ struct FfnOperands {
     __half* parts;             // [T, 2 * 2 Fp]: high parts, low parts
     __half* codes;             // [2 Fp, K] or NULL (no dX)
     __half* xs;                // [T, K] or NULL (no dW)
+    unsigned* far;             // tokens left out of xs
     int T, K, F, Fp;
     int split_blocks, code_blocks, x_blocks;
 };
@@ -795,13 +803,16 @@ __global__ void __launch_bounds__(256) ffn_operands_kernel(const FfnOperands q) 
         return;
     }
     block -= q.code_blocks;
-    // 16 activations of one token: x_q * 2^(er - max er + 8), back in column order
+    // 16 activations of one token: x_q * 2^(er - max er + 8), back in column order; zeros
+    // for a token without a gradient and for one that ffn_far_kernel adds
     const long long n = static_cast<long long>(q.T) * words;
     const int top = row_exponent(*q.all_max);
     for (long long i = block * 256ll + threadIdx.x; i < n; i += q.x_blocks * 256ll) {
         const long long t = i / words;
-        const int e = row_exponent(__ldg(q.row_max + t)) - top + 8;
-        const float s = e < -40 ? 0.f : pow2f(e);  // 127 * 2^-40 is below half of fp16's smallest step
+        const unsigned bits = __ldg(q.row_max + t);
+        const int e = token_shift(bits, top);
+        const float s = e < -24 ? 0.f : pow2f(e);
+        if (i == t * words && token_far(bits, top)) atomicAdd(q.far, 1u);
         const uint4 u = __ldg(reinterpret_cast<const uint4*>(q.xq) + i);
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};  // even 0-6, odd 1-7, even 8-14, odd 9-15
         uint32_t o[8];
@@ -858,6 +869,120 @@ __global__ void __launch_bounds__(256) ffn_sum_kernel(const float4* __restrict__
             a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w;
         }
         out[i] = a;
+    }
+}
+
+// dW's terms of the far tokens (token_far), added to the gradients that the product has
+// written: dW[f, k] += (1 / scale[f]) * sum_t v[t, f] * x_q[t, k], v from fp32 memory.
+// Most calls have none and the kernel ends at once.  Tiles of 64 units x 64 k, 4 x 4
+// of them a thread; the tokens in order, added in groups of 32, 32 groups of 1024:
+// at most 32 + 32 + T / 1024 roundings of a sum.  On CUDA cores: at 4096 tokens, 2048 ->
+// 7168, the backward takes 0.84 ms with no far token, 1.14 with one, 1.41 with 64 and
+// 19 with all but one.
+struct FfnFar {
+    const unsigned* far;
+    const unsigned* row_max;
+    const unsigned* all_max;
+    const float* v;            // [T, 2 Fp]
+    const int8_t* xq;          // [T, K], pairing order
+    const float* scale_g;
+    const float* scale_u;
+    float* dwg;                // each [F, K] or NULL
+    float* dwu;
+    int T, K, F, Fp, ternary;
+};
+__global__ void __launch_bounds__(256) ffn_far_kernel(const FfnFar q) {
+    constexpr int TILE = 64, GROUP = 32;
+    __shared__ int list[256];
+    __shared__ int count[8];
+    __shared__ float sv[GROUP][TILE];
+    __shared__ float sx[GROUP][TILE];
+    asm volatile("griddepcontrol.launch_dependents;");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (*q.far == 0u) return;
+    const int top = row_exponent(*q.all_max), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int ft = (q.F + TILE - 1) / TILE, kt = (q.K + TILE - 1) / TILE;
+    const long long per_matrix = static_cast<long long>(ft) * kt;
+    const long long tiles = per_matrix * ((q.dwg != nullptr) + (q.dwu != nullptr));
+    const int f4 = tid / 16 * 4, k4 = tid % 16 * 4;  // this thread's corner of the tile
+    for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+        const bool up = !q.dwg || tile >= per_matrix;
+        const long long at = tile % per_matrix;
+        const int f0 = static_cast<int>(at / kt) * TILE, k0 = static_cast<int>(at % kt) * TILE;
+        float sum[4][4], mid[4][4];
+#pragma unroll
+        for (int a = 0; a < 4; ++a)
+#pragma unroll
+            for (int b = 0; b < 4; ++b) sum[a][b] = mid[a][b] = 0.f;
+        int groups = 0;
+        for (int t0 = 0; t0 < q.T; t0 += 256) {
+            // the far ones of 256 tokens, in order
+            const bool mine = t0 + tid < q.T && token_far(__ldg(q.row_max + t0 + tid), top);
+            const unsigned votes = __ballot_sync(0xFFFFFFFFu, mine);
+            __syncthreads();  // the list has been read
+            if (lane == 0) count[warp] = __popc(votes);
+            __syncthreads();
+            int before = 0, n = 0;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) {
+                before += w < warp ? count[w] : 0;
+                n += count[w];
+            }
+            if (mine) list[before + __popc(votes & ((1u << lane) - 1u))] = t0 + tid;
+            for (int g0 = 0; g0 < n; g0 += GROUP) {
+                const int m = n - g0 < GROUP ? n - g0 : GROUP;
+                __syncthreads();  // the list is complete; the previous group has been read
+                for (int i = tid; i < m * TILE; i += 256) {
+                    const int j = i / TILE, c = i % TILE, f = f0 + c, k = k0 + c;
+                    const long long t = list[g0 + j];
+                    sv[j][c] = f < q.F ? __ldg(q.v + t * 2 * q.Fp + (up ? q.Fp : 0) + f) : 0.f;
+                    // columns 0, 2, 4, 6, 1, 3, 5, 7 of each 8: the pairing order
+                    const int at8 = (k & 1) * 4 + ((k & 7) >> 1);
+                    sx[j][c] = k < q.K ? static_cast<float>(q.xq[t * q.K + (k & ~7) + at8]) : 0.f;
+                }
+                __syncthreads();
+                float part[4][4];
+#pragma unroll
+                for (int a = 0; a < 4; ++a)
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) part[a][b] = 0.f;
+                for (int j = 0; j < m; ++j) {
+                    const float4 v = *reinterpret_cast<const float4*>(&sv[j][f4]);
+                    const float4 x = *reinterpret_cast<const float4*>(&sx[j][k4]);
+                    const float va[4] = {v.x, v.y, v.z, v.w}, xa[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                    for (int a = 0; a < 4; ++a)
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) part[a][b] = fmaf(va[a], xa[b], part[a][b]);
+                }
+                const bool full = ++groups == 32;
+#pragma unroll
+                for (int a = 0; a < 4; ++a)
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        mid[a][b] += part[a][b];
+                        if (full) {
+                            sum[a][b] += mid[a][b];
+                            mid[a][b] = 0.f;
+                        }
+                    }
+                if (full) groups = 0;
+            }
+        }
+        float* const out = up ? q.dwu : q.dwg;
+        const float* const scale = up ? q.scale_u : q.scale_g;
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+            const int f = f0 + f4 + a;
+            if (f >= q.F) break;
+            const float s = q.ternary ? 1.0f : __frcp_rn(__ldg(scale + f));
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+                if (k0 + k4 + b < q.K) {
+                    float* const d = out + static_cast<size_t>(f) * q.K + k0 + k4 + b;
+                    *d += (sum[a][b] + mid[a][b]) * s;
+                }
+        }
     }
 }
 
@@ -950,7 +1075,7 @@ FfnBwdSpace ffn_bwd_space(long long T, long long K, long long F, int need_dx, in
     FfnBwdSpace s;
     s.fwd = ffn_space(T, K, F);
     s.Fp = (F + 127) / 128 * 128;
-    s.nmax16 = (T + 1 + 3) / 4;  // row maxima and the maximum of all, in 16-byte units
+    s.nmax16 = (T + 2 + 3) / 4;  // row maxima, the maximum of all, the far tokens' count: 16-byte units
     s.maxima = s.fwd.end;
     s.v = s.maxima + round256(static_cast<size_t>(s.nmax16) * 16);
     s.parts = s.v + round256(static_cast<size_t>(T) * 2 * s.Fp * 4);
@@ -1144,6 +1269,7 @@ cudaError_t launch_ffn_backward(const float* dh, const uint16_t* x, long long T,
     float* const v = reinterpret_cast<float*>(base + sp.v);
     unsigned* const row_max = reinterpret_cast<unsigned*>(base + sp.maxima);
     unsigned* const all_max = row_max + T;
+    unsigned* const far = all_max + 1;
     const int8_t* const xq = reinterpret_cast<const int8_t*>(base + sp.fwd.xq);
     const float* const s_tok = q.s_tok;
     q.all_max = all_max;
@@ -1163,6 +1289,7 @@ cudaError_t launch_ffn_backward(const float* dh, const uint16_t* x, long long T,
     o.xq = xq;
     o.codes = codes;
     o.xs = xs;
+    o.far = far;
     o.K = Ki;
     o.F = Fi;
     o.Fp = Fp;
@@ -1244,6 +1371,11 @@ cudaError_t launch_ffn_backward(const float* dh, const uint16_t* x, long long T,
         e = stack ? join(dx_sums, 2 * dx_splits, gm::BM, T, dx) : join(dx_sums, dx_splits, sp.dx_rows, T, dx);
     if (e == cudaSuccess && dw_splits > 1 && dwg) e = join(dw_sums, dw_splits, 2 * sp.Fp, F, dwg);
     if (e == cudaSuccess && dw_splits > 1 && dwu) e = join(dw_sums + sp.Fp * K, dw_splits, 2 * sp.Fp, F, dwu);
+    if (e == cudaSuccess && need_dw) {
+        const FfnFar q_far{far, row_max, all_max, v, xq, scale_g, scale_u, dwg, dwu, Ti, Ki, Fi, Fp, ternary};
+        const long long tiles = ((F + 63) / 64) * ((K + 63) / 64) * ((dwg != nullptr) + (dwu != nullptr)), most = 2ll * num_sms;
+        e = pdl_launch(ffn_far_kernel, dim3(static_cast<unsigned>(tiles < most ? tiles : most)), dim3(256), 0, st, q_far);
+    }
     return e;
 }
 

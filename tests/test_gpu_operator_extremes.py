@@ -1,0 +1,50 @@
+"""Norms, the gated feed-forward block, the cross entropy and their modules where
+values, sizes or callers lie far apart.
+
+The 64-bit references and bounds are those of the operators' own test files unless
+a test states another."""
+import pytest
+import torch
+
+import test_gpu_cross_entropy as ce
+from test_gpu_ffn_gated import Case
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def sbl():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import sparse_linear_layers_b200 as m
+    return m
+
+
+_check = ce._check  # an output that holds NaN does not pass
+
+
+# ---------------------------------------------------------------- the feed-forward block
+@pytest.mark.parametrize("T,K,F", [(5, 80, 40), (40, 256, 130), (300, 272, 260), (1500, 896, 150), (3001, 64, 100)])
+@pytest.mark.parametrize("act,ternary", [("silu", False), ("relu2", True)])
+def test_gradients_of_tokens_far_apart(sbl, T, K, F, act, ternary):
+    """Tokens whose gradients differ by up to 2^-75, and hidden units that only the
+    small ones reach: the floor of each token is 2^-38 of its own largest v."""
+    c = Case(sbl, T, K, F, nm=[(2, 4), (3, 4), (6, 8), (4, 8)][T % 4], act=act, seed=T + F)
+    g = torch.Generator().manual_seed(T)
+    power = torch.tensor([0, 20, 30, 33, 34, 41, 50, 75])[torch.randint(0, 8, (T, 1), generator=g)]
+    power[0], power[-1] = 0, 50
+    dh = torch.randn(T, F, generator=g) * 2.0 ** -power.double()
+    dh[:, F // 2:] *= power >= 33
+    dh[:, F - 7:] *= power >= 50
+    dh = dh.float()
+    refs = c.grads(dh, ternary)
+    got = sbl.sbl_ffn_gated_backward(dh.cuda(), c.x, c.gate, c.up, act=act, dw_ternary=ternary)
+    for name, v, (r, b) in zip(("dx", "dgate", "dup"), got, refs):
+        # 2^-126 times an activation of at most 127 / s: v itself near fp32's end
+        _check(name, v, r, b - 1e-37 + 1e-34)
+    for need in ((True, False, False), (False, True, False), (False, False, True)):
+        one = sbl.sbl_ffn_gated_backward(dh.cuda(), c.x, c.gate, c.up, act=act, dw_ternary=ternary, need_dx=need[0],
+                                         need_dgate=need[1], need_dup=need[2])
+        for o, v, n in zip(one, got, need):
+            assert (o is not None) == n and (o is None or torch.equal(o, v))
+    assert sbl.sbl_device_status() == 0
