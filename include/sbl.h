@@ -388,8 +388,8 @@ sbl_status sbl_ffn_gated_backward(const float* dh, const uint16_t* x_bf16, int64
  *   workspace sbl_linear_cross_entropy_workspace_bytes(T, V) bytes, 256-byte
  *             aligned (8 bytes per token and 128 words; 32 words up to 128 tokens).
  * D % 16 == 0; T, D, V up to 2^24 and T * V below 2^46, else SBL_ERR_UNSUPPORTED.  x and W finite
- * (NaN or Inf in the row of a token reaches that token's loss and lse alone; an
- * ignored token's loss stays 0).  Asynchronous on `stream`.
+ * (NaN or Inf in the row of a token reaches that token's loss and lse alone, NaN in
+ * a row of W every token's; an ignored token's loss stays 0).  Asynchronous on `stream`.
  */
 size_t sbl_linear_cross_entropy_workspace_bytes(int64_t T, int64_t V);
 sbl_status sbl_linear_cross_entropy(const uint16_t* x_bf16, int64_t T, int64_t D, const uint16_t* w_bf16, int64_t V,

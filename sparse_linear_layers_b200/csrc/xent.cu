@@ -102,7 +102,8 @@ struct LsePart {
         // (z - m) log2 e, not z log2 e - m log2 e in one step: the maximum's term has to
         // be exactly 1, or a likely word's small loss is the rounding of m log2 e
         const float2 l2 = both(kLog2e), less = both(-m);
-        float2 s2[2] = {make_float2(mx == -INFINITY ? 0.f : sum * exp2_fast((mx - m) * kLog2e), 0.f), make_float2(0.f, 0.f)};
+        // by the sum, not by mx == -inf: 32 NaN logits leave mx there (max drops NaN) and a NaN sum
+        float2 s2[2] = {make_float2(sum == 0.f ? 0.f : sum * exp2_fast((mx - m) * kLog2e), 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             const float2 e = mul2(add2(make_float2(v[2 * i], v[2 * i + 1]), less), l2);

@@ -48,3 +48,18 @@ def test_gradients_of_tokens_far_apart(sbl, T, K, F, act, ternary):
         for o, v, n in zip(one, got, need):
             assert (o is not None) == n and (o is None or torch.equal(o, v))
     assert sbl.sbl_device_status() == 0
+
+
+# ---------------------------------------------------------------- the cross entropy
+@pytest.mark.parametrize("T", [9, 128, 200, 300, 1000])
+@pytest.mark.parametrize("words", [(0, 32), (128, 192), (0, 128), (290, 300), (480, 513)])
+def test_nan_words_reach_every_loss(sbl, T, words):
+    """Rows of the vocabulary that hold NaN: every token has such a logit."""
+    x, w, t = (v.cuda() for v in ce._inputs(T, 64, 513, seed=7))
+    t = torch.where(t == -100, 200, t)
+    t[1] = -100
+    w[words[0]:words[1]] = float("nan")
+    loss, lse = sbl.sbl_linear_cross_entropy(x, w, t)
+    assert torch.isnan(lse).all() and loss[1] == 0
+    loss[1] = float("nan")
+    assert torch.isnan(loss).all()
