@@ -407,7 +407,8 @@ sbl_status sbl_linear_cross_entropy(const uint16_t* x_bf16, int64_t T, int64_t D
  *   workspace sbl_linear_cross_entropy_backward_workspace_bytes(T, D, V, dx != NULL)
  *             bytes, 256-byte aligned (at most 512 MB for the gradient of one
  *             piece of the logits, more only for T > 2^17, and fp32 sums of dx).
- * The logits are computed again, one piece of the vocabulary at a time.  G is
+ * The logits are computed again, to the forward's bits, one piece of the vocabulary at
+ * a time.  G is
  * rounded to bf16 for the tensor cores (relative to max |dloss|, so a uniform
  * dloss is exact); sums are fp32, and dx and dw are rounded once.  The same
  * inputs give the same bits.  Limits and errors as the forward; a target

@@ -52,6 +52,11 @@ constexpr int kLogitSegment = 16;
 // Up to 256 tokens, whose time is W's way from memory, segments of 2: over few
 // losses, some of them small, the sum's error shows (a token: 1e-6 of its loss).
 constexpr int kFewSegment = 2;
+// The backward's logits are summed in the same segments, so that they are the ones
+// that lse is of, bit for bit.  With a sum of its own in one piece a likely word's
+// G = p - 1, which may be 1e-6, was off by 2e-5 at D = 2048 and 3e-4 at 16384; so by
+// 5e-7 at both (fp32 products and log-sum-exp: 4e-7).  It costs the tall tiles above
+// D = 1024: loss and gradients of 4096 x 32000 x 2048 1.54 ms instead of 1.48.
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -128,9 +133,9 @@ struct GradInputs {
     long long ignore, v0;
     int T, V, n;  // n: words of the piece
 };
-// -lse log2 e and dloss / c of a token; d stays 0 for one without a gradient.
+// -lse and dloss / c of a token; d stays 0 for one without a gradient.
 __device__ __forceinline__ void token_factors(const GradInputs& q, float c, int token, long long y, float& less, float& d) {
-    less = -__ldg(q.lse + token) * kLog2e;
+    less = -__ldg(q.lse + token);
     if (y != q.ignore && y >= 0 && y < q.V && c != 0.f) d = __fdiv_rn(__ldg(q.dloss + token), c);
 }
 
@@ -164,7 +169,8 @@ struct GradTile {
         const float2 l2 = both(kLog2e), ls = both(less);
 #pragma unroll
         for (int i = 0; i < 32; i += 2) {
-            const float2 e = fma2(make_float2(v[i], v[i + 1]), l2, ls);
+            // the difference first: for a likely word it is small and exact
+            const float2 e = mul2(add2(make_float2(v[i], v[i + 1]), ls), l2);
             v[i] = exp2_fast(e.x);
             v[i + 1] = exp2_fast(e.y);
         }
@@ -305,7 +311,7 @@ struct GradWords {
         uint32_t h[16];
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-            v[i] = exp2_fast(fmaf(v[i], kLog2e, __shfl_sync(0xFFFFFFFFu, less, i)));
+            v[i] = exp2_fast((v[i] + __shfl_sync(0xFFFFFFFFu, less, i)) * kLog2e);
             if (hot) v[i] -= __shfl_sync(0xFFFFFFFFu, at, i) == t.lane ? 1.0f : 0.0f;
             const float di = __shfl_sync(0xFFFFFFFFu, d, i);
             // words past the last, which the products read, and ignored tokens (see GradTile): zeros
@@ -481,6 +487,9 @@ __global__ void __launch_bounds__(256) xent_dx_kernel(const float* __restrict__ 
 size_t round256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
 int parts(long long T, long long V) { return static_cast<int>(T <= kFewTokens ? (V + 31) / 32 : (V + 127) / 128); }
 
+// One segment holds a logit's whole sum: tall tiles need none.
+bool one_segment(long long D) { return D <= kLogitSegment * gm::BK; }
+
 // Words per piece of the backward: at most 2^28 entries of G (512 MB).  Smaller
 // pieces stay in L2 but cost more launches and more passes over dX's sums
 // (8192 x 128000 x 896: 2^26 entries 7.96 ms, 2^28 6.93 ms, 2^29 6.70 ms).
@@ -586,8 +595,7 @@ cudaError_t launch_xent(const uint16_t* x, long long T, long long D, const uint1
         if (!gemm_operand(&a, false, false, x, T, D, D) || !gemm_operand(&b, false, false, w, V, D, D))
             return cudaErrorInvalidValue;
         const GemmShape shape{Ti, Vi, Di, 0, 8, 1, 0, gm::BM, 0, 0};
-        // one segment holds the whole sum: tall tiles need none
-        const bool tall = D <= kLogitSegment * gm::BK && gemm_tall(T, V, 1);
+        const bool tall = one_segment(D) && gemm_tall(T, V, 1);
         e = T <= 256 ? launch_gemm_f16<LsePart, 1, 1, false, false, false, kFewSegment>(a, b, p, shape, status, st)
             : tall   ? launch_gemm_f16<LsePart, 1, 2, false, false, false, 0>(a, b, p, shape, status, st)
                      : launch_gemm_f16<LsePart, 1, 1, false, false, false, kLogitSegment>(a, b, p, shape, status, st);
@@ -638,8 +646,8 @@ cudaError_t launch_xent_backward(const float* dloss, const uint16_t* x, long lon
                 !gemm_result_bf16(&p.g, g, T, piece, pitch) || !gemm_result_bf16(&p.g_low, g + piece, T, piece, pitch))
                 return cudaErrorInvalidValue;
             const GemmShape shape{ni, Ti, Di, 0, 1, 1, 0, gemm_a_box(n), 0, 0};
-            e = T <= 64 ? launch_gemm_f16<GradWords, 1, 1, false, false, false, 0, 64>(wk, xk, p, shape, status, st)
-                        : launch_gemm_f16<GradWords, 1, 1, false, false, false, 0, 128>(wk, xk, p, shape, status, st);
+            e = T <= 64 ? launch_gemm_f16<GradWords, 1, 1, false, false, false, kFewSegment, 64>(wk, xk, p, shape, status, st)
+                        : launch_gemm_f16<GradWords, 1, 1, false, false, false, kFewSegment, 128>(wk, xk, p, shape, status, st);
         } else {
             GradTile::Params p;
             p.q = in;
@@ -647,8 +655,10 @@ cudaError_t launch_xent_backward(const float* dloss, const uint16_t* x, long lon
                 !gemm_result_bf16(&p.g, g, T, n, pitch))
                 return cudaErrorInvalidValue;
             const GemmShape shape{Ti, ni, Di, 0, 8, 1, 0, gm::BM, 0, 0};
-            e = gemm_tall(T, n, 1) ? launch_gemm_f16<GradTile, 1, 2, false, false, false, 0>(xk, wk, p, shape, status, st)
-                                   : launch_gemm_f16<GradTile, 1, 1, false, false, false, 0>(xk, wk, p, shape, status, st);
+            e = T <= 256 ? launch_gemm_f16<GradTile, 1, 1, false, false, false, kFewSegment>(xk, wk, p, shape, status, st)
+                : one_segment(D) && gemm_tall(T, n, 1)
+                    ? launch_gemm_f16<GradTile, 1, 2, false, false, false, 0>(xk, wk, p, shape, status, st)
+                    : launch_gemm_f16<GradTile, 1, 1, false, false, false, kLogitSegment>(xk, wk, p, shape, status, st);
         }
         if (e != cudaSuccess) return e;
         const long long g_cols = parts ? piece + n : n;

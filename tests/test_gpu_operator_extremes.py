@@ -10,6 +10,8 @@ import test_gpu_cross_entropy as ce
 from test_gpu_ffn_gated import Case
 
 pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+BF16 = torch.finfo(torch.bfloat16).eps / 2
 
 
 @pytest.fixture(scope="module")
@@ -63,3 +65,36 @@ def test_nan_words_reach_every_loss(sbl, T, words):
     assert torch.isnan(lse).all() and loss[1] == 0
     loss[1] = float("nan")
     assert torch.isnan(loss).all()
+
+
+@pytest.mark.parametrize("T,D", [(9, 4096), (100, 4096), (200, 4096), (300, 4096), (600, 2064)])
+def test_gradients_of_likely_words(sbl, T, D):
+    """Targets of probability 1 - 1e-3 to 1 - 1e-7, whose G = p - 1 is far below the
+    logits.  Logits off by at most e move log p_v by 2 e (1 - p_v), as long as the
+    backward's logits are the ones that lse is of; beside that p has a relative error
+    of eps = 2^-21 + (100 + |lse| + 12) u: the exponentials of lse and of p, at most 100
+    additions near 1, the rounding of lse and of the difference."""
+    g = torch.Generator().manual_seed(T + D)
+    V = 500
+    w = torch.randn(V, D, generator=g) / D ** 0.5
+    t = torch.randint(0, V, (T,), generator=g)
+    x = 0.5 * torch.randn(T, D, generator=g) + torch.linspace(13, 22, T)[:, None] * w[t]
+    x, w = x.bfloat16(), w.bfloat16()
+    d = torch.ones(T)
+    z, lse, loss, p, hot, dd = ce._refs(x, w, t, d)
+    assert loss.min() < 1e-6 and loss.max() > 1e-4
+    e, _, _ = ce._bounds(x, w, z, lse, loss)
+    eps = (2.0 ** -21 + (112 + lse.abs()) * U)[:, None]
+    rest = 1 - p
+    rest[hot > 0] = -torch.expm1(-loss)
+    G = torch.where(hot > 0, -rest, p)
+    dG = p * (torch.expm1(2 * e[:, None] * rest) + eps) * (1 + BF16) + G.abs() * ((BF16 if T > 128 else BF16 ** 2) + 4 * U)
+    Ga, wa, xa = G.abs() + dG, w.double().abs(), x.double().abs()
+    n = 2 if T > 128 else 4
+    dx, dw = G @ w.double(), G.T @ x.double()
+    bx = dG @ wa + (n * V / 16 + 64) * U * (Ga @ wa)
+    bw = dG.T @ xa + (n * T / 16 + 8) * U * (Ga.T @ xa)
+    _, got_lse = sbl.sbl_linear_cross_entropy(x.cuda(), w.cuda(), t.cuda())
+    got = sbl.sbl_linear_cross_entropy_backward(d.cuda(), x.cuda(), w.cuda(), t.cuda(), got_lse)
+    _check("dx", got[0], dx, bx * (1 + 2 * BF16) + BF16 * dx.abs())
+    _check("dw", got[1], dw, bw * (1 + 2 * BF16) + BF16 * dw.abs())
