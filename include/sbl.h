@@ -319,7 +319,8 @@ enum { SBL_ACT_SILU = 0, SBL_ACT_RELU2 = 1 };
  * sbl_ffn_gated — the gated feed-forward block on prepared weights:
  *   h[t, f] = act(g[t, f]) * u[t, f], g and u what sbl_linear gives in fp32 on
  *   the gate and the up matrix (Sparse-BitNet Guide, "Mathematical Formulation
- *   of Sparse-BitLinear"), act SiLU (g * sigmoid(g)) or max(g, 0)^2.  Both
+ *   of Sparse-BitLinear"), act SiLU (g * sigmoid(g), a sigmoid below 2^-126 taken as
+ *   0) or max(g, 0)^2, multiplied with u last, so that only h itself can overflow.  Both
  *   products, the activation and the product of the two in one kernel: neither
  *   g nor u is written.  sbl_linear on h with the down matrix completes the block.
  *

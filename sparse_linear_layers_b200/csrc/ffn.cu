@@ -74,10 +74,11 @@ __device__ __forceinline__ float2 rcp2(float2 a) {
     return r;
 }
 
-// act(g) * u
+// act(g) * u, in this order: g * u may pass fp32's range where act(g) * u does not.
+// A sigmoid below 2^-126 comes out as 0.
 template <int ACT>
 __device__ __forceinline__ float2 act_times(float2 g, float2 u) {
-    if (ACT == kActSilu) return mul2(mul2(g, u), rcp2(add2(exp_neg2(g), both(1.0f))));
+    if (ACT == kActSilu) return mul2(mul2(g, rcp2(add2(exp_neg2(g), both(1.0f)))), u);
     const float2 r = make_float2(fmaxf(g.x, 0.0f), fmaxf(g.y, 0.0f));
     return mul2(mul2(r, r), u);
 }
@@ -508,7 +509,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp::THREADS, 1)
                         const float2 gv = dequant2(g[i], g[i + 1], sgi, is), uv = dequant2(u[i], u[i + 1], sui, is);
                         float2 a, da;
                         act_both<ACT>(gv, a, da);
-                        const float2 vg = mul2(mul2(mul2(dhv, uv), da), mul2(sgi, is));
+                        // u * act'(g) first: dh * u may pass fp32's range where dh * u * act'(g) does not
+                        const float2 vg = mul2(mul2(mul2(uv, da), dhv), mul2(sgi, is));
                         const float2 vu = mul2(mul2(dhv, a), mul2(sui, is));
                         // a token past the end has inv_s = 0, a unit past F a scale of 0
                         g[i] = __float_as_uint(vg.x);

@@ -52,6 +52,49 @@ def test_gradients_of_tokens_far_apart(sbl, T, K, F, act, ternary):
     assert sbl.sbl_device_status() == 0
 
 
+@pytest.mark.parametrize("T", [1, 12, 40])
+def test_silu_of_enormous_activations(sbl, T):
+    """g * u beyond fp32's range where act(g) * u is not.  x = 127 gives x_q = 127 and s = 1
+    exactly, so g = 2032 scale_gate and u = 2032 scale_up of the chosen signs, acc * scale
+    no larger than u (with s = 127 the layer's own acc * scale / s would pass fp32's range
+    for u above 3.4e38 / 127).  The sigmoid has the relative error delta of the ordinary
+    cases; below 2^-126, where it counts as 0, an absolute one of 2^-126."""
+    K, A, gs = 16, 16 * 127, torch.tensor([-100.0, -80.0, -60.0, -100.0, -86.0, 3.0, 0.5, -88.0])
+    us = torch.tensor([4e36, 8e36, 3e37, -4e36, 1e38, 1e37, -2e37, 1e38])
+    F = gs.numel()
+    rows = lambda v: torch.where(v[:, None] > 0, 0x55, 0xAA).to(torch.uint8).expand(F, K // 4).contiguous()  # all +1 / all -1
+    make = lambda v: sbl.PreparedWeights(rows(v).cuda(), (v.abs() / A).cuda(), 2, 4, K)
+    gate, up = make(gs), make(us)
+    x = torch.full((T, K), 127.0, dtype=torch.bfloat16, device="cuda")
+    g, u = gs.sign().double() * (gs.abs() / A).double() * A, us.sign().double() * (us.abs() / A).double() * A
+    sig = torch.sigmoid(g)
+    delta = (5 + 1.2 * g.abs()) * 2.0 ** -23 + 4 * U * (1 + g.abs())
+    h = (g * sig * u).expand(T, F)
+    bound = (h.abs() * (delta + 12 * U) + g.abs() * u.abs() * 2.0 ** -126).expand(T, F)
+    for dt in (torch.float32, torch.bfloat16):
+        out = torch.finfo(dt).eps / 2
+        _check("h", sbl.sbl_ffn_gated(x, gate, up, out_dtype=dt), h, bound * (1 + 2 * out) + out * h.abs())
+    # dh = 1000: dh * u passes fp32's range before act'(g) brings it back
+    keep = gs < 0
+    dh = torch.full((T, F), 1000.0) * keep
+    du, dg = dh.double() * g * sig, dh.double() * u * sig * (1 + g * (1 - sig))
+    du_err = dh.double() * g.abs() * (sig * (delta + 12 * U) + 2.0 ** -126)
+    slope = 1 + g.abs()
+    dg_err = dh.double() * u.abs() * slope * (sig * (2 * delta + 20 * U) + 2.0 ** -125)
+    dx, dwg, dwu = sbl.sbl_ffn_gated_backward(dh.cuda(), x, gate, up)
+    # dW: x_hat = 127; the reductions' (T / 128 + 80) u, and 2^-38 of the token's largest v
+    sg, su = (gs.abs() / A).double(), (us.abs() / A).double()
+    floor = torch.maximum((dg.abs() * sg).amax(1), (du.abs() * su).amax(1))[:, None] * 2.0 ** -38 + 1e-37
+    for name, v, q, e, sc in (("dgate", dwg, dg, dg_err, sg), ("dup", dwu, du, du_err, su)):
+        ref = 127 * q.sum(0)[:, None].expand(F, K)
+        b = 127 * (e.sum(0) + (T / 128 + 90) * U * q.abs().sum(0) + (floor.sum(0) * 1.01 / sc))[:, None].expand(F, K)
+        _check(name, v, ref, b)
+    ref = ((dg * g.sign() * sg).sum(1) + (du * u.sign() * su).sum(1))[:, None].expand(T, K)
+    terms = (dg.abs() * sg).sum(1) + (du.abs() * su).sum(1)
+    b = (dg_err * sg).sum(1) + (du_err * su).sum(1) + (2 * F / 128 + 90) * U * terms + 2 * F * floor[:, 0]
+    _check("dx", dx, ref, b[:, None].expand(T, K))
+
+
 # ---------------------------------------------------------------- the cross entropy
 @pytest.mark.parametrize("T", [9, 128, 200, 300, 1000])
 @pytest.mark.parametrize("words", [(0, 32), (128, 192), (0, 128), (290, 300), (480, 513)])
