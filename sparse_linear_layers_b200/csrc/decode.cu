@@ -352,8 +352,7 @@ static cudaError_t launch_decode_lt(const DecodeGroup& grp, int K, const uint16_
     const long long blocks = (groups + NTH / 32 - 1) / (NTH / 32);
     const size_t smem = static_cast<size_t>(TT) * K;
     if (smem > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(decode_kernel<L, TT, CW, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(smem));
+        cudaError_t e = allow_shared<decode_kernel<L, TT, CW, NB>>();
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};

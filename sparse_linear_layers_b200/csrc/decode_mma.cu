@@ -300,8 +300,7 @@ static cudaError_t launch_dm(const uint8_t* packed, const float* row_scale, int 
     const int blocks = (R + tiles_per_block - 1) / tiles_per_block;
     const size_t smem = dm_smem_bytes(K, TP, NT);
     if (smem > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(decode_mma_kernel<NT, CW, PREQ>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(smem));
+        cudaError_t e = allow_shared<decode_mma_kernel<NT, CW, PREQ>>();
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};
@@ -332,7 +331,7 @@ static cudaError_t launch_dm_cw(int CW, const uint8_t* packed, const float* row_
                                   stream);
 }
 
-bool decode_mma_supported(long long K) { return K % 64 == 0 && K > 0 && dm_smem_bytes(static_cast<int>(K), 1, 2) <= 200 * 1024; }
+bool decode_mma_supported(long long K) { return K % 64 == 0 && K > 0 && dm_smem_bytes(static_cast<int>(K), 1, 2) <= kMostShared; }
 
 // Passes of up to 16 tokens (as many as fit 200 KB of shared memory); later
 // passes read the weights again, mostly from L2.  Needs K % 64 == 0.  With
@@ -347,7 +346,7 @@ cudaError_t launch_decode_mma(const uint8_t* packed, const float* row_scale, lon
     const int R = (Oi + 15) / 16;
     const int KS = choose_ks(R, C, CW == 4 ? 2 : kDmBatch, num_sms);
     int cap = kDmMaxTokens;
-    while (cap > 1 && dm_smem_bytes(Ki, cap, cap > 8 ? 2 : 1) > 200 * 1024) --cap;
+    while (cap > 1 && dm_smem_bytes(Ki, cap, cap > 8 ? 2 : 1) > kMostShared) --cap;
     for (long long t0 = 0; t0 < T; t0 += cap) {
         const int TP = static_cast<int>(T - t0 < cap ? T - t0 : cap);
         const int t0i = static_cast<int>(t0);

@@ -1025,7 +1025,7 @@ struct FfnDw {
 size_t round256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
 
 bool takes_decode(long long T, long long K) {
-    return T <= fd::MAX_TOKENS && K <= (1 << 20) && fd::smem_bytes(static_cast<int>(K), 1) <= 200 * 1024;
+    return T <= fd::MAX_TOKENS && K <= (1 << 20) && fd::smem_bytes(static_cast<int>(K), 1) <= kMostShared;
 }
 
 // Quantised activations, their scales, and the padded codes of both matrices.
@@ -1181,9 +1181,7 @@ cudaError_t launch_decode_as(const uint8_t* pg, const float* sg, const uint8_t* 
                              cudaStream_t st) {
     const size_t smem = fd::smem_bytes(K, TP);
     if (smem > 48 * 1024)
-        if (cudaError_t e = cudaFuncSetAttribute(ffn_decode_kernel<NT, CW, ACT>,
-                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)))
-            return e;
+        if (cudaError_t e = allow_shared<ffn_decode_kernel<NT, CW, ACT>>()) return e;
     const int tiles = (F + 7) / 8, per_block = fd::warps(NT) / KS;
     return pdl_launch(ffn_decode_kernel<NT, CW, ACT>, dim3((tiles + per_block - 1) / per_block), dim3(fd::warps(NT) * 32), smem,
                       st, pg, sg, pu, su, F, K, x, t0, TP, KS, h, h_bf16, status);
@@ -1212,7 +1210,7 @@ cudaError_t run_decode(const uint16_t* x, long long T, int K, const uint8_t* pg,
     while (KS < most && 2 * KS <= C && static_cast<long long>(tiles) * 2 * KS <= static_cast<long long>(num_sms) * fd::SM_WARPS)
         KS *= 2;
     int cap = fd::MAX_TOKENS;  // tokens of one pass
-    while (cap > 1 && fd::smem_bytes(K, cap) > 200 * 1024) --cap;
+    while (cap > 1 && fd::smem_bytes(K, cap) > kMostShared) --cap;
     for (int t0 = 0; t0 < T; t0 += cap) {
         const int TP = static_cast<int>(T) - t0 < cap ? static_cast<int>(T) - t0 : cap;
         const int ks = KS < fd::warps(TP > 8 ? 2 : 1) ? KS : fd::warps(TP > 8 ? 2 : 1);

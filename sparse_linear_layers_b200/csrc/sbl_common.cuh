@@ -1,6 +1,7 @@
 // Shared device helpers of the Sparse-BitLinear kernels (sm_100a only).
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -24,6 +25,23 @@ inline cudaError_t pdl_launch(Kern kernel, dim3 grid, dim3 block, size_t smem, c
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Opts a kernel in to kMostShared bytes of dynamic shared memory on the current device,
+// the most any size asks of the decode kernels, once.  (Set to each call's own bytes,
+// one host thread's smaller value could come between another's larger one and its
+// launch, which was then refused.)
+constexpr int kMostShared = 200 * 1024;
+template <auto Kern>
+inline cudaError_t allow_shared() {
+    static std::atomic<bool> done[64];
+    int dev = 0;
+    if (cudaError_t e = cudaGetDevice(&dev)) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    if (cudaError_t e = cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared)) return e;
+    done[dev].store(true, std::memory_order_release);
+    return cudaSuccess;
 }
 
 // Bits of the per-device status word (see sbl_device_status in sbl.h).

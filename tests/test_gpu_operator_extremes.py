@@ -3,6 +3,10 @@ values, sizes or callers lie far apart.
 
 The 64-bit references and bounds are those of the operators' own test files unless
 a test states another."""
+import ctypes
+import os
+import subprocess
+
 import pytest
 import torch
 
@@ -93,6 +97,65 @@ def test_silu_of_enormous_activations(sbl, T):
     terms = (dg.abs() * sg).sum(1) + (du.abs() * su).sum(1)
     b = (dg_err * sg).sum(1) + (du_err * su).sum(1) + (2 * F / 128 + 90) * U * terms + 2 * F * floor[:, 0]
     _check("dx", dx, ref, b[:, None].expand(T, K))
+
+
+CALLERS = r"""
+#include <pthread.h>
+#include <stdint.h>
+#include "sbl.h"
+struct call { const void* f; void* x; void* w; void* s; void* h; void* ws; int64_t K; void* stream; int repeats, linear; long refused; };
+static void* loop(void* p) {
+    struct call* c = p;
+    for (int i = 0; i < c->repeats; ++i) {
+        sbl_status r = c->linear
+            ? ((__typeof__(&sbl_linear_path))c->f)(c->x, c->linear, c->K, c->w, c->s, 8, 2, 4, c->h, SBL_F32, 0, c->ws, 1 << 21, SBL_PATH_DECODE, c->stream)
+            : ((__typeof__(&sbl_ffn_gated))c->f)(c->x, 16, c->K, c->w, c->s, c->w, c->s, 8, 2, 4, SBL_ACT_SILU, c->h, SBL_F32, 0, 0, c->stream);
+        if (r != SBL_OK) ++c->refused;
+    }
+    return 0;
+}
+long two_at_once(struct call* c) {
+    pthread_t t[2];
+    for (int i = 0; i < 2; ++i) if (pthread_create(&t[i], 0, loop, c + i)) return -1;
+    for (int i = 0; i < 2; ++i) pthread_join(t[i], 0);
+    return c[0].refused + c[1].refused;
+}
+"""
+
+
+@pytest.mark.parametrize("linear", [0, 8, 16])
+def test_decode_calls_of_two_threads(sbl, linear, tmp_path):
+    """Calls for a few tokens, of different lengths K, from two host threads at once (in C:
+    Python's lock would keep them apart): what one asks of the kernel's shared memory
+    does not undercut the other's launch.  sbl_ffn_gated, and sbl_linear's decode on the
+    CUDA cores (8 tokens, K % 64 != 0) and the warp-level MMA (16)."""
+    from sparse_linear_layers_b200._lib import lib
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    src, so = tmp_path / "callers.c", tmp_path / "callers.so"
+    src.write_text(CALLERS)
+    subprocess.run(["gcc", "-O2", "-std=gnu99", "-shared", "-fPIC", "-pthread", f"-I{root}/include", str(src), "-o", str(so)],
+                   check=True)
+    fields = [(n, ctypes.c_void_p) for n in ("f", "x", "w", "s", "h", "ws")] + [("K", ctypes.c_int64), ("stream", ctypes.c_void_p)] \
+        + [("repeats", ctypes.c_int), ("linear", ctypes.c_int), ("refused", ctypes.c_long)]
+    Call = type("Call", (ctypes.Structure,), {"_fields_": fields})
+    f = ctypes.cast(lib.sbl_linear_path if linear else lib.sbl_ffn_gated, ctypes.c_void_p)
+    held, calls, streams = [], (Call * 2)(), [torch.cuda.Stream(), torch.cuda.Stream()]
+    for c, K, st in zip(calls, (8208, 16400) if linear == 8 else (4096, 8192), streams):
+        x = torch.randn(16, K, device="cuda").bfloat16()
+        w = sbl.PreparedWeights(torch.full((8, K // 4), 0x21, dtype=torch.uint8, device="cuda"),
+                                torch.full((8,), 0.01, device="cuda"), 2, 4, K)
+        ws, h = torch.empty(1 << 21, dtype=torch.uint8, device="cuda"), torch.zeros(linear or 16, 8, device="cuda")
+        want = sbl.sbl_linear(x[:linear].contiguous(), w, path="decode") if linear else sbl.sbl_ffn_gated(x, w, w)
+        c.f, c.x, c.w, c.s, c.h, c.ws = f, x.data_ptr(), w.packed.data_ptr(), w.row_scale.data_ptr(), h.data_ptr(), ws.data_ptr()
+        c.K, c.stream, c.repeats, c.linear = K, st.cuda_stream, 5000, linear
+        held.append((x, w, ws, h, want))
+    torch.cuda.synchronize()
+    run = ctypes.CDLL(str(so)).two_at_once
+    run.restype = ctypes.c_long
+    assert run(calls) == 0
+    torch.cuda.synchronize()
+    for *_, h, want in held:
+        assert torch.equal(h, want)
 
 
 # ---------------------------------------------------------------- the cross entropy
