@@ -493,12 +493,15 @@ __global__ void __launch_bounds__(nrm::STREAM_THREADS, 1)
             get_pairs(a, f);
             get_pairs(d, g);
         };
-        // xhat = x * rstd - mean * rstd
-        float2 scale[R], shift[R];
+        // xhat = (x - mean) * rstd, as in the other kernels: of a mean far from 0,
+        // x * rstd - mean * rstd would keep the rounding of mean * rstd, and its one
+        // instruction less gains nothing (16384 x 4864 bf16: the same 92 us)
+        float2 scale[R], less[R];
+        auto xhat = [&](int r, float2 f) { return mul2(LAYER ? add2(f, less[r]) : f, scale[r]); };
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             scale[r] = both(rstd[r]);
-            shift[r] = both(-mean[r] * rstd[r]);
+            less[r] = both(-mean[r]);
             float2 s1 = make_float2(0.f, 0.f), s0 = s1;
 #pragma unroll
             for (int c = 0; c < NC; ++c)
@@ -507,7 +510,7 @@ __global__ void __launch_bounds__(nrm::STREAM_THREADS, 1)
                     each(r, c, f, g);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float2 xh = LAYER ? fma2(f[i], scale[r], shift[r]) : mul2(f[i], scale[r]);
+                        const float2 xh = xhat(r, f[i]);
                         const float2 q = mul2(g[i], wv[c][i]);
                         s1 = fma2(q, xh, s1);
                         if (LAYER) s0 = add2(s0, q);
@@ -533,7 +536,7 @@ __global__ void __launch_bounds__(nrm::STREAM_THREADS, 1)
                         each(r, c, f, g);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const float2 xh = LAYER ? fma2(f[i], scale[r], shift[r]) : mul2(f[i], scale[r]);
+                            const float2 xh = xhat(r, f[i]);
                             const float2 q = mul2(g[i], wv[c][i]);
                             f[i] = fma2(xh, c1, LAYER ? fma2(q, scale[r], c0) : mul2(q, scale[r]));
                         }

@@ -11,6 +11,7 @@ import pytest
 import torch
 
 import test_gpu_cross_entropy as ce
+import test_gpu_norm as nm
 from test_gpu_ffn_gated import Case
 
 pytestmark = pytest.mark.gpu
@@ -204,3 +205,31 @@ def test_gradients_of_likely_words(sbl, T, D):
     got = sbl.sbl_linear_cross_entropy_backward(d.cuda(), x.cuda(), w.cuda(), t.cuda(), got_lse)
     _check("dx", got[0], dx, bx * (1 + 2 * BF16) + BF16 * dx.abs())
     _check("dw", got[1], dw, bw * (1 + 2 * BF16) + BF16 * dw.abs())
+
+
+# ---------------------------------------------------------------- norms
+@pytest.mark.parametrize("T,K", [(33, 896), (1900, 896), (7, 8192), (500, 4864), (9601, 272), (400, 5136), (35, 16400)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_backward_far_from_zero_mean(sbl, T, K, dtype):
+    """Rows whose mean is 1000 times their spread, by the formulas of the very mean and
+    rstd given: x - mean is rounded once and so is its product with rstd, X = 2 u
+    |xhat|, in every kernel (few rows, many rows, long rows)."""
+    g = torch.Generator().manual_seed(K)
+    x = (torch.randn(T, K, generator=g) + 1000.0 * torch.sign(torch.randn(T, 1, generator=g))).to(dtype)
+    dy, w = torch.randn(T, K, generator=g).to(dtype), 1 + 0.2 * torch.randn(K, generator=g)
+    m64, r64 = nm._stats(x.double(), "layer", 1e-5)
+    mean, rstd = m64[:, 0].float(), r64[:, 0].float()
+    m, r, xd, dyd, wd = mean.double()[:, None], rstd.double()[:, None], x.double(), dy.double(), w.double()
+    xh, D = (xd - m) * r, 40 + K / 4096
+    X, q = 2.01 * U * xh.abs(), dyd * wd
+    m1, m0 = (q * xh).mean(1, keepdim=True), q.mean(1, keepdim=True)
+    m1_err = (q.abs() * X).mean(1, keepdim=True) + (D + 3) * U * (q * xh).abs().mean(1, keepdim=True)
+    m0_err = (D + 3) * U * q.abs().mean(1, keepdim=True)
+    out = torch.finfo(dtype).eps / 2
+    dx = r * (q - m0 - xh * m1)
+    size = q.abs() + m0.abs() + (xh * m1).abs()
+    bx = r * (m0_err + xh.abs() * m1_err + X * (m1.abs() + m1_err) + 6 * U * size) * (1 + 2 * out) + out * dx.abs()
+    got = sbl.sbl_norm_backward(dy.cuda(), x.cuda(), w.cuda(), mean.cuda(), rstd.cuda(), kind="layer")
+    _check("dx", got[0], dx, bx)
+    _check("dw", got[1], (dyd * xh).sum(0), (dyd.abs() * X).sum(0) + (T + 99) * U * (dyd * xh).abs().sum(0))
+    _check("db", got[2], dyd.sum(0), (T + 99) * U * dyd.abs().sum(0))
