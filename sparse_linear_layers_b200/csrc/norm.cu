@@ -14,7 +14,9 @@
 // count (30 per element with 8 columns a thread, a quarter of them a sum's
 // shuffles), so a thread takes up to 32 columns of two rows and the arithmetic
 // runs on pairs of fp32 values.  All sums are fp32; the variance is the sum of
-// squared differences from the mean.
+// squared differences from the mean, which is divided, not multiplied by 1 / K: a
+// constant row, whose sum is exact in bf16, then has exactly its value as the mean
+// (K = 896: 3.0 came out as 3 - 2^-22, which rstd = 316 makes 7e-5).
 //
 // Forward: a group of warps holds its rows in registers between the sums and
 // the results; weights come from L1 once per two rows.  16384 x 4864 bf16:
@@ -217,7 +219,7 @@ __global__ void __launch_bounds__(NC == 1 && R == 1 ? 1024 : nrm::FWD_THREADS, N
         }
         group_sums<R>(mean, wpr, wig, red[0] + group * wpr * R, barrier);
 #pragma unroll
-        for (int r = 0; r < R; ++r) mean[r] *= inv_k;
+        for (int r = 0; r < R; ++r) mean[r] = __fdiv_rn(mean[r], static_cast<float>(K));
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -646,7 +648,7 @@ __global__ void __launch_bounds__(nrm::WIDE_THREADS)
                 raw.get(f);
                 s += ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
             }
-            mean = block_sum(s, red) * inv_k;
+            mean = __fdiv_rn(block_sum(s, red), static_cast<float>(K));
         }
         float q = 0.f;
         for (int c = threadIdx.x * 8; c < K; c += nrm::WIDE_THREADS * 8) {

@@ -233,3 +233,19 @@ def test_backward_far_from_zero_mean(sbl, T, K, dtype):
     _check("dx", got[0], dx, bx)
     _check("dw", got[1], (dyd * xh).sum(0), (dyd.abs() * X).sum(0) + (T + 99) * U * (dyd * xh).abs().sum(0))
     _check("db", got[2], dyd.sum(0), (T + 99) * U * dyd.abs().sum(0))
+
+
+@pytest.mark.parametrize("T,K", nm.SHAPES)
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_norm_outputs_are_numbers(sbl, T, K, kind, dtype):
+    """Finite rows, a constant one and one of zeros among them, give finite outputs."""
+    x, dy, w, b = (v.cuda() for v in nm._inputs(T, K, dtype, seed=T + 2 * K, offset=100.0))
+    x[T // 2] = 3.0
+    if T > 2:
+        x[T - 1] = 0.0
+    y, mean, rstd = sbl.sbl_norm(x, w, b, kind=kind, eps=1e-5, with_stats=True)
+    outs = [y, rstd, *sbl.sbl_norm_backward(dy, x, w, mean, rstd, kind=kind)] + ([mean] if kind == "layer" else [])
+    assert all(torch.isfinite(v).all() for v in outs)
+    if kind == "layer":  # with no spread only the bias is left
+        assert torch.equal(y[T // 2], b.to(dtype))
