@@ -249,3 +249,28 @@ def test_norm_outputs_are_numbers(sbl, T, K, kind, dtype):
     assert all(torch.isfinite(v).all() for v in outs)
     if kind == "layer":  # with no spread only the bias is left
         assert torch.equal(y[T // 2], b.to(dtype))
+
+
+def test_far_rows_are_numbers(sbl):
+    """Past 2^31 elements: the last rows of a norm and of the block, as numbers."""
+    if torch.cuda.get_device_properties(0).total_memory < 120 << 30:
+        pytest.skip("needs 60 GB on the device")
+    T, K, n = 270001, 8192, 40
+    x = torch.zeros(T, K, dtype=torch.bfloat16, device="cuda")
+    x[-n:] = torch.randn(n, K, device="cuda").bfloat16()
+    w = torch.rand(K, device="cuda") + 0.5
+    y, mean, rstd = sbl.sbl_norm(x, w, w, kind="layer", with_stats=True)
+    assert torch.isfinite(y[-2 * n:]).all() and torch.isfinite(mean).all() and torch.isfinite(rstd).all()
+    dx, dw, db = sbl.sbl_norm_backward(y, x, w, mean, rstd, kind="layer")
+    assert torch.isfinite(dx[-2 * n:]).all() and torch.isfinite(dw).all() and torch.isfinite(db).all()
+    del x, y, dx
+    T, K, F = 540011, 64, 4096
+    c = Case(sbl, 150, K, F, seed=6)
+    x = torch.zeros(T, K, dtype=torch.bfloat16, device="cuda")
+    x[-150:] = c.x
+    h = sbl.sbl_ffn_gated(x, c.gate, c.up)
+    assert torch.isfinite(h[-300:]).all() and h[-150:].any()
+    got = sbl.sbl_ffn_gated_backward(h, x, c.gate, c.up)
+    assert torch.isfinite(got[0][-300:]).all() and all(torch.isfinite(v).all() for v in got[1:])
+    del x, h, got
+    torch.cuda.empty_cache()
