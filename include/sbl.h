@@ -216,7 +216,7 @@ sbl_status sbl_norm(const void* x, int dtype, int64_t T, int64_t K, int kind, co
  *   workspace   sbl_norm_backward_workspace_bytes(T, K, dtype) bytes, 256-byte
  *               aligned, when dweight or dbias is given (else SBL_ERR_WORKSPACE);
  *               calls that share it must be ordered on one stream.
- * At least one output.  Asynchronous on `stream`.
+ * At least one output unless T == 0.  Asynchronous on `stream`.
  */
 size_t sbl_norm_backward_workspace_bytes(int64_t T, int64_t K, int dtype);
 sbl_status sbl_norm_backward(const void* dy, const void* x, int dtype, int64_t T, int64_t K, int kind,
@@ -276,7 +276,7 @@ enum { SBL_BWD_DW_TERNARY = 1 };
  * reduction length (O for dX, T for dW; n + 3 for SBL_BWD_DW_TERNARY).
  * Empty reductions write zeros (dW for T == 0, dX for O == 0).  Only the
  * pointers the requested outputs read must be valid.  At least one of dX, dW
- * must be non-NULL.
+ * must be non-NULL unless T or O is 0.
  * K % 16 == 0; any T, O >= 0.  Asynchronous on `stream`; no workspace.
  */
 sbl_status sbl_linear_backward(const float* dY, int64_t T, int64_t O, const int8_t* x_q, const float* s_tok,
@@ -353,7 +353,7 @@ sbl_status sbl_ffn_gated(const uint16_t* x_bf16, int64_t T, int64_t K, const uin
  *
  *   dh        fp32 [T, F] (4-byte aligned), finite: gradient with respect to h.
  *   dX        fp32 [T, K]; dW_gate, dW_up fp32 [F, K] (outputs), each may be
- *             NULL, not all; overwritten (zeros for empty sums).
+ *             NULL, not all unless T or F is 0; overwritten (zeros for empty sums).
  *   workspace sbl_ffn_gated_backward_workspace_bytes(T, K, F, dX != NULL,
  *             dW_gate != NULL || dW_up != NULL) bytes, 256-byte aligned
  *             (about 16 bytes per token and hidden unit).
@@ -403,8 +403,8 @@ sbl_status sbl_linear_cross_entropy(const uint16_t* x_bf16, int64_t T, int64_t D
  *   ignored tokens; dX = G . W, dW = G^T . x.
  *
  *   dloss     fp32 [T] (4-byte aligned), finite; lse as sbl_linear_cross_entropy wrote it.
- *   dx, dw    bf16 [T, D] and [V, D] (outputs), each may be NULL, not both;
- *             overwritten (dw with zeros for T == 0).
+ *   dx, dw    bf16 [T, D] and [V, D] (outputs), each may be NULL, not both unless
+ *             T == 0; overwritten (dw with zeros for T == 0).
  *   workspace sbl_linear_cross_entropy_backward_workspace_bytes(T, D, V, dx != NULL)
  *             bytes, 256-byte aligned (at most 512 MB for the gradient of one
  *             piece of the logits, more only for T > 2^17, and fp32 sums of dx).

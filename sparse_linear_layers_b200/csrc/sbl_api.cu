@@ -273,15 +273,15 @@ sbl_status sbl_norm_backward(const void* dy, const void* x, int dtype, int64_t T
                              const float* weight, const float* mean, const float* rstd, void* dx, float* dweight,
                              float* dbias, void* workspace, size_t workspace_bytes, void* stream) {
     if (sbl_status s = check_norm(dtype, T, K, kind)) return s;
-    if (!dx && !dweight && !dbias) return SBL_ERR_INVALID_ARG;
     if (!aligned(dweight, 16) || !aligned(dbias, 16)) return SBL_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (T == 0) {  // empty sums
+    if (T == 0) {  // empty sums; an empty dx has no address either
         cudaError_t e = cudaSuccess;
         if (dweight) e = cudaMemsetAsync(dweight, 0, static_cast<size_t>(K) * sizeof(float), st);
         if (dbias && e == cudaSuccess) e = cudaMemsetAsync(dbias, 0, static_cast<size_t>(K) * sizeof(float), st);
         return from_cuda(e);
     }
+    if (!dx && !dweight && !dbias) return SBL_ERR_INVALID_ARG;
     if (!dy || !x || !weight || !rstd || (kind == SBL_NORM_LAYER && !mean) || dx == x || dx == dy)
         return SBL_ERR_INVALID_ARG;
     for (const void* p : {dy, x, static_cast<const void*>(weight), static_cast<const void*>(dx)})
@@ -320,7 +320,7 @@ sbl_status sbl_linear_backward(const float* dY, int64_t T, int64_t O, const int8
     if (T < 0 || O < 0) return SBL_ERR_INVALID_ARG;
     if (flags & ~SBL_BWD_DW_TERNARY) return SBL_ERR_INVALID_ARG;
     if (sbl_status s = check_k(K)) return s;
-    if (!dX && !dW) return SBL_ERR_INVALID_ARG;
+    if (!dX && !dW && T > 0 && O > 0) return SBL_ERR_INVALID_ARG;  // an empty output has no address
     const bool any_dx = dX && T > 0, any_dw = dW && O > 0;  // outputs with elements
     const bool ternary = (flags & SBL_BWD_DW_TERNARY) != 0;
     // what the requested outputs read: every pointer non-null and 16-byte aligned
@@ -352,7 +352,7 @@ sbl_status sbl_linear_backward_ws(const float* dY, int64_t T, int64_t O, const i
     if (T < 0 || O < 0) return SBL_ERR_INVALID_ARG;
     if (flags & ~SBL_BWD_DW_TERNARY) return SBL_ERR_INVALID_ARG;
     if (sbl_status s = check_k(K)) return s;
-    if (!dX && !dW) return SBL_ERR_INVALID_ARG;
+    if (!dX && !dW && T > 0 && O > 0) return SBL_ERR_INVALID_ARG;  // an empty output has no address
     // empty reductions (all zeros) and empty outputs: the CUDA-core entry point
     if (T == 0 || O == 0)
         return sbl_linear_backward(dY, T, O, x_q, s_tok, K, packed, row_scale, dX, dW, flags, stream);
@@ -414,18 +414,18 @@ sbl_status sbl_ffn_gated_backward(const float* dh, const uint16_t* x_bf16, int64
                                   float* dW_up, int flags, void* workspace, size_t workspace_bytes, void* stream) {
     if (sbl_status s = check_ffn(T, K, F, n, m, act)) return s;
     if (flags & ~SBL_BWD_DW_TERNARY) return SBL_ERR_INVALID_ARG;
-    if (!dX && !dW_gate && !dW_up) return SBL_ERR_INVALID_ARG;
     for (const void* p : {static_cast<const void*>(dX), static_cast<const void*>(dW_gate),
                           static_cast<const void*>(dW_up)})
         if (!aligned(p, 16)) return SBL_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (T == 0 || F == 0) {  // empty sums
+    if (T == 0 || F == 0) {  // empty sums; an empty output has no address either
         cudaError_t e = cudaSuccess;
         if (dX && T > 0) e = cudaMemsetAsync(dX, 0, static_cast<size_t>(T) * K * sizeof(float), st);
         for (float* w : {dW_gate, dW_up})
             if (w && F > 0 && e == cudaSuccess) e = cudaMemsetAsync(w, 0, static_cast<size_t>(F) * K * sizeof(float), st);
         return from_cuda(e);
     }
+    if (!dX && !dW_gate && !dW_up) return SBL_ERR_INVALID_ARG;
     if (!dh || !aligned(dh, 4)) return SBL_ERR_INVALID_ARG;
     for (const void* p : {static_cast<const void*>(x_bf16), static_cast<const void*>(packed_gate), static_cast<const void*>(scale_gate),
                           static_cast<const void*>(packed_up), static_cast<const void*>(scale_up)})
@@ -481,10 +481,11 @@ sbl_status sbl_linear_cross_entropy_backward(const float* dloss, const uint16_t*
                                              int64_t ignore_index, const float* lse, uint16_t* dx, uint16_t* dw,
                                              void* workspace, size_t workspace_bytes, void* stream) {
     if (sbl_status s = check_xent(T, D, V)) return s;
-    if (!dx && !dw) return SBL_ERR_INVALID_ARG;
     if (!aligned(dx, 16) || !aligned(dw, 16)) return SBL_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    // an empty dx has no address either
     if (T == 0) return dw ? from_cuda(cudaMemsetAsync(dw, 0, static_cast<size_t>(V) * D * 2, st)) : SBL_OK;
+    if (!dx && !dw) return SBL_ERR_INVALID_ARG;
     if (!xent_inputs_ok(x_bf16, w_bf16, target, dloss, lse)) return SBL_ERR_INVALID_ARG;
     if (!workspace || !aligned(workspace, 256) ||
         workspace_bytes < sbl::xent_backward_workspace_bytes(T, D, V, dx != nullptr))

@@ -274,3 +274,35 @@ def test_far_rows_are_numbers(sbl):
     assert torch.isfinite(got[0][-300:]).all() and all(torch.isfinite(v).all() for v in got[1:])
     del x, h, got
     torch.cuda.empty_cache()
+
+
+# ---------------------------------------------------------------- empty batches
+def test_one_gradient_of_an_empty_batch(sbl):
+    """No tokens, and only the gradient of the input (or of one weight) wanted."""
+    w = torch.ones(64, device="cuda")
+    e, s = torch.empty((0, 64), device="cuda"), torch.empty((0,), device="cuda")
+    eb = e.bfloat16()
+    p = sbl.PreparedWeights(torch.zeros((16, 16), dtype=torch.uint8, device="cuda"), torch.ones(16, device="cuda"), 2, 4, 64)
+    W = torch.ones((50, 64), dtype=torch.bfloat16, device="cuda")
+    t = torch.empty((0,), dtype=torch.int64, device="cuda")
+    calls = [(3, lambda n: sbl.sbl_norm_backward(e, e, w, s, s, kind="layer", need_dx=n[0], need_dw=n[1], need_db=n[2])),
+             (3, lambda n: sbl.sbl_ffn_gated_backward(torch.empty((0, 16), device="cuda"), eb, p, p, need_dx=n[0],
+                                                      need_dgate=n[1], need_dup=n[2])),
+             (2, lambda n: sbl.sbl_linear_cross_entropy_backward(s, eb, W, t, s, need_dx=n[0], need_dw=n[1])),
+             (2, lambda n: sbl.sbl_linear_backward(torch.empty((0, 16), device="cuda"), torch.empty((0, 64), dtype=torch.int8, device="cuda"),
+                                                   s, p, need_dx=n[0], need_dw=n[1]))]
+    for outs, call in calls:
+        for i in range(outs):
+            got = call([j == i for j in range(outs)])
+            assert [v is not None for v in got] == [j == i for j in range(outs)]
+            assert not got[i].any() and (i > 0 or got[0].shape == (0, 64))
+
+
+def test_modules_with_frozen_weights_on_an_empty_batch(sbl):
+    x = torch.empty((0, 64), device="cuda", requires_grad=True)
+    norm = sbl.SparseBitNorm(64, bias=True, device="cuda").requires_grad_(False)
+    ffn = sbl.SparseBitFeedForward(64, 96, device="cuda").requires_grad_(False)
+    head = sbl.LinearCrossEntropy(64, 50, reduction="sum", device="cuda").requires_grad_(False)
+    loss = head(ffn(norm(x)), torch.empty((0,), dtype=torch.int64, device="cuda"))
+    loss.backward()
+    assert loss == 0 and x.grad.shape == (0, 64)
