@@ -698,7 +698,7 @@ inline GemmPlan gemm_plan(const GemmWork& w1, const GemmWork& w2) {
             if (s2 > 1 && (s2 > w2.most || s2 > w2.KB || w2.tiles * s2 > 148)) break;
             const double l2 = tile_us(w2, s2);
             const long long n2 = w2.tiles * s2;
-            const int lead = extra ? static_cast<int>(l1 / l2 + 0.5) : 0;
+            const int lead = extra && n2 ? static_cast<int>(l1 / l2 + 0.5) : 0;  // no second product: nothing to lead with
             const long long early = n2 < idle * lead ? n2 : idle * lead, rest = n2 - early, full = rest / 74, tail = rest % 74;
             const double a = each * l1 + static_cast<double>((early + idle - 1) / idle + full + (tail > 0)) * l2;
             const double b = extra ? (each + 1) * l1 + static_cast<double>(full + (tail > idle)) * l2 : 0.0;

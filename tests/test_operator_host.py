@@ -16,3 +16,42 @@ def test_empty_batches_ask_for_nothing_on_the_host():
         assert lin(0, 8) == lin(4, 0) == 0 and lin(4, 8) == 1
     # sizes and types are checked all the same
     assert norm(-1) == 1 and norm(0, 2) == 1 and ffn(-1, 8) == 1 and ce(-1) == 1
+
+
+PLAN_PROGRAM = r"""
+#include <cstdio>
+#include "gemm_f16.cuh"
+using namespace sbl;
+int main() {
+    const GemmWork none{0, 1, 0.0, 0.0, 0.0, 1};
+    int wrong = 0;
+    for (long long tiles = 1; tiles < 700; ++tiles)
+        for (long long KB : {1, 3, 14, 37, 250, 2048}) {
+            const GemmWork x{tiles, KB, 0.55, 1.0, 1e6, 64};
+            const GemmPlan p = gemm_plan(x, none);
+            // alone: the rounds of 74 pairs, and no tiles of a second product to begin with
+            const double s = p.splits1;
+            const double us = (long long)((tiles * p.splits1 + 73) / 74) * ((KB + p.splits1 - 1) / p.splits1 * 0.55 + 1.0) +
+                              (s > 1 ? 3.0 + s * 2.0 / 6.0 : 0.0);
+            if (p.lead != 0 || p.splits2 != 1 || !(p.us - us < 1e-9 && us - p.us < 1e-9)) {
+                if (!wrong++) printf("%lld tiles of %lld: lead %d, splits %d %d, %g us for %g\n", tiles, KB, p.lead, p.splits1, p.splits2, p.us, us);
+            }
+        }
+    printf("%d wrong\n", wrong);
+    return wrong != 0;
+}
+"""
+
+
+def test_plan_of_one_product_alone(tmp_path):
+    """gemm_plan with no second product: a finite plan, without tiles of it to lead with."""
+    import subprocess
+
+    from sparse_linear_layers_b200 import build
+    src = tmp_path / "plan.cu"
+    src.write_text(PLAN_PROGRAM)
+    exe = str(tmp_path / "plan")
+    subprocess.run([build._nvcc(), *build.ARCH, "-std=c++17", "--expt-relaxed-constexpr", "-I", build.INCLUDE, "-I", build.CSRC,
+                    str(src), "-o", exe], check=True)
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=60)
+    assert r.returncode == 0, r.stdout
