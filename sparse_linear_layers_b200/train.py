@@ -47,6 +47,10 @@ def _stop_on_nonfinite(where: str) -> None:
     status = api.sbl_device_status()
     if status == _lib.SBL_ERR_NONFINITE:
         raise FloatingPointError(f"{where}: non-finite latent weights or activations")
+    if status == _lib.SBL_ERR_INVALID_ARG:
+        # never the caller's own: it prepares its weights in its own pattern
+        raise _lib.SblError(status, f"found by {where} and set by an earlier call (sbl_linear_cross_entropy for a target "
+                                    "outside the vocabulary, or sbl_linear for weights not in their pattern)")
     if status != _lib.SBL_OK:
         raise _lib.SblError(status, f"{where} forward")
 
@@ -262,16 +266,30 @@ class LinearCrossEntropy(torch.nn.Module):
 
     ``weight`` is fp32 [vocab, in_features], cast to bf16 (as x is) for the
     products.  ``reduction``: "mean" over the tokens whose target is not
-    ``ignore_index``, "sum", or "none" (per token, 0 for ignored ones)."""
+    ``ignore_index``, "sum", or "none" (per token, 0 for ignored ones).
 
-    def __init__(self, in_features: int, vocab: int, ignore_index: int = -100, reduction: str = "mean", device=None):
+    With ``check_targets`` (the default) a forward whose targets are neither words nor
+    ``ignore_index`` raises IndexError before it runs.  Reading them waits for the stream;
+    ``check_targets=False``, and a forward captured in a graph, skip the wait and the
+    check: the loss of such a token is then NaN, and sbl_device_status reports it."""
+
+    def __init__(self, in_features: int, vocab: int, ignore_index: int = -100, reduction: str = "mean", device=None,
+                 check_targets: bool = True):
         super().__init__()
         if reduction not in ("mean", "sum", "none"):
             raise ValueError(f"reduction must be mean, sum or none, got {reduction!r}")
         self.in_features, self.vocab = in_features, vocab
-        self.ignore_index, self.reduction = ignore_index, reduction
+        self.ignore_index, self.reduction, self.check_targets = ignore_index, reduction, check_targets
         self.weight = torch.nn.Parameter(torch.empty((vocab, in_features), dtype=torch.float32, device=device))
         torch.nn.init.normal_(self.weight, std=0.02)
+
+    def _stop_on_bad_targets(self, t: torch.Tensor) -> None:
+        if t.is_cuda and torch.cuda.is_current_stream_capturing():
+            return
+        bad = ((t < 0) | (t >= self.vocab)) & (t != self.ignore_index)
+        if bad.any():
+            raise IndexError(f"LinearCrossEntropy: target {t[bad][0].item()} is neither one of {self.vocab} words nor "
+                             f"ignore_index={self.ignore_index}")
 
     def forward(self, x: torch.Tensor, target: torch.Tensor) -> torch.Tensor:
         if x.shape[:-1] != target.shape or x.shape[-1] != self.in_features:
@@ -279,6 +297,8 @@ class LinearCrossEntropy(torch.nn.Module):
                              f"{self.in_features}")
         x2 = x.reshape(-1, self.in_features).to(torch.bfloat16).contiguous()
         t = target.reshape(-1).contiguous()
+        if self.check_targets:
+            self._stop_on_bad_targets(t)
         loss = LinearCrossEntropyFunction.apply(x2, self.weight.to(torch.bfloat16), t, self.ignore_index)
         if self.reduction == "none":
             return loss.reshape(target.shape)

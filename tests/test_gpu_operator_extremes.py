@@ -207,6 +207,36 @@ def test_gradients_of_likely_words(sbl, T, D):
     _check("dw", got[1], dw, bw * (1 + 2 * BF16) + BF16 * dw.abs())
 
 
+def test_module_names_its_bad_targets(sbl):
+    """A target outside the vocabulary: the module's own error before anything runs;
+    without its check, or in a graph, the loss is NaN and no other module's forward
+    claims the error as its own."""
+    x = torch.randn(20, 64, device="cuda")
+    t = torch.randint(0, 77, (20,), device="cuda")
+    t[3] = -100
+    for wrong in (77, -1, 1 << 40):
+        head = sbl.LinearCrossEntropy(64, 77, device="cuda")
+        head(x, t)
+        bad = t.clone()
+        bad[5] = wrong
+        with pytest.raises(IndexError, match="LinearCrossEntropy"):
+            head(x, bad)
+        assert sbl.sbl_device_status() == 0
+        free = sbl.LinearCrossEntropy(64, 77, device="cuda", check_targets=False)
+        assert torch.isnan(free(x, bad))
+        with pytest.raises(sbl.SblError, match="sbl_linear_cross_entropy"):
+            sbl.SparseBitFeedForward(64, 96, device="cuda")(x)
+        assert sbl.sbl_device_status() == 0
+    # a forward in a graph is not checked; the graph's loss is the module's
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.no_grad():
+        with torch.cuda.graph(graph):
+            loss = head(x, t)
+    graph.replay()
+    assert torch.equal(loss, head(x, t))
+
+
 # ---------------------------------------------------------------- norms
 @pytest.mark.parametrize("T,K", [(33, 896), (1900, 896), (7, 8192), (500, 4864), (9601, 272), (400, 5136), (35, 16400)])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])

@@ -55,3 +55,32 @@ def test_plan_of_one_product_alone(tmp_path):
                     str(src), "-o", exe], check=True)
     r = subprocess.run([exe], capture_output=True, text=True, timeout=60)
     assert r.returncode == 0, r.stdout
+
+
+def test_bad_targets_are_named_before_anything_runs():
+    import pytest
+    import torch
+
+    from sparse_linear_layers_b200 import train
+    head = train.LinearCrossEntropy(16, 10, ignore_index=99)
+    for wrong in (-1, 10, 1 << 40, -100):
+        with pytest.raises(IndexError, match="LinearCrossEntropy.*%d " % wrong):
+            head(torch.zeros(2, 16), torch.tensor([3, wrong]))
+    for ok in (0, 9, 99):
+        with pytest.raises(ValueError):       # past the check: x is not on a GPU
+            head(torch.zeros(2, 16), torch.tensor([3, ok]))
+    head.check_targets = False
+    with pytest.raises(ValueError):
+        head(torch.zeros(2, 16), torch.tensor([3, 10]))
+
+
+def test_an_earlier_calls_status_is_not_blamed_on_a_module(monkeypatch):
+    import pytest
+
+    from sparse_linear_layers_b200 import _lib, api, train
+    monkeypatch.setattr(api, "sbl_device_status", lambda: _lib.SBL_ERR_INVALID_ARG)
+    with pytest.raises(_lib.SblError, match="earlier call .sbl_linear_cross_entropy"):
+        train._stop_on_nonfinite("SparseBitLinear")
+    monkeypatch.setattr(api, "sbl_device_status", lambda: _lib.SBL_ERR_NONFINITE)
+    with pytest.raises(FloatingPointError, match="SparseBitLinear"):
+        train._stop_on_nonfinite("SparseBitLinear")
