@@ -361,7 +361,7 @@ sbl_status sbl_ffn_gated(const uint16_t* x_bf16, int64_t T, int64_t K, const uin
  * s_tok, each output is within (n / 128 + 80) * 2^-24 * sum |terms| of the sum
  * over these fp32 v (n the reduction length, 2 F or T), plus 2^-38 of the
  * largest |v| of each token times what it multiplies.  (The terms of dW of tokens whose
- * largest |v| is below 2^-32 of all tokens' largest are summed on CUDA cores, in
+ * largest |v| is below 2^-22 of all tokens' largest are summed on CUDA cores, in
  * fp32, which takes longer where there are many.)  The same inputs give the same bits.
  * Other arguments, limits and errors as the forward.
  */

@@ -32,9 +32,10 @@
 // the token's largest value to [2^14, 2^15), into two fp16 parts (11 + 11
 // significant bits; what they drop is at most 2^-22 of v plus 2^-39 of the
 // token's largest |v|), writes the codes as fp16, and x_q * 2^(er[t] - max er + 8) as fp16,
-// exact down to er = max er - 32.  Tokens below that (their largest |v| under 2^-32 of
-// all tokens' largest) would lose bits of x_q, then all of it, and with it the
-// gradient of a hidden unit that only they reach: they are left out of dW's product and
+// normal numbers down to er = max er - 22.  Tokens below that (their largest |v| under
+// 2^-22 of all tokens' largest) would be subnormal, whose products the tensor cores align
+// as if they were larger (a hidden unit that only such tokens reach: off by 2^-17 at 2^-30),
+// then lose bits of x_q, then all of it.  They are left out of dW's product and
 // counted, and ffn_far_kernel adds their terms in fp32.  Two products of those in one launch (gemm_f16.cuh,
 // fp16 operands, both parts summed, segments of 4 k-blocks promoted to
 // round-to-nearest sums) give dX and dW: at 4096 x 2048 -> 7168 0.57 ms, the tensor
@@ -729,8 +730,9 @@ __device__ __forceinline__ int row_exponent(unsigned bits) {
 }
 // Power of two that x_q of a token takes in dW's product.
 __device__ __forceinline__ int token_shift(unsigned bits, int top) { return row_exponent(bits) - top + 8; }
-// Whether fp16 holds x_q times that: multiples of 2^-24.
-__device__ __forceinline__ bool token_far(unsigned bits, int top) { return bits != 0u && token_shift(bits, top) < -24; }
+// Whether x_q times that falls below fp16's normal numbers.
+constexpr int kLeastShift = -14;
+__device__ __forceinline__ bool token_far(unsigned bits, int top) { return bits != 0u && token_shift(bits, top) < kLeastShift; }
 __device__ __forceinline__ float pow2f(int e) { return __uint_as_float(static_cast<unsigned>(e + 127) << 23); }
 
 struct FfnOperands {
@@ -813,7 +815,7 @@ __global__ void __launch_bounds__(256) ffn_operands_kernel(const FfnOperands q) 
         const long long t = i / words;
         const unsigned bits = __ldg(q.row_max + t);
         const int e = token_shift(bits, top);
-        const float s = e < -24 ? 0.f : pow2f(e);
+        const float s = e < kLeastShift ? 0.f : pow2f(e);
         if (i == t * words && token_far(bits, top)) atomicAdd(q.far, 1u);
         const uint4 u = __ldg(reinterpret_cast<const uint4*>(q.xq) + i);
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};  // even 0-6, odd 1-7, even 8-14, odd 9-15
@@ -876,11 +878,12 @@ __global__ void __launch_bounds__(256) ffn_sum_kernel(const float4* __restrict__
 
 // dW's terms of the far tokens (token_far), added to the gradients that the product has
 // written: dW[f, k] += (1 / scale[f]) * sum_t v[t, f] * x_q[t, k], v from fp32 memory.
-// Most calls have none and the kernel ends at once.  Tiles of 64 units x 64 k, 4 x 4
-// of them a thread; the tokens in order, added in groups of 32, 32 groups of 1024:
-// at most 32 + 32 + T / 1024 roundings of a sum.  On CUDA cores: at 4096 tokens, 2048 ->
-// 7168, the backward takes 0.84 ms with no far token, 1.14 with one, 1.41 with 64 and
-// 19 with all but one.
+// Most calls have none and the kernel ends at once.  Tiles of 128 units x 128 k, 8 x 8
+// of them a thread; the tokens in order, added in groups of 32, 32 groups of 1024, the
+// 1024s to dW: 32 + 32 + T / 1024 roundings of a sum at most.  The list of the far tokens
+// stays in shared memory for all of a block's tiles unless it is longer than KEEP.  On
+// CUDA cores: at 4096 tokens, 2048 -> 7168, the backward takes 0.85 ms with no far
+// token, 1.02 with one, 1.15 with 64 and 10.3 with all but one.
 struct FfnFar {
     const unsigned* far;
     const unsigned* row_max;
@@ -894,97 +897,142 @@ struct FfnFar {
     int T, K, F, Fp, ternary;
 };
 __global__ void __launch_bounds__(256) ffn_far_kernel(const FfnFar q) {
-    constexpr int TILE = 64, GROUP = 32;
-    __shared__ int list[256];
-    __shared__ int count[8];
-    __shared__ float sv[GROUP][TILE];
-    __shared__ float sx[GROUP][TILE];
+    constexpr int TILE = 128, GROUP = 32, CHUNK = 1024, KEEP = 2048;
+    __shared__ int list[KEEP + CHUNK];
+    __shared__ int warp_count[8];
+    __shared__ __align__(16) float sv[GROUP][TILE];
+    __shared__ __align__(16) float sx[GROUP][TILE];
     asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (*q.far == 0u) return;
     const int top = row_exponent(*q.all_max), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    // lists the far tokens from t0 on, in order, until it holds more than KEEP; moves t0 on
+    auto fill = [&](int& t0) {
+        int n = 0;
+        while (t0 < q.T && n <= KEEP) {
+            const int t = t0 + 4 * tid;
+            unsigned mine = 0;
+            if (t < q.T) {  // row_max ends on a 16-byte unit
+                const uint4 b = __ldg(reinterpret_cast<const uint4*>(q.row_max + t));
+                const unsigned bits[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) mine |= t + i < q.T && token_far(bits[i], top) ? 1u << i : 0u;
+            }
+            const int c = __popc(mine);
+            int upto = c;  // of the warp's threads up to this one
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int o = __shfl_up_sync(0xFFFFFFFFu, upto, off);
+                if (lane >= off) upto += o;
+            }
+            __syncthreads();  // the last counts, and the last list, have been read
+            if (lane == 31) warp_count[warp] = upto;
+            __syncthreads();
+            int at = n + upto - c;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) {
+                at += w < warp ? warp_count[w] : 0;
+                n += warp_count[w];
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (mine >> i & 1u) list[at++] = t + i;
+            t0 += CHUNK;
+        }
+        __syncthreads();
+        return n;
+    };
+    int t0 = 0;
+    int n = fill(t0);
+    const bool whole = t0 >= q.T;
     const int ft = (q.F + TILE - 1) / TILE, kt = (q.K + TILE - 1) / TILE;
     const long long per_matrix = static_cast<long long>(ft) * kt;
     const long long tiles = per_matrix * ((q.dwg != nullptr) + (q.dwu != nullptr));
-    const int f4 = tid / 16 * 4, k4 = tid % 16 * 4;  // this thread's corner of the tile
+    const int fc = tid / 16 * 4, kc = tid % 16 * 4;  // this thread's units fc .. + 3 and 64 + fc .. + 3, k likewise
     for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
         const bool up = !q.dwg || tile >= per_matrix;
         const long long at = tile % per_matrix;
         const int f0 = static_cast<int>(at / kt) * TILE, k0 = static_cast<int>(at % kt) * TILE;
-        float sum[4][4], mid[4][4];
-#pragma unroll
-        for (int a = 0; a < 4; ++a)
-#pragma unroll
-            for (int b = 0; b < 4; ++b) sum[a][b] = mid[a][b] = 0.f;
-        int groups = 0;
-        for (int t0 = 0; t0 < q.T; t0 += 256) {
-            // the far ones of 256 tokens, in order
-            const bool mine = t0 + tid < q.T && token_far(__ldg(q.row_max + t0 + tid), top);
-            const unsigned votes = __ballot_sync(0xFFFFFFFFu, mine);
-            __syncthreads();  // the list has been read
-            if (lane == 0) count[warp] = __popc(votes);
-            __syncthreads();
-            int before = 0, n = 0;
-#pragma unroll
-            for (int w = 0; w < 8; ++w) {
-                before += w < warp ? count[w] : 0;
-                n += count[w];
-            }
-            if (mine) list[before + __popc(votes & ((1u << lane) - 1u))] = t0 + tid;
-            for (int g0 = 0; g0 < n; g0 += GROUP) {
-                const int m = n - g0 < GROUP ? n - g0 : GROUP;
-                __syncthreads();  // the list is complete; the previous group has been read
-                for (int i = tid; i < m * TILE; i += 256) {
-                    const int j = i / TILE, c = i % TILE, f = f0 + c, k = k0 + c;
-                    const long long t = list[g0 + j];
-                    sv[j][c] = f < q.F ? __ldg(q.v + t * 2 * q.Fp + (up ? q.Fp : 0) + f) : 0.f;
-                    // columns 0, 2, 4, 6, 1, 3, 5, 7 of each 8: the pairing order
-                    const int at8 = (k & 1) * 4 + ((k & 7) >> 1);
-                    sx[j][c] = k < q.K ? static_cast<float>(q.xq[t * q.K + (k & ~7) + at8]) : 0.f;
-                }
-                __syncthreads();
-                float part[4][4];
-#pragma unroll
-                for (int a = 0; a < 4; ++a)
-#pragma unroll
-                    for (int b = 0; b < 4; ++b) part[a][b] = 0.f;
-                for (int j = 0; j < m; ++j) {
-                    const float4 v = *reinterpret_cast<const float4*>(&sv[j][f4]);
-                    const float4 x = *reinterpret_cast<const float4*>(&sx[j][k4]);
-                    const float va[4] = {v.x, v.y, v.z, v.w}, xa[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                    for (int a = 0; a < 4; ++a)
-#pragma unroll
-                        for (int b = 0; b < 4; ++b) part[a][b] = fmaf(va[a], xa[b], part[a][b]);
-                }
-                const bool full = ++groups == 32;
-#pragma unroll
-                for (int a = 0; a < 4; ++a)
-#pragma unroll
-                    for (int b = 0; b < 4; ++b) {
-                        mid[a][b] += part[a][b];
-                        if (full) {
-                            sum[a][b] += mid[a][b];
-                            mid[a][b] = 0.f;
-                        }
-                    }
-                if (full) groups = 0;
-            }
-        }
+        const float* const vp = q.v + (up ? q.Fp : 0) + f0;
         float* const out = up ? q.dwu : q.dwg;
         const float* const scale = up ? q.scale_u : q.scale_g;
+        float sum[8][8];
 #pragma unroll
-        for (int a = 0; a < 4; ++a) {
-            const int f = f0 + f4 + a;
-            if (f >= q.F) break;
-            const float s = q.ternary ? 1.0f : __frcp_rn(__ldg(scale + f));
+        for (int a = 0; a < 8; ++a)
 #pragma unroll
-            for (int b = 0; b < 4; ++b)
-                if (k0 + k4 + b < q.K) {
-                    float* const d = out + static_cast<size_t>(f) * q.K + k0 + k4 + b;
-                    *d += (sum[a][b] + mid[a][b]) * s;
+            for (int b = 0; b < 8; ++b) sum[a][b] = 0.f;
+        auto flush = [&] {
+#pragma unroll
+            for (int a = 0; a < 8; ++a) {
+                const int f = f0 + fc + (a & 3) + (a >> 2) * 64;
+                if (f >= q.F) continue;
+                const float s = q.ternary ? 1.0f : __frcp_rn(__ldg(scale + f));
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int k = k0 + kc + h * 64;
+                    if (k >= q.K) continue;  // K % 16 == 0: four columns at once
+                    float4* const d = reinterpret_cast<float4*>(out + static_cast<size_t>(f) * q.K + k);
+                    float4 o = *d;
+                    o.x += sum[a][4 * h] * s;
+                    o.y += sum[a][4 * h + 1] * s;
+                    o.z += sum[a][4 * h + 2] * s;
+                    o.w += sum[a][4 * h + 3] * s;
+                    *d = o;
                 }
-        }
+#pragma unroll
+                for (int b = 0; b < 8; ++b) sum[a][b] = 0.f;
+            }
+        };
+        int groups = 0;
+        if (!whole) t0 = 0;
+        do {
+            if (!whole) n = fill(t0);
+            for (int g0 = 0; g0 < n; g0 += GROUP) {
+                const int m = n - g0 < GROUP ? n - g0 : GROUP;
+                __syncthreads();  // the previous group has been read
+                for (int i = tid; i < m * (TILE / 4); i += 256) {  // v's units past F, up to Fp, are zeros
+                    const int j = i / (TILE / 4), c = i % (TILE / 4) * 4;
+                    *reinterpret_cast<float4*>(&sv[j][c]) =
+                        __ldg(reinterpret_cast<const float4*>(vp + static_cast<long long>(list[g0 + j]) * 2 * q.Fp + c));
+                }
+                if (const int j = tid / 8, c = tid % 8 * 16; j < m) {
+                    uint4 u = make_uint4(0u, 0u, 0u, 0u);
+                    if (k0 + c < q.K)
+                        u = __ldg(reinterpret_cast<const uint4*>(q.xq + static_cast<long long>(list[g0 + j]) * q.K + k0 + c));
+                    const uint32_t w[4] = {u.x, u.y, u.z, u.w};  // even 0-6, odd 1-7, even 8-14, odd 9-15
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        sx[j][c + i] = static_cast<float>(static_cast<int8_t>(w[(i >> 3) * 2 + (i & 1)] >> (8 * ((i & 7) >> 1))));
+                }
+                __syncthreads();
+                float part[8][8];
+#pragma unroll
+                for (int a = 0; a < 8; ++a)
+#pragma unroll
+                    for (int b = 0; b < 8; ++b) part[a][b] = 0.f;
+                for (int j = 0; j < m; ++j) {
+                    float va[8], xa[8];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        *reinterpret_cast<float4*>(va + 4 * h) = *reinterpret_cast<const float4*>(&sv[j][fc + 64 * h]);
+                        *reinterpret_cast<float4*>(xa + 4 * h) = *reinterpret_cast<const float4*>(&sx[j][kc + 64 * h]);
+                    }
+#pragma unroll
+                    for (int a = 0; a < 8; ++a)
+#pragma unroll
+                        for (int b = 0; b < 8; ++b) part[a][b] = fmaf(va[a], xa[b], part[a][b]);
+                }
+#pragma unroll
+                for (int a = 0; a < 8; ++a)
+#pragma unroll
+                    for (int b = 0; b < 8; ++b) sum[a][b] += part[a][b];
+                if (++groups == 32) {
+                    flush();
+                    groups = 0;
+                }
+            }
+        } while (!whole && t0 < q.T);
+        if (groups) flush();
     }
 }
 
@@ -1373,7 +1421,7 @@ cudaError_t launch_ffn_backward(const float* dh, const uint16_t* x, long long T,
     if (e == cudaSuccess && dw_splits > 1 && dwu) e = join(dw_sums + sp.Fp * K, dw_splits, 2 * sp.Fp, F, dwu);
     if (e == cudaSuccess && need_dw) {
         const FfnFar q_far{far, row_max, all_max, v, xq, scale_g, scale_u, dwg, dwu, Ti, Ki, Fi, Fp, ternary};
-        const long long tiles = ((F + 63) / 64) * ((K + 63) / 64) * ((dwg != nullptr) + (dwu != nullptr)), most = 2ll * num_sms;
+        const long long tiles = ((F + 127) / 128) * ((K + 127) / 128) * ((dwg != nullptr) + (dwu != nullptr)), most = num_sms;
         e = pdl_launch(ffn_far_kernel, dim3(static_cast<unsigned>(tiles < most ? tiles : most)), dim3(256), 0, st, q_far);
     }
     return e;

@@ -33,16 +33,17 @@ _check = ce._check  # an output that holds NaN does not pass
 # ---------------------------------------------------------------- the feed-forward block
 @pytest.mark.parametrize("T,K,F", [(5, 80, 40), (40, 256, 130), (300, 272, 260), (1500, 896, 150), (3001, 64, 100)])
 @pytest.mark.parametrize("act,ternary", [("silu", False), ("relu2", True)])
-def test_gradients_of_tokens_far_apart(sbl, T, K, F, act, ternary):
+@pytest.mark.parametrize("powers", [(0, 20, 30, 33, 34, 41, 50, 75), (0, 12, 16, 19, 20, 21, 22), (0, 22, 24, 26, 28, 30, 31)])
+def test_gradients_of_tokens_far_apart(sbl, T, K, F, act, ternary, powers):
     """Tokens whose gradients differ by up to 2^-75, and hidden units that only the
     small ones reach: the floor of each token is 2^-38 of its own largest v."""
     c = Case(sbl, T, K, F, nm=[(2, 4), (3, 4), (6, 8), (4, 8)][T % 4], act=act, seed=T + F)
     g = torch.Generator().manual_seed(T)
-    power = torch.tensor([0, 20, 30, 33, 34, 41, 50, 75])[torch.randint(0, 8, (T, 1), generator=g)]
-    power[0], power[-1] = 0, 50
+    power = torch.tensor(powers)[torch.randint(0, len(powers), (T, 1), generator=g)]
+    power[0], power[-1] = powers[0], powers[-2]
     dh = torch.randn(T, F, generator=g) * 2.0 ** -power.double()
-    dh[:, F // 2:] *= power >= 33
-    dh[:, F - 7:] *= power >= 50
+    dh[:, F // 2:] *= power >= powers[len(powers) // 2]
+    dh[:, F - 7:] *= power >= powers[-2]
     dh = dh.float()
     refs = c.grads(dh, ternary)
     got = sbl.sbl_ffn_gated_backward(dh.cuda(), c.x, c.gate, c.up, act=act, dw_ternary=ternary)
@@ -55,6 +56,32 @@ def test_gradients_of_tokens_far_apart(sbl, T, K, F, act, ternary):
         for o, v, n in zip(one, got, need):
             assert (o is not None) == n and (o is None or torch.equal(o, v))
     assert sbl.sbl_device_status() == 0
+
+
+@pytest.mark.parametrize("d", [0, 15, 20, 22, 23, 26, 29, 30, 31, 32, 40])
+def test_gradients_of_one_small_token_beside_others(sbl, d):
+    """A column of dW whose terms are one token's, 2^-d of the largest token (which has
+    x = 0 there), and smaller ones of tokens in between: each sum within 90 u of its
+    terms.  One weight a row, at column 0 with x = 127, makes s = 1, g = u = 127 scale
+    and dup = sum dh g^2 x (squared ReLU)."""
+    T, K, F = 16, 16, 128
+    packed = torch.zeros(F, K // 4, dtype=torch.uint8)
+    packed[:, 0] = 1
+    w = sbl.PreparedWeights(packed.cuda(), torch.full((F,), 1 / 128, device="cuda"), 2, 4, K)
+    g = torch.Generator().manual_seed(d)
+    x, dh = torch.zeros(T, K), torch.zeros(T, F)
+    x[:, 0] = 127
+    dh[0] = 1.9
+    x[1, 1:] = torch.randint(1, 3, (K - 1,), generator=g).float()
+    dh[1] = (1 + torch.rand(F, generator=g)) * 2.0 ** -d
+    x[2:, 1:] = torch.randint(-9, 10, (T - 2, K - 1), generator=g).float()
+    dh[2:] = torch.randn(T - 2, F, generator=g) * 2.0 ** -(d + 8)
+    dh[2:, 0] = 2.0 ** -max(d - 9, 0)   # what scales them: their largest
+    terms = dh.double() * (127 / 128) ** 2
+    _, _, dup = sbl.sbl_ffn_gated_backward(dh.cuda(), x.bfloat16().cuda(), w, w, act="relu2")
+    floor = 2.0 ** -38 * 2 * terms.abs().amax(1, keepdim=True)    # the gate's v is twice the up's
+    bound = 90 * U * (terms.abs().T @ x.double().abs()) + (floor * x.double().abs()).sum(0)
+    _check("dup", dup, terms.T @ x.double(), bound)
 
 
 @pytest.mark.parametrize("T", [1, 12, 40])
