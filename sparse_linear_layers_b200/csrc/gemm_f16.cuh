@@ -30,7 +30,10 @@
 // into segments of SEGMENT k-blocks; each segment starts from zero and the
 // epilogue threads add it, rounding to nearest, to sums in registers.
 // Costs one 128-column TMEM read and 128 additions per thread and segment,
-// hidden behind the next segment's MMAs.
+// hidden behind the next segment's MMAs.  The sums beside a slice being read take
+// all 168 registers: 64 to 88 bytes a thread spill in the epilogue warps, 244 in the
+// kernel that holds both of the feed-forward block's epilogues (0.57 ms all the same,
+// 0.60 as two launches).
 //
 // Warps: 8 MH epilogue (warp w: TMEM lanes 32 (w % 4) .. + 31, columns
 // 128 (w / 4 % 2) .. + 127 of buffer w / 8), one TMA producer, one for TMEM

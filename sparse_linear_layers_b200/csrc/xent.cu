@@ -30,8 +30,8 @@
 // Bound by what feeds the tensor cores (gemm_f16.cuh) and, over longer runs, by
 // the power limit: 2 T V D operations forward, 6 T V D backward (a third of them
 // the second time z is computed, the price of not keeping it).  At 8192 x
-// 128000 x 896 the four products take 6.5 ms, 1160 TFLOP/s (a library bf16 product
-// of 8192^3 sustains 1395); at 4096 x 32000 x 2048 1.75 ms, 1230 TFLOP/s.  The epilogues
+// 128000 x 896 the four products take 6.6 ms, 1140 TFLOP/s (a library bf16 product
+// of 8192^3 sustains 1395); at 4096 x 32000 x 2048 1.84 ms, 1170 TFLOP/s.  The epilogues
 // spend about three instructions per logit on pairs of values; an index into
 // a row's registers anywhere in them would put the row into local memory.
 #include <cuda.h>
@@ -49,7 +49,7 @@ namespace {
 // one piece, D = 2048 left lse 1.5e-6 off (the tensor cores' rounding towards
 // zero), three times what a sum rounded to nearest leaves.
 constexpr int kLogitSegment = 16;
-// Up to 256 tokens, whose time is W's way from memory, segments of 2: over few
+// Up to 256 tokens, whose MMAs leave the tensor pipe mostly idle, segments of 2: over few
 // losses, some of them small, the sum's error shows (a token: 1e-6 of its loss).
 constexpr int kFewSegment = 2;
 // The backward's logits are summed in the same segments, so that they are the ones
@@ -200,8 +200,9 @@ struct GradTile {
 // Up to kFewTokens the logits' tiles are turned: 256 words x 64 or 128 tokens
 // instead of 256 tokens, most of them past the end, x 256 words.  A thread then
 // holds one word's logits of 32 tokens, and a warp's 32 words are a part of the row.
-// 64 x 128000 x 896: 53 us forward, 66% of the copy bandwidth (70 us not turned), 49 us
-// for G (54); one token x 15710 x 1440: 15.5 us (19), of which 5 are the launch.
+// 64 x 128000 x 896: 53 us forward, 66% of the copy bandwidth (70 us not turned), 58 us
+// for G (49 with the logits in one sum).  Neither memory nor L2 is at its limit there (52%
+// of DRAM's peak, 36 bytes/ns to an SM); what sets the pace is not known.  One token x 15710 x 1440: 15.5 us (19), of which 5 are the launch.
 constexpr int kFewTokens = 128;
 
 // Reduces 32 values over the 32 lanes; lane l gets value l's result (norm.cu's
@@ -504,8 +505,8 @@ long long piece_words(long long T, long long V) {
 // Up to kFewTokens G goes as two bf16 parts: the rounding of a token's
 // one large entry, its target's, moves a whole row of dX and dW together, and
 // over a few tokens such errors do not average out (1 to 8 tokens: up to 1.75
-// times the error that rounding the results alone leaves).  These sizes are bound by
-// reading W and writing dW, which hides the second part's MMAs.
+// times the error that rounding the results alone leaves).  The second part's MMAs have
+// room: the tensor pipe is 48% busy with both (64 x 128000 x 896).
 bool g_parts(long long T) { return T <= kFewTokens; }
 
 // With G in two parts they lie in the two CTAs' rows of one A (GemmShape::stack),

@@ -207,7 +207,8 @@ class SparseBitFeedForward(torch.nn.Module):
     ``gate`` and ``up`` are fp32 latent weights [hidden_features, in_features],
     ``down`` a SparseBitLinear back to in_features (both sizes multiples of 16);
     ``act`` is "silu" or "relu2" (the squared ReLU).  x of any leading shape is cast to bf16; the output is
-    fp32.  ``dw_ternary`` and ``check_finite`` as in SparseBitLinear."""
+    fp32.  h enters ``down`` in bf16, and the gradients of h and of x are rounded to bf16 on
+    their way.  ``dw_ternary`` and ``check_finite`` as in SparseBitLinear."""
 
     def __init__(self, in_features: int, hidden_features: int, n: int = 2, m: int = 4, act: str = "silu",
                  dw_ternary: bool = False, device=None, check_finite: bool = True):
@@ -265,7 +266,7 @@ class LinearCrossEntropy(torch.nn.Module):
     states [..., in_features] against targets [...] of int64 words.
 
     ``weight`` is fp32 [vocab, in_features], cast to bf16 (as x is) for the
-    products.  ``reduction``: "mean" over the tokens whose target is not
+    products; its gradient is rounded to bf16 once.  ``reduction``: "mean" over the tokens whose target is not
     ``ignore_index``, "sum", or "none" (per token, 0 for ignored ones).
 
     With ``check_targets`` (the default) a forward whose targets are neither words nor
