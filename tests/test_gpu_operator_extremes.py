@@ -31,7 +31,9 @@ _check = ce._check  # an output that holds NaN does not pass
 
 
 # ---------------------------------------------------------------- the feed-forward block
-@pytest.mark.parametrize("T,K,F", [(5, 80, 40), (40, 256, 130), (300, 272, 260), (1500, 896, 150), (3001, 64, 100)])
+@pytest.mark.parametrize("T,K,F", [(5, 80, 40), (40, 256, 130), (300, 272, 260), (1500, 896, 150), (3001, 64, 100),
+                                   # more small tokens than the kernel's list of them holds at once
+                                   (7003, 144, 40)])
 @pytest.mark.parametrize("act,ternary", [("silu", False), ("relu2", True)])
 @pytest.mark.parametrize("powers", [(0, 20, 30, 33, 34, 41, 50, 75), (0, 12, 16, 19, 20, 21, 22), (0, 22, 24, 26, 28, 30, 31)])
 def test_gradients_of_tokens_far_apart(sbl, T, K, F, act, ternary, powers):
