@@ -137,6 +137,11 @@ sbl_status device_info(DeviceInfo** out) {
     return SBL_OK;
 }
 
+// Whether two ranges of device memory share a byte (NULL: an output not wanted).
+inline bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && x < y + b_bytes && y < x + a_bytes;
+}
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 // 2:4, 3:4 and 6:8 (the patterns of the guide and the halo card) and 4:8 (the
@@ -252,7 +257,8 @@ sbl_status sbl_norm(const void* x, int dtype, int64_t T, int64_t K, int kind, co
     if (sbl_status s = check_norm(dtype, T, K, kind)) return s;
     if (!(eps >= 0.0f) || !(eps < 3.0e38f)) return SBL_ERR_INVALID_ARG;
     if (T == 0) return SBL_OK;
-    if (!x || !weight || !y || x == y) return SBL_ERR_INVALID_ARG;
+    const size_t bytes = static_cast<size_t>(T) * K * (dtype == SBL_BF16 ? 2 : 4);
+    if (!x || !weight || !y || overlap(x, bytes, y, bytes)) return SBL_ERR_INVALID_ARG;
     for (const void* p : {x, static_cast<const void*>(weight), static_cast<const void*>(bias), static_cast<const void*>(y)})
         if (!aligned(p, 16)) return SBL_ERR_INVALID_ARG;
     if (!aligned(mean, 4) || !aligned(rstd, 4)) return SBL_ERR_INVALID_ARG;
@@ -282,7 +288,9 @@ sbl_status sbl_norm_backward(const void* dy, const void* x, int dtype, int64_t T
         return from_cuda(e);
     }
     if (!dx && !dweight && !dbias) return SBL_ERR_INVALID_ARG;
-    if (!dy || !x || !weight || !rstd || (kind == SBL_NORM_LAYER && !mean) || dx == x || dx == dy)
+    const size_t bytes = static_cast<size_t>(T) * K * (dtype == SBL_BF16 ? 2 : 4);
+    if (!dy || !x || !weight || !rstd || (kind == SBL_NORM_LAYER && !mean) || overlap(dx, bytes, x, bytes) ||
+        overlap(dx, bytes, dy, bytes))
         return SBL_ERR_INVALID_ARG;
     for (const void* p : {dy, x, static_cast<const void*>(weight), static_cast<const void*>(dx)})
         if (!aligned(p, 16)) return SBL_ERR_INVALID_ARG;
@@ -396,6 +404,8 @@ sbl_status sbl_ffn_gated(const uint16_t* x_bf16, int64_t T, int64_t K, const uin
         if (!p || !aligned(p, 16)) return SBL_ERR_INVALID_ARG;
     const size_t need = sbl::ffn_workspace_bytes(T, K, F);
     if (need && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return SBL_ERR_WORKSPACE;
+    if (overlap(h, static_cast<size_t>(T) * F * (h_dtype == SBL_BF16 ? 2 : 4), x_bf16, static_cast<size_t>(T) * K * 2))
+        return SBL_ERR_INVALID_ARG;
     DeviceInfo* d;
     if (sbl_status s = device_info(&d)) return s;
     return from_cuda(sbl::launch_ffn(x_bf16, T, K, packed_gate, scale_gate, packed_up, scale_up, F, act, h,
@@ -490,6 +500,10 @@ sbl_status sbl_linear_cross_entropy_backward(const float* dloss, const uint16_t*
     if (!workspace || !aligned(workspace, 256) ||
         workspace_bytes < sbl::xent_backward_workspace_bytes(T, D, V, dx != nullptr))
         return SBL_ERR_WORKSPACE;
+    const size_t x_bytes = static_cast<size_t>(T) * D * 2, w_bytes = static_cast<size_t>(V) * D * 2;
+    if (overlap(dx, x_bytes, x_bf16, x_bytes) || overlap(dx, x_bytes, w_bf16, w_bytes) ||
+        overlap(dw, w_bytes, x_bf16, x_bytes) || overlap(dw, w_bytes, w_bf16, w_bytes))
+        return SBL_ERR_INVALID_ARG;
     DeviceInfo* d;
     if (sbl_status s = device_info(&d)) return s;
     return from_cuda(sbl::launch_xent_backward(dloss, x_bf16, T, D, w_bf16, V,

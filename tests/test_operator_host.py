@@ -84,3 +84,30 @@ def test_an_earlier_calls_status_is_not_blamed_on_a_module(monkeypatch):
     monkeypatch.setattr(api, "sbl_device_status", lambda: _lib.SBL_ERR_NONFINITE)
     with pytest.raises(FloatingPointError, match="SparseBitLinear"):
         train._stop_on_nonfinite("SparseBitLinear")
+
+
+def test_outputs_over_inputs_are_refused_on_the_host():
+    """One row further on, or the same memory: some kernels read their inputs until
+    their last output is written."""
+    from sparse_linear_layers_b200._lib import lib
+    x, far, big = 1 << 20, 1 << 30, 1 << 40
+    norm = lambda y, dt=1: lib.sbl_norm(x, dt, 8, 64, 0, far, None, 1e-5, y, None, None, None)
+    for y in (x, x + 128, x - 128, x + 7 * 128):
+        assert norm(y) == 1 and norm(y, 0) == 1
+    back = lambda dx, dy=far: lib.sbl_norm_backward(dy, x, 1, 8, 64, 0, far, None, far, dx, None, None, None, 0, None)
+    for dx in (x + 128, x - 7 * 128, far + 256, far - 128):
+        assert back(dx) == 1
+    ffn = lambda h, T, F, dt: lib.sbl_ffn_gated(x, T, 64, far, far, far, far, F, 2, 4, 0, h, dt, far, big, None)
+    for T in (8, 40):
+        assert ffn(x, T, 64, 1) == 1 and ffn(x + 128, T, 16, 0) == 1 and ffn(x - 16, T, 1, 0) == 1
+    ce = lambda dx, dw: lib.sbl_linear_cross_entropy_backward(far, x, 8, 64, 2 * x, 100, far, -100, far, dx, dw, far, big, None)
+    for p in (x, x + 128, 2 * x, 2 * x + 99 * 128, 2 * x - 128):
+        assert ce(p, None) == 1 and ce(None, p) == 1
+    if not has_device():    # beside its input: nothing is refused before the missing device
+        assert norm(x + 8 * 128) == back(x - 8 * 128) == ffn(x + 8 * 128, 8, 64, 1) == ffn(x - 8 * 4, 8, 1, 0) == 4
+        assert ce(x + 8 * 128, 2 * x + 100 * 128) == 4
+
+
+def has_device():
+    import torch
+    return torch.cuda.is_available()
