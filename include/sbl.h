@@ -330,7 +330,7 @@ enum { SBL_ACT_SILU = 0, SBL_ACT_RELU2 = 1 };
  *             N:M pattern (n, m); scales positive, as sbl_prepare_weights
  *             writes them.
  *   h         [T, F] (output), fp32 (SBL_F32) or bf16 (SBL_BF16, rounded once); must
- *             not overlap x.
+ *             not overlap x for up to 16 tokens.
  *   workspace sbl_ffn_gated_workspace_bytes(T, K, F) bytes, 256-byte aligned;
  *             0 bytes (NULL allowed) for up to 16 tokens.  Calls that share it
  *             must be ordered on one stream.
@@ -405,7 +405,8 @@ sbl_status sbl_linear_cross_entropy(const uint16_t* x_bf16, int64_t T, int64_t D
  *
  *   dloss     fp32 [T] (4-byte aligned), finite; lse as sbl_linear_cross_entropy wrote it.
  *   dx, dw    bf16 [T, D] and [V, D] (outputs), each may be NULL, not both unless
- *             T == 0, nor overlap x or W; overwritten (dw with zeros for T == 0).
+ *             T == 0; overwritten (dw with zeros for T == 0).  dw must not overlap x
+ *             or W.
  *   workspace sbl_linear_cross_entropy_backward_workspace_bytes(T, D, V, dx != NULL)
  *             bytes, 256-byte aligned (at most 512 MB for the gradient of one
  *             piece of the logits, more only for T > 2^17, and fp32 sums of dx).

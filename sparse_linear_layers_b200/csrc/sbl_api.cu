@@ -404,7 +404,8 @@ sbl_status sbl_ffn_gated(const uint16_t* x_bf16, int64_t T, int64_t K, const uin
         if (!p || !aligned(p, 16)) return SBL_ERR_INVALID_ARG;
     const size_t need = sbl::ffn_workspace_bytes(T, K, F);
     if (need && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return SBL_ERR_WORKSPACE;
-    if (overlap(h, static_cast<size_t>(T) * F * (h_dtype == SBL_BF16 ? 2 : 4), x_bf16, static_cast<size_t>(T) * K * 2))
+    // a few tokens, without a workspace: their kernel reads x until its last output is written
+    if (!need && overlap(h, static_cast<size_t>(T) * F * (h_dtype == SBL_BF16 ? 2 : 4), x_bf16, static_cast<size_t>(T) * K * 2))
         return SBL_ERR_INVALID_ARG;
     DeviceInfo* d;
     if (sbl_status s = device_info(&d)) return s;
@@ -501,9 +502,8 @@ sbl_status sbl_linear_cross_entropy_backward(const float* dloss, const uint16_t*
         workspace_bytes < sbl::xent_backward_workspace_bytes(T, D, V, dx != nullptr))
         return SBL_ERR_WORKSPACE;
     const size_t x_bytes = static_cast<size_t>(T) * D * 2, w_bytes = static_cast<size_t>(V) * D * 2;
-    if (overlap(dx, x_bytes, x_bf16, x_bytes) || overlap(dx, x_bytes, w_bf16, w_bytes) ||
-        overlap(dw, w_bytes, x_bf16, x_bytes) || overlap(dw, w_bytes, w_bf16, w_bytes))
-        return SBL_ERR_INVALID_ARG;
+    // dw is written piece by piece (dx after all of them)
+    if (overlap(dw, w_bytes, x_bf16, x_bytes) || overlap(dw, w_bytes, w_bf16, w_bytes)) return SBL_ERR_INVALID_ARG;
     DeviceInfo* d;
     if (sbl_status s = device_info(&d)) return s;
     return from_cuda(sbl::launch_xent_backward(dloss, x_bf16, T, D, w_bf16, V,

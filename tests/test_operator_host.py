@@ -98,11 +98,11 @@ def test_outputs_over_inputs_are_refused_on_the_host():
     for dx in (x + 128, x - 7 * 128, far + 256, far - 128):
         assert back(dx) == 1
     ffn = lambda h, T, F, dt: lib.sbl_ffn_gated(x, T, 64, far, far, far, far, F, 2, 4, 0, h, dt, far, big, None)
-    for T in (8, 40):
-        assert ffn(x, T, 64, 1) == 1 and ffn(x + 128, T, 16, 0) == 1 and ffn(x - 16, T, 1, 0) == 1
+    for T in (1, 8, 16):
+        assert ffn(x, T, 64, 1) == 1 and ffn(x + 128 * T - 16, T, 16, 0) == 1 and ffn(x - 16, T, 5, 0) == 1
     ce = lambda dx, dw: lib.sbl_linear_cross_entropy_backward(far, x, 8, 64, 2 * x, 100, far, -100, far, dx, dw, far, big, None)
     for p in (x, x + 128, 2 * x, 2 * x + 99 * 128, 2 * x - 128):
-        assert ce(p, None) == 1 and ce(None, p) == 1
+        assert ce(None, p) == 1 and ce(far, p) == 1
     if not has_device():    # beside its input: nothing is refused before the missing device
         assert norm(x + 8 * 128) == back(x - 8 * 128) == ffn(x + 8 * 128, 8, 64, 1) == ffn(x - 8 * 4, 8, 1, 0) == 4
         assert ce(x + 8 * 128, 2 * x + 100 * 128) == 4
