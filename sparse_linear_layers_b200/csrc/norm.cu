@@ -499,7 +499,7 @@ __global__ void __launch_bounds__(nrm::STREAM_THREADS, 1)
         // x * rstd - mean * rstd would keep the rounding of mean * rstd, and its one
         // instruction less gains nothing (16384 x 4864 bf16: the same 92 us)
         float2 scale[R], less[R];
-        auto xhat = [&](int r, float2 f) { return mul2(LAYER ? add2(f, less[r]) : f, scale[r]); };
+        auto xhat = [](float2 f, float2 less_r, float2 scale_r) { return mul2(LAYER ? add2(f, less_r) : f, scale_r); };
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             scale[r] = both(rstd[r]);
@@ -512,7 +512,7 @@ __global__ void __launch_bounds__(nrm::STREAM_THREADS, 1)
                     each(r, c, f, g);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float2 xh = xhat(r, f[i]);
+                        const float2 xh = xhat(f[i], less[r], scale[r]);
                         const float2 q = mul2(g[i], wv[c][i]);
                         s1 = fma2(q, xh, s1);
                         if (LAYER) s0 = add2(s0, q);
@@ -538,7 +538,7 @@ __global__ void __launch_bounds__(nrm::STREAM_THREADS, 1)
                         each(r, c, f, g);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const float2 xh = xhat(r, f[i]);
+                            const float2 xh = xhat(f[i], less[r], scale[r]);
                             const float2 q = mul2(g[i], wv[c][i]);
                             f[i] = fma2(xh, c1, LAYER ? fma2(q, scale[r], c0) : mul2(q, scale[r]));
                         }
